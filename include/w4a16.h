@@ -506,6 +506,147 @@ int w4a16_moe_gemm_combine_noalloc(const uint16_t* A, const int32_t* Wq, const u
                                    int32_t E, int64_t N, int64_t K, int32_t B,
                                    int32_t tiled, void* stream);
 
+/*
+ * ---------------------------------------------------------- W8A8 (FP8) ----
+ * 8-bit floating-point operands with a power-of-two scale per block of 128
+ * (the W8A8-FP8 side of the rollout comparison of [RL]).
+ *  - Codes: e4m3 (OCP; largest value 448, 0x7F / 0xFF NaN), one byte each,
+ *    [R, K] row-major, K % 16 == 0.
+ *  - Scales: e8m0 bytes b = 2^(b - 127) (255 = NaN).  One per 128
+ *    consecutive k of an activation row: SX [M, C]; one per 128 x 128 block
+ *    of a weight: SW [ceil(N/128), C].  C = w8_scale_cols(K): a row of scales
+ *    is whole dwords; bytes past ceil(K/128) are padding (written as 127,
+ *    never read).  The last block of a row or column may be partial.
+ *  - Limits: K <= 2^22, rows <= 2^31 - 1, 2^40 elements per matrix, 2^32
+ *    threads per launch; beyond: W4_ERR_UNSUPPORTED.
+ *
+ * w8_scale_cols -- 4 * ceil(K / 512); -1 if K < 0.
+ */
+int64_t w8_scale_cols(int64_t K);
+
+/*
+ * w8_quantize_rows -- activations bf16 X [M, K] -> X8 [M, K], SX [M, C].
+ *   for each row and block of 128 consecutive k, amax = max |x|:
+ *     e    = the smallest integer >= -127 with amax <= 448 * 2^e; 0 if amax = 0
+ *     SX   = e + 127
+ *     X8   = e4m3_rne( x * 2^-e )            (the product is exact)
+ * A block that holds Inf or NaN gets scale 255 and codes 0x7F (NaN), which
+ * every product over it returns.  X, X8 16-byte aligned, SX 4-byte aligned.
+ * M or K == 0 is a no-op.  Bit-exact with the definition.
+ */
+int w8_quantize_rows(const uint16_t* X, int64_t M, int64_t K, uint8_t* X8, uint8_t* SX,
+                     void* stream);
+
+/*
+ * w8_quantize_blocks -- weights bf16 W [N, K] -> W8 [N, K], SW, with one
+ * exponent per 128 x 128 block by the same rule; and, unless WT8 is NULL, the
+ * transposed codes WT8 [K, N] with ST [ceil(K/128), w8_scale_cols(N)]: the
+ * same numbers, since a square block transposes onto itself (the input
+ * gradient dX = dY W' is then w8a8_gemm on WT8).  WT8 needs N % 16 == 0
+ * (W4_ERR_SHAPE); WT8 and ST come together or not at all (W4_ERR_NULL).
+ * W, W8, WT8 16-byte aligned, SW, ST 4-byte aligned.  N or K == 0 is a no-op.
+ */
+int w8_quantize_blocks(const uint16_t* W, int64_t N, int64_t K, uint8_t* W8, uint8_t* SW,
+                       uint8_t* WT8, uint8_t* ST, void* stream);
+
+/*
+ * w8_silu_mul_quantize -- SwiGLU and quantization between the expert
+ * projections, in one pass:
+ *   a[r, i] = silu(H1[r, i]) * H1[r, I + i]      (fp32, not rounded to bf16)
+ *   A8, SA  = the rows of a, quantized as w8_quantize_rows does
+ * H1 bf16 [R, 2I], A8 [R, I], both 16-byte aligned; SA [R, w8_scale_cols(I)],
+ * 4-byte aligned; I % 16 == 0.  R or I == 0 is a no-op.  The exponential is
+ * good to a few units in the last place of fp32, so a value next to a
+ * rounding border may take either neighbouring code.
+ */
+int w8_silu_mul_quantize(const uint16_t* H1, int64_t R, int64_t I, uint8_t* A8, uint8_t* SA,
+                         void* stream);
+
+/*
+ * w8a8_gemm -- Y = (X8, SX) * (W8, SW)^T, fp32 accumulation:
+ *   Y[m, n] = bf16_rne( sum_k X8[m, k] 2^(SX[m, k/128] - 127)
+ *                             W8[n, k] 2^(SW[n/128, k/128] - 127) )
+ * (order unspecified but fixed).  The matrix unit adds products in groups of
+ * eight consecutive k, each cut toward zero to 2^-13 of the group's largest
+ * (no form of its fp8 products keeps more); sums of groups are fp32.  That is
+ * below the bf16 rounding of Y unless a result is some hundred times smaller
+ * than its terms.  X8 [M, K], W8 [N, K] 16-byte aligned, SX, SW
+ * 4-byte aligned, Y bf16 [M, N] 2-byte aligned.  M*N == 0 is a no-op; K == 0
+ * writes zeros.
+ */
+int w8a8_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const uint8_t* SW,
+              uint16_t* Y, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * w8_pick_block_size -- alignment block size of the grouped W8A8 product:
+ * the smallest power of two that holds the mean number of pairs per expert,
+ * from 16 to 64.  0 if T < 0, k < 1 or E < 1.
+ */
+int32_t w8_pick_block_size(int64_t T, int32_t k, int32_t E);
+
+/*
+ * w8a8_moe_gemm -- the grouped product over aligned expert blocks.  For every
+ * block b < num_tokens_post_padded / B with e = expert_ids[b] in [0, E) and
+ * every slot holding a pair f = sorted_token_ids[b*B + i] < T*k:
+ *   Y[f, :] = w8a8_gemm of row f / x_row_div of (X8, SX) with expert e
+ * X8 [(T*k) / x_row_div, K], SX one scale row each; W8 [E, N, K], SW
+ * [E, ceil(N/128), C]; Y bf16 [T*k, N].  Rows of Y that no slot names are not
+ * written.  Alignment arrays as moe_align_block_size fills them (same T, k, E,
+ * B); B a multiple of 16 up to 1024 (W4_ERR_SHAPE, W4_ERR_UNSUPPORTED),
+ * x_row_div in {1, k}, E <= 1024, N, K >= 1.  Alignment as w8a8_gemm.
+ */
+int w8a8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const uint8_t* SW,
+                  const int32_t* sorted_token_ids, const int32_t* expert_ids,
+                  const int32_t* num_tokens_post_padded, uint16_t* Y, int64_t T, int32_t k,
+                  int32_t E, int64_t N, int64_t K, int32_t B, int32_t x_row_div, void* stream);
+
+/*
+ * w4_moe_route_scored -- routing by scores, with a bias that only the choice
+ * sees and a limit to the best groups of experts (a reading: the pages name
+ * gating and routing but give no formula; w4_moe_route is the plain softmax
+ * rule).  Per token, in 64-bit arithmetic:
+ *   s[e] = sigmoid(l[e]), or softmax(l)[e]
+ *   c[e] = s[e] + bias[e]                    (bias fp32 [E], or NULL: 0)
+ *   group g (E / groups consecutive experts) is worth the sum of its
+ *   group_top (1 or 2) largest c; the topk_groups best groups stay (equal
+ *   worth: the lower index)
+ *   ids = the k largest c of the groups that stay, in descending order
+ *   (equal c: the lower index)
+ *   w[j] = scale * s[ids[j]] / sum_i s[ids[i]]   (renorm; 0 where the sum is 0)
+ *        = scale * s[ids[j]]                     (otherwise)
+ * weights rounded to fp32 once.  An expert whose logit or bias is NaN or -Inf
+ * is masked: never chosen, no part of the softmax (a logit's mask) or of its
+ * group's worth.  +Inf logits count as the largest finite number.  Slots for
+ * which no unmasked expert is left hold the lowest untaken indices with
+ * weight 0, so a row without any expert yields indices 0..k-1 and zeros.
+ * logits fp32 [T, E]; ids int32, weights fp32 [T, k]; E % groups == 0,
+ * 1 <= topk_groups <= groups (W4_ERR_SHAPE); E <= 1024, k <= 16, k <= E,
+ * groups <= 64, topk_groups * (E / groups) >= k, T <= 2^25
+ * (W4_ERR_UNSUPPORTED).  T == 0 is a no-op.
+ */
+int w4_moe_route_scored(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k,
+                        int32_t sigmoid, int32_t groups, int32_t topk_groups, int32_t group_top,
+                        int32_t renorm, float scale, int32_t* topk_ids, float* topk_weights,
+                        void* stream);
+
+/*
+ * w4_moe_route_scored_bwd -- gradient of w4_moe_route_scored's weights to the
+ * logits, with the choice held fixed (the bias has none: no weight depends
+ * on it).  With g = scale * grad_weights and p = s / sum s over the picks:
+ *   softmax, renorm:  dl[ids j] = p_j (g_j - sum_i g_i p_i)
+ *   sigmoid, renorm:  dl[ids j] = p_j (1 - s_j) (g_j - sum_i g_i p_i)
+ *   sigmoid:          dl[ids j] = g_j s_j (1 - s_j)
+ *   softmax:          dl[e] = s_e (sum_{j: ids j = e} g_j - sum_j g_j s_j), every e
+ * and 0 elsewhere; 64-bit arithmetic, rounded to fp32 once.  topk_ids and
+ * topk_weights are the forward's outputs; a slot whose weight is 0 or whose
+ * id is outside [0, E) takes no part; slots naming one expert twice add up.
+ * grad_weights fp32 [T, k]; grad_logits fp32 [T, E], written whole.
+ */
+int w4_moe_route_scored_bwd(const float* logits, const int32_t* topk_ids,
+                            const float* topk_weights, const float* grad_weights, int64_t T,
+                            int32_t E, int32_t k, int32_t sigmoid, int32_t renorm, float scale,
+                            float* grad_logits, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,7 +18,12 @@ Layouts (all row-major, contiguous, on one GPU):
   St, Zt  bf16 / uint8 [E, w4_repacked_group_elems(N, K)]  scales and zero
           points in kernel order (w4_repack_groups / w4_restore_groups);
           the *_tiled products read Wt, St and Zt and take N explicitly
+  X8, W8  float8_e4m3fn [M, K], [N, K] or [E, N, K]   codes of the W8A8 products
+  SX, SW  float8_e8m0fnu [M, C], [ceil(N/128), C] or [E, ceil(N/128), C]   one
+          scale per 128 k of a row / per 128 x 128 block; C = w8_scale_cols(K)
 """
+
+import math
 
 import torch
 
@@ -35,6 +40,8 @@ __all__ = [
     "w4_repacked_words", "w4_repack", "w4_restore", "w4_repacked_group_elems",
     "w4_repack_groups", "w4_restore_groups", "w4a16_gemm_tiled",
     "w4a16_moe_gemm_tiled", "w4a16_moe_gemm_swiglu_tiled",
+    "w8_scale_cols", "w8_quantize_rows", "w8_quantize_blocks", "w8_silu_mul_quantize", "w8a8_gemm",
+    "w8_pick_block_size", "w8a8_moe_gemm", "w4_moe_route_scored", "w4_moe_route_scored_bwd",
 ]
 
 
@@ -764,3 +771,190 @@ def w4a16_moe_gemm_combine_noalloc(A, Wq, S, sorted_token_ids, expert_ids,
         _ptr(num_tokens_post_padded), _ptr(topk_ids), _ptr(topk_weights), _ptr(H2), _ptr(out),
         T, k, E, N, K, B, 1 if tiled else 0, _stream(A)))
     return out, H2
+
+
+# ------------------------------------------------- W8A8 and the scored router --
+
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _call(name, tensors, *args):
+    """The entry point ``name`` on the device of ``tensors`` (all one device,
+    which need not be the current one) and that device's current stream."""
+    index = tensors[0].device.index
+    for t in tensors:
+        if t is not None and t.device.index != index:
+            raise ValueError(f"{name}: operands on different GPUs")
+    fn = getattr(_lib.load(), name)
+    if index == torch.cuda.current_device():
+        _lib.check(name, fn(*args, _stream(tensors[0])))
+    else:
+        with torch.cuda.device(index):
+            _lib.check(name, fn(*args, _stream(tensors[0])))
+
+
+def _out(t, name, shape, dtype, like):
+    """``t`` checked, or a new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need(t, name, dtype)
+    if t.numel() != math.prod(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _shape(t, name, dtype, shape):
+    _need(t, name, dtype, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _w8_blocks(n):
+    return (n + 127) // 128
+
+
+def w8_scale_cols(K):
+    """Scale bytes of a row of K codes: 4 * ceil(K / 512)."""
+    n = int(_lib.load().w8_scale_cols(K))
+    if n < 0:
+        raise ValueError("invalid K")
+    return n
+
+
+def w8_quantize_rows(X, X8=None, SX=None):
+    """bf16 X [M, K] -> (X8 [M, K], SX [M, C]): e4m3 codes with one
+    power-of-two scale per 128 consecutive k (K % 16 == 0)."""
+    _need(X, "X", torch.bfloat16, 2)
+    M, K = X.shape
+    X8 = _out(X8, "X8", (M, K), _E4M3, X)
+    SX = _out(SX, "SX", (M, w8_scale_cols(K)), _E8M0, X)
+    _call("w8_quantize_rows", (X, X8, SX), _ptr(X), M, K, _ptr(X8), _ptr(SX))
+    return X8, SX
+
+
+def w8_quantize_blocks(W, transposed=False, W8=None, SW=None, WT8=None, ST=None):
+    """bf16 W [N, K] -> (W8 [N, K], SW [ceil(N/128), C], WT8, ST): one scale
+    per 128 x 128 block.  ``transposed``: also the same codes as WT8 [K, N]
+    with ST [ceil(K/128), w8_scale_cols(N)] (N % 16 == 0); else None, None."""
+    _need(W, "W", torch.bfloat16, 2)
+    N, K = W.shape
+    W8 = _out(W8, "W8", (N, K), _E4M3, W)
+    SW = _out(SW, "SW", (_w8_blocks(N), w8_scale_cols(K)), _E8M0, W)
+    if transposed:
+        WT8 = _out(WT8, "WT8", (K, N), _E4M3, W)
+        ST = _out(ST, "ST", (_w8_blocks(K), w8_scale_cols(N)), _E8M0, W)
+    elif WT8 is not None or ST is not None:
+        raise ValueError("WT8 and ST are outputs of transposed=True")
+    _call("w8_quantize_blocks", (W, W8, SW, WT8, ST), _ptr(W), N, K, _ptr(W8), _ptr(SW), _ptr(WT8),
+          _ptr(ST))
+    return W8, SW, WT8, ST
+
+
+def w8_silu_mul_quantize(H1, A8=None, SA=None):
+    """bf16 H1 [R, 2I] -> (A8 [R, I], SA [R, w8_scale_cols(I)]): silu(H1[:, :I])
+    * H1[:, I:] in fp32, quantized as w8_quantize_rows does (I % 16 == 0)."""
+    _need(H1, "H1", torch.bfloat16, 2)
+    R, I2 = H1.shape
+    if I2 % 2:
+        raise ValueError("H1 must have an even number of columns")
+    I = I2 // 2
+    A8 = _out(A8, "A8", (R, I), _E4M3, H1)
+    SA = _out(SA, "SA", (R, w8_scale_cols(I)), _E8M0, H1)
+    _call("w8_silu_mul_quantize", (H1, A8, SA), _ptr(H1), R, I, _ptr(A8), _ptr(SA))
+    return A8, SA
+
+
+def w8a8_gemm(X8, SX, W8, SW, out=None):
+    """Y bf16 [M, N] = (X8, SX) * (W8, SW)^T with fp32 accumulation."""
+    _need(X8, "X8", _E4M3, 2)
+    _need(W8, "W8", _E4M3, 2)
+    M, K = X8.shape
+    N = W8.shape[0]
+    if W8.shape[1] != K:
+        raise ValueError(f"shape mismatch: X8 {tuple(X8.shape)} W8 {tuple(W8.shape)}")
+    cols = w8_scale_cols(K)
+    _shape(SX, "SX", _E8M0, (M, cols))
+    _shape(SW, "SW", _E8M0, (_w8_blocks(N), cols))
+    out = _out(out, "out", (M, N), torch.bfloat16, X8)
+    _call("w8a8_gemm", (X8, SX, W8, SW, out), _ptr(X8), _ptr(SX), _ptr(W8), _ptr(SW), _ptr(out), M,
+          N, K)
+    return out
+
+
+def w8_pick_block_size(T, k, E):
+    return int(_lib.load().w8_pick_block_size(T, k, E))
+
+
+def w8a8_moe_gemm(X8, SX, W8, SW, sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, B,
+                  x_row_div, out=None):
+    """Grouped W8A8 expert product over aligned blocks of B (a multiple of 16).
+
+    Row f of ``out`` bf16 [T*k, N] = row f // x_row_div of (X8, SX) times
+    expert e of (W8 [E, N, K], SW [E, ceil(N/128), C]) for every valid slot f
+    of every block with e = expert_ids[b].  Other rows are not written.
+    """
+    _need(X8, "X8", _E4M3, 2)
+    _need(W8, "W8", _E4M3, 3)
+    E, N, K = W8.shape
+    cols = w8_scale_cols(K)
+    if x_row_div not in (1, k):
+        raise ValueError("x_row_div must be 1 or k")
+    rows = (T * k) // x_row_div
+    if tuple(X8.shape) != (rows, K):
+        raise ValueError(f"X8 must be [{rows}, {K}], got {list(X8.shape)}")
+    _shape(SX, "SX", _E8M0, (rows, cols))
+    _shape(SW, "SW", _E8M0, (E, _w8_blocks(N), cols))
+    cap = w4_moe_align_capacity(T, k, E, B)
+    if cap < 0:
+        raise ValueError("invalid T, k, E or B")
+    for t, n, size in ((sorted_token_ids, "sorted_token_ids", cap),
+                       (expert_ids, "expert_ids", cap // B),
+                       (num_tokens_post_padded, "num_tokens_post_padded", 1)):
+        _need(t, n, torch.int32)
+        if t.numel() < size:
+            raise ValueError(f"{n} needs {size} entries")
+    out = _out(out, "out", (T * k, N), torch.bfloat16, X8)
+    _call("w8a8_moe_gemm", (X8, SX, W8, SW, sorted_token_ids, expert_ids, num_tokens_post_padded, out),
+          _ptr(X8), _ptr(SX), _ptr(W8), _ptr(SW), _ptr(sorted_token_ids), _ptr(expert_ids),
+          _ptr(num_tokens_post_padded), _ptr(out), T, k, E, N, K, B, x_row_div)
+    return out
+
+
+def w4_moe_route_scored(logits, k, sigmoid=False, bias=None, groups=1, topk_groups=1, group_top=1,
+                        renorm=True, scale=1.0, topk_ids=None, topk_weights=None):
+    """fp32 logits [T, E] -> (int32 ids [T, k], fp32 weights [T, k]) by scores.
+
+    Scores are sigmoid(logits) or the row's softmax; the choice goes by score
+    + ``bias`` (fp32 [E]) within the ``topk_groups`` best of ``groups`` groups
+    (worth: the sum of their ``group_top`` largest); weights are ``scale``
+    times the chosen scores, which ``renorm`` makes sum to one.  Ties go to
+    the lower index; NaN and -Inf mask an expert.
+    """
+    _need(logits, "logits", torch.float32, 2)
+    T, E = logits.shape
+    if bias is not None:
+        _shape(bias, "bias", torch.float32, (E,))
+    topk_ids = _out(topk_ids, "topk_ids", (T, k), torch.int32, logits)
+    topk_weights = _out(topk_weights, "topk_weights", (T, k), torch.float32, logits)
+    _call("w4_moe_route_scored", (logits, bias, topk_ids, topk_weights), _ptr(logits), _ptr(bias), T,
+          E, k, int(sigmoid), groups, topk_groups, group_top, int(renorm), scale, _ptr(topk_ids),
+          _ptr(topk_weights))
+    return topk_ids, topk_weights
+
+
+def w4_moe_route_scored_bwd(logits, topk_ids, topk_weights, grad_weights, sigmoid=False, renorm=True,
+                            scale=1.0, grad_logits=None):
+    """Gradient of w4_moe_route_scored's weights to the logits (the choice held
+    fixed): fp32 [T, E] from the forward's outputs and grad_weights [T, k]."""
+    _need(logits, "logits", torch.float32, 2)
+    T, E = logits.shape
+    _need(topk_ids, "topk_ids", torch.int32, 2)
+    k = topk_ids.shape[1]
+    _shape(topk_ids, "topk_ids", torch.int32, (T, k))
+    _shape(topk_weights, "topk_weights", torch.float32, (T, k))
+    _shape(grad_weights, "grad_weights", torch.float32, (T, k))
+    grad_logits = _out(grad_logits, "grad_logits", (T, E), torch.float32, logits)
+    _call("w4_moe_route_scored_bwd", (logits, topk_ids, topk_weights, grad_weights, grad_logits),
+          _ptr(logits), _ptr(topk_ids), _ptr(topk_weights), _ptr(grad_weights), T, E, k,
+          int(sigmoid), int(renorm), scale, _ptr(grad_logits))
+    return grad_logits

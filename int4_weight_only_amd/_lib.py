@@ -59,6 +59,18 @@ SIGNATURES = {
                                             _i32, _i64, _i64, _i32, _i32, _p]),
     "w4a16_moe_gemm_swiglu_tiled": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _i64, _i32,
                                                    _i32, _i64, _i64, _i32, _i32, _p]),
+    "w8_scale_cols": (_i64, [_i64]),
+    "w8_quantize_rows": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p]),
+    "w8_quantize_blocks": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p, _p, _p]),
+    "w8_silu_mul_quantize": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p]),
+    "w8a8_gemm": (ctypes.c_int, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
+    "w8_pick_block_size": (_i32, [_i64, _i32, _i32]),
+    "w8a8_moe_gemm": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i64, _i64,
+                                     _i32, _i32, _p]),
+    "w4_moe_route_scored": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                           ctypes.c_float, _p, _p, _p]),
+    "w4_moe_route_scored_bwd": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, _i32,
+                                               ctypes.c_float, _p, _p]),
 }
 
 _lib = None

@@ -6,6 +6,7 @@
 #include "w4a16.h"
 
 #include "common.h"
+#include "w8.h"
 
 namespace {
 
@@ -578,6 +579,161 @@ int w4a16_moe_gemm_combine_noalloc(const uint16_t* A, const int32_t* Wq, const u
                                                 num_tokens_post_padded, topk_ids, topk_weights,
                                                 H2, Out, words, T, k, E, N, K, B, tiled != 0,
                                                 as_stream(stream)));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------ W8A8 and the scored router --
+
+namespace {
+
+constexpr int64_t kMaxElems = (int64_t)1 << 40;
+constexpr int64_t kMaxGrid = (int64_t)1 << 32;      // threads of one launch
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 25;    // one wave each
+
+// Sizes of an e4m3 operand [R, K]: K in whole 16-byte pieces.
+int w8_shape(int64_t R, int64_t K) {
+  if (R < 0 || K < 0 || K % 16 != 0) return W4_ERR_SHAPE;
+  if (K > w4::kW8MaxK || R > kMaxI32 || R * K > kMaxElems) return W4_ERR_UNSUPPORTED;
+  return W4_OK;
+}
+
+int route_rule(int32_t E, int32_t k, int32_t groups, int32_t topk_groups, int32_t group_top) {
+  if (E < 1 || k < 1 || groups < 1 || topk_groups < 1 || topk_groups > groups || E % groups != 0)
+    return W4_ERR_SHAPE;
+  if (group_top != 1 && group_top != 2) return W4_ERR_SHAPE;
+  if (E > 1024 || k > 16 || k > E || groups > 64 || (int64_t)topk_groups * (E / groups) < k)
+    return W4_ERR_UNSUPPORTED;
+  return W4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t w8_scale_cols(int64_t K) { return K < 0 ? -1 : w4::w8_cols(K); }
+
+int w8_quantize_rows(const uint16_t* X, int64_t M, int64_t K, uint8_t* X8, uint8_t* SX,
+                     void* stream) {
+  const int v = w8_shape(M, K);
+  if (v != W4_OK) return v;
+  if (M == 0 || K == 0) return W4_OK;
+  if (!X || !X8 || !SX) return W4_ERR_NULL;
+  if (!aligned(X, 16) || !aligned(X8, 16) || !aligned(SX, 4)) return W4_ERR_MISALIGNED;
+  return hip_status(w4::launch_w8_quantize_rows(X, M, K, X8, SX, as_stream(stream)));
+}
+
+int w8_quantize_blocks(const uint16_t* W, int64_t N, int64_t K, uint8_t* W8, uint8_t* SW,
+                       uint8_t* WT8, uint8_t* ST, void* stream) {
+  const int v = w8_shape(N, K);
+  if (v != W4_OK) return v;
+  if (N == 0 || K == 0) return W4_OK;
+  if (!W || !W8 || !SW || (WT8 != nullptr) != (ST != nullptr)) return W4_ERR_NULL;
+  if (WT8) {
+    const int u = w8_shape(K, N);
+    if (u != W4_OK) return u;
+  }
+  if (w4::w8_cols(K) * (w4::w8_blocks(N) + 3) * 256 >= kMaxGrid) return W4_ERR_UNSUPPORTED;
+  if (!aligned(W, 16) || !aligned(W8, 16) || !aligned(SW, 4) || !aligned(WT8, 16) ||
+      !aligned(ST, 4))
+    return W4_ERR_MISALIGNED;
+  return hip_status(w4::launch_w8_quantize_blocks(W, N, K, W8, SW, WT8, ST, as_stream(stream)));
+}
+
+int w8_silu_mul_quantize(const uint16_t* H1, int64_t R, int64_t I, uint8_t* A8, uint8_t* SA,
+                         void* stream) {
+  const int v = w8_shape(R, I);
+  if (v != W4_OK) return v;
+  if (R == 0 || I == 0) return W4_OK;
+  if (!H1 || !A8 || !SA) return W4_ERR_NULL;
+  if (!aligned(H1, 16) || !aligned(A8, 16) || !aligned(SA, 4)) return W4_ERR_MISALIGNED;
+  return hip_status(w4::launch_w8_silu_mul_quantize(H1, R, I, A8, SA, as_stream(stream)));
+}
+
+int w8a8_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const uint8_t* SW,
+              uint16_t* Y, int64_t M, int64_t N, int64_t K, void* stream) {
+  if (M < 0 || N < 0) return W4_ERR_SHAPE;
+  int v = w8_shape(M, K);
+  if (v == W4_OK) v = w8_shape(N, K);
+  if (v != W4_OK) return v;
+  if (M * N > kMaxElems || w4::w8_gemm_threads(M, N, K) >= kMaxGrid) return W4_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return W4_OK;
+  if (!Y) return W4_ERR_NULL;
+  if (!aligned(Y, 2)) return W4_ERR_MISALIGNED;
+  if (K == 0) return hip_status(w4::launch_zero_bf16(Y, M * N, as_stream(stream)));
+  if (!X8 || !SX || !W8 || !SW) return W4_ERR_NULL;
+  if (!aligned(X8, 16) || !aligned(W8, 16) || !aligned(SX, 4) || !aligned(SW, 4))
+    return W4_ERR_MISALIGNED;
+  return hip_status(w4::launch_w8_gemm(X8, SX, W8, SW, Y, M, N, K, as_stream(stream)));
+}
+
+int32_t w8_pick_block_size(int64_t T, int32_t k, int32_t E) {
+  if (T < 0 || k < 1 || E < 1) return 0;
+  const int64_t mean = (T * k + E - 1) / E;
+  int32_t B = 16;
+  while (B < 64 && B < mean) B *= 2;
+  return B;
+}
+
+int w8a8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const uint8_t* SW,
+                  const int32_t* sorted_token_ids, const int32_t* expert_ids,
+                  const int32_t* num_tokens_post_padded, uint16_t* Y, int64_t T, int32_t k,
+                  int32_t E, int64_t N, int64_t K, int32_t B, int32_t x_row_div, void* stream) {
+  if (T < 0 || k < 1 || E < 1 || N < 1 || K < 16 || K % 16 != 0 || B < 16 || B % 16 != 0)
+    return W4_ERR_SHAPE;
+  if (x_row_div != 1 && x_row_div != k) return W4_ERR_SHAPE;
+  if (B > 1024 || E > 1024 || T > kMaxI32 || N > kMaxI32 || K > w4::kW8MaxK ||
+      T * k + (int64_t)E * B >= kMaxI32 || T * k * N > kMaxElems || N * K > kMaxElems ||
+      E * (N * K) > kMaxElems)
+    return W4_ERR_UNSUPPORTED;
+  if (w4::w8_moe_threads(T, k, E, N, K, B) >= kMaxGrid) return W4_ERR_UNSUPPORTED;
+  if (T == 0) return W4_OK;
+  if (!X8 || !SX || !W8 || !SW || !sorted_token_ids || !expert_ids || !num_tokens_post_padded || !Y)
+    return W4_ERR_NULL;
+  if (!aligned(X8, 16) || !aligned(W8, 16) || !aligned(SX, 4) || !aligned(SW, 4) ||
+      !aligned(Y, 2) || !aligned(sorted_token_ids, 4) || !aligned(expert_ids, 4) ||
+      !aligned(num_tokens_post_padded, 4))
+    return W4_ERR_MISALIGNED;
+  return hip_status(w4::launch_w8_moe_gemm(X8, SX, W8, SW, sorted_token_ids, expert_ids,
+                                           num_tokens_post_padded, Y, T, k, E, N, K, B, x_row_div,
+                                           as_stream(stream)));
+}
+
+int w4_moe_route_scored(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k,
+                        int32_t sigmoid, int32_t groups, int32_t topk_groups, int32_t group_top,
+                        int32_t renorm, float scale, int32_t* topk_ids, float* topk_weights,
+                        void* stream) {
+  if (T < 0) return W4_ERR_SHAPE;
+  const int v = route_rule(E, k, groups, topk_groups, group_top);
+  if (v != W4_OK) return v;
+  if (T > kMaxTokens) return W4_ERR_UNSUPPORTED;
+  if (T == 0) return W4_OK;
+  if (!logits || !topk_ids || !topk_weights) return W4_ERR_NULL;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(topk_ids, 4) ||
+      !aligned(topk_weights, 4))
+    return W4_ERR_MISALIGNED;
+  const w4::RouteRule r = {sigmoid != 0, groups, topk_groups, group_top, renorm != 0, scale};
+  return hip_status(w4::launch_route_scored(logits, bias, T, E, k, r, topk_ids, topk_weights,
+                                            as_stream(stream)));
+}
+
+int w4_moe_route_scored_bwd(const float* logits, const int32_t* topk_ids,
+                            const float* topk_weights, const float* grad_weights, int64_t T,
+                            int32_t E, int32_t k, int32_t sigmoid, int32_t renorm, float scale,
+                            float* grad_logits, void* stream) {
+  if (T < 0) return W4_ERR_SHAPE;
+  const int v = route_rule(E, k, 1, 1, 1);
+  if (v != W4_OK) return v;
+  if (T > kMaxTokens) return W4_ERR_UNSUPPORTED;
+  if (T == 0) return W4_OK;
+  if (!logits || !topk_ids || !topk_weights || !grad_weights || !grad_logits) return W4_ERR_NULL;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
+      !aligned(grad_weights, 4) || !aligned(grad_logits, 4))
+    return W4_ERR_MISALIGNED;
+  const w4::RouteRule r = {sigmoid != 0, 1, 1, 1, renorm != 0, scale};
+  return hip_status(w4::launch_route_scored_bwd(logits, topk_ids, topk_weights, grad_weights, T, E,
+                                                k, r, grad_logits, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,77 @@
+// Internal declarations of the 8-bit floating-point (W8A8) kernels and the
+// scored router.
+//
+// Values: e4m3 codes (OCP, largest 448) with one power-of-two scale per
+// block of 128 along K (activations) or 128 x 128 (weights), stored as its
+// biased exponent b (e8m0: 2^(b - 127), 255 = NaN).  CDNA4's
+// v_mfma_scale_f32_*_f8f6f4 takes such a byte per lane and 32 elements and
+// applies it inside the matrix pipe, so the block scales cost no vector
+// instruction and the accumulator is the matrix unit's own for the whole K.
+#pragma once
+
+#include "common.h"
+
+namespace w4 {
+
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kW8Block = 128;       // elements per scale along K, rows per weight scale
+constexpr int kW8MaxK = 1 << 22;    // a tile of 256 rows spans less than 2^31 bytes
+
+// scale bytes of a row: whole dwords, so that the scales of four K blocks
+// are one aligned load
+__host__ __device__ __forceinline__ int64_t w8_cols(int64_t K) { return (K + 511) / 512 * 4; }
+__host__ __device__ __forceinline__ int64_t w8_blocks(int64_t n) { return (n + 127) / 128; }
+
+// D[16x16] += A[16x128] * B[128x16] of e4m3 codes, fp32 accumulation, one
+// scale byte per operand row (byte SA of sa, SB of sb).  Lane l supplies 32
+// bytes of A row (l % 16) and of B column (l % 16); lanes l / 16 = 0..3
+// split the 128 elements of the block between them, in any order that A and
+// B share (one scale covers the whole block).  It receives
+// D[4 (l / 16) + r][l % 16], r = 0..3.
+// Precision: the unit cuts each product toward zero to 2^-13 of the largest
+// in its group of eight consecutive bytes and adds the groups in fp32
+// (measured; the older 16x16x32 fp8 form does the same).  Exact products
+// would need the codes widened to bf16, at half the matrix rate and twice
+// the operand traffic, to move a result by less than its bf16 rounding.
+template <int SA = 0, int SB = 0>
+__device__ __forceinline__ f32x4 mfma8_16(i32x8 a, i32x8 b, f32x4 c, uint32_t sa, uint32_t sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, SA, (int)sa, SB, (int)sb);
+}
+
+__device__ __forceinline__ i32x8 join16(u32x4 lo, u32x4 hi) {
+  return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,
+               (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+
+hipError_t launch_w8_quantize_rows(const uint16_t* X, int64_t M, int64_t K, uint8_t* X8,
+                                   uint8_t* SX, hipStream_t st);
+hipError_t launch_w8_quantize_blocks(const uint16_t* W, int64_t N, int64_t K, uint8_t* W8,
+                                     uint8_t* SW, uint8_t* WT8, uint8_t* ST, hipStream_t st);
+hipError_t launch_w8_silu_mul_quantize(const uint16_t* H1, int64_t R, int64_t I, uint8_t* A8,
+                                       uint8_t* SA, hipStream_t st);
+// threads the products would start at most (for the launch limit)
+int64_t w8_gemm_threads(int64_t M, int64_t N, int64_t K);
+hipError_t launch_w8_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
+                          const uint8_t* SW, uint16_t* Y, int64_t M, int64_t N, int64_t K,
+                          hipStream_t st);
+int64_t w8_moe_threads(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B);
+hipError_t launch_w8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
+                              const uint8_t* SW, const int32_t* sorted_ids,
+                              const int32_t* expert_ids, const int32_t* ntpp, uint16_t* Y,
+                              int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B,
+                              int32_t x_row_div, hipStream_t st);
+// the scored router
+struct RouteRule {
+  bool sigmoid;                     // scores: sigmoid, or softmax over the row
+  int groups, topk_groups, group_top;
+  bool renorm;
+  float scale;
+};
+hipError_t launch_route_scored(const float* logits, const float* bias, int64_t T, int32_t E,
+                               int32_t k, const RouteRule& r, int32_t* ids, float* w,
+                               hipStream_t st);
+hipError_t launch_route_scored_bwd(const float* logits, const int32_t* ids, const float* w,
+                                   const float* dw, int64_t T, int32_t E, int32_t k,
+                                   const RouteRule& r, float* dlogits, hipStream_t st);
+}  // namespace w4

@@ -18,6 +18,16 @@ with zero points ("Quantization basics: from FP32 to INT4" §2.3) run the
 ``_asym`` forms of the two grouped products; experts converted to the
 kernel-order layouts (``repack_experts``, §4's weight-layout conversion,
 codes and per-group values alike) run the ``_tiled`` forms.
+
+``moe_layer_w8`` is the layer on 8-bit floating-point experts (the W8A8 side
+of the pages' rollout comparison) behind the scored router:
+
+    logits --w4_moe_route_scored--> ids, weights
+    X --w8_quantize_rows--> X8, SX
+    X8 --w8a8_moe_gemm (gate_up, x_row_div = k)--> H1 [T*k, 2I]
+    H1 --w8_silu_mul_quantize--> A8, SA
+    A8 --w8a8_moe_gemm (down, x_row_div = 1)--> H2 [T*k, H]
+    H2, weights --w4_moe_sum--> Out [T, H]
 """
 
 from dataclasses import dataclass
@@ -28,7 +38,10 @@ from . import (moe_align_block_size, w4_moe_align_capacity, w4_moe_combine_works
                w4_moe_route, w4_moe_sum, w4a16_moe_gemm_combine,
                w4_pick_block_size, w4_quantize_pack, w4_quantize_pack_asym, w4_repack,
                w4_repack_groups, w4_silu_mul, w4a16_moe_gemm, w4a16_moe_gemm_asym, w4a16_moe_gemm_swiglu,
-               w4a16_moe_gemm_swiglu_asym, w4a16_moe_gemm_swiglu_tiled, w4a16_moe_gemm_tiled)
+               w4a16_moe_gemm_swiglu_asym, w4a16_moe_gemm_swiglu_tiled, w4a16_moe_gemm_tiled,
+               w4_moe_route_scored, w4_moe_route_scored_bwd, w8_pick_block_size,
+               w8_quantize_blocks, w8_quantize_rows, w8_scale_cols, w8_silu_mul_quantize,
+               w8a8_moe_gemm)
 
 
 @dataclass
@@ -215,4 +228,134 @@ def moe_layer(X, logits, k, gate_up, down, B=None, buffers=None, fused=True,
     """Routing plus ``moe_forward``: logits fp32 [T, E] -> Out bf16 [T, H]."""
     ids, w = w4_moe_route(logits, k)
     out, b = moe_forward(X, ids, w, gate_up, down, B, buffers, fused, fused_combine)
+    return out, ids, w, b
+
+
+# ------------------------------------------------- W8A8 experts, scored router --
+
+class RouteScored(torch.autograd.Function):
+    """``w4_moe_route_scored`` whose weights carry a gradient to the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, k, sigmoid, bias, groups, topk_groups, group_top, renorm, scale):
+        logits = logits.contiguous()
+        ids, w = w4_moe_route_scored(logits, k, sigmoid, bias, groups, topk_groups, group_top,
+                                     renorm, scale)
+        ctx.save_for_backward(logits, ids, w)
+        ctx.rule = (sigmoid, renorm, scale)
+        ctx.mark_non_differentiable(ids)
+        return ids, w
+
+    @staticmethod
+    def backward(ctx, _, grad_w):
+        logits, ids, w = ctx.saved_tensors
+        return (w4_moe_route_scored_bwd(logits, ids, w, grad_w.contiguous(), *ctx.rule),
+                *(None,) * 8)
+
+
+def route_scored(logits, k, sigmoid=False, bias=None, groups=1, topk_groups=1, group_top=1,
+                 renorm=True, scale=1.0):
+    """(ids, weights) of ``w4_moe_route_scored``, the weights differentiable
+    to ``logits``.  The bias only steers the choice and gets no gradient."""
+    return RouteScored.apply(logits, k, sigmoid, bias, groups, topk_groups, group_top, renorm,
+                             scale)
+
+
+@dataclass
+class ExpertWeightsW8:
+    """Stacked 8-bit weights of E experts: W8 float8_e4m3fn [E, N, K], SW
+    float8_e8m0fnu [E, ceil(N/128), w8_scale_cols(K)]."""
+    W8: torch.Tensor
+    SW: torch.Tensor
+
+    @property
+    def E(self):
+        return self.W8.shape[0]
+
+    @property
+    def N(self):
+        return self.W8.shape[1]
+
+    @property
+    def K(self):
+        return self.W8.shape[2]
+
+    def nbytes(self):
+        return self.W8.numel() + self.SW.numel()
+
+
+def quantize_experts_w8(E, N, K, source, device):
+    """``quantize_experts`` for 8-bit experts: ``source(e)`` returns expert
+    e's bf16 [N, K] weight; one source matrix is alive at a time."""
+    W8 = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=device)
+    SW = torch.empty((E, (N + 127) // 128, w8_scale_cols(K)), dtype=torch.float8_e8m0fnu,
+                     device=device)
+    for e in range(E):
+        w = source(e)
+        w8_quantize_blocks(w, W8=W8[e], SW=SW[e])
+        del w
+    return ExpertWeightsW8(W8, SW)
+
+
+@dataclass
+class MoEBuffersW8:
+    ids: torch.Tensor
+    weights: torch.Tensor
+    sorted_token_ids: torch.Tensor
+    expert_ids: torch.Tensor
+    ntpp: torch.Tensor
+    X8: torch.Tensor
+    SX: torch.Tensor
+    H1: torch.Tensor
+    A8: torch.Tensor
+    SA: torch.Tensor
+    H2: torch.Tensor
+    out: torch.Tensor
+
+
+def alloc_buffers_w8(T, k, E, H, I, B, device):
+    cap = w4_moe_align_capacity(T, k, E, B)
+
+    def new(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=device)
+    i32, bf, e4m3, e8m0 = torch.int32, torch.bfloat16, torch.float8_e4m3fn, torch.float8_e8m0fnu
+    return MoEBuffersW8(new((T, k), i32), new((T, k), torch.float32), new(cap, i32),
+                        new(cap // B, i32), new(1, i32), new((T, H), e4m3),
+                        new((T, w8_scale_cols(H)), e8m0), new((T * k, 2 * I), bf),
+                        new((T * k, I), e4m3), new((T * k, w8_scale_cols(I)), e8m0),
+                        new((T * k, H), bf), new((T, H), bf))
+
+
+def moe_forward_w8(X, topk_ids, topk_weights, gate_up, down, B=None, buffers=None):
+    """Expert part of the layer for routed tokens on 8-bit experts.
+
+    X bf16 [T, H]; topk_ids int32 [T, k]; topk_weights fp32 [T, k]; gate_up:
+    E experts of [2I, H]; down: E experts of [H, I] (``ExpertWeightsW8``).  B
+    defaults to ``w8_pick_block_size``.  Returns (Out bf16 [T, H], buffers).
+    """
+    T, H = X.shape
+    k = topk_ids.shape[1]
+    E = gate_up.E
+    I = gate_up.N // 2
+    if gate_up.N % 2 or down.E != E or down.N != H or down.K != I or gate_up.K != H:
+        raise ValueError("expert weight shapes do not match X")
+    if B is None:
+        B = w8_pick_block_size(T, k, E)
+    b = buffers or alloc_buffers_w8(T, k, E, H, I, B, X.device)
+    w8_quantize_rows(X, b.X8, b.SX)
+    plan = moe_align_block_size(topk_ids, E, B, b.sorted_token_ids, b.expert_ids, b.ntpp)
+    w8a8_moe_gemm(b.X8, b.SX, gate_up.W8, gate_up.SW, *plan, T, k, B, k, out=b.H1)
+    w8_silu_mul_quantize(b.H1, b.A8, b.SA)
+    w8a8_moe_gemm(b.A8, b.SA, down.W8, down.SW, *plan, T, k, B, 1, out=b.H2)
+    w4_moe_sum(b.H2, topk_weights, T, k, out=b.out)
+    return b.out, b
+
+
+def moe_layer_w8(X, logits, k, gate_up, down, sigmoid=False, bias=None, groups=1, topk_groups=1,
+                 group_top=1, renorm=True, scale=1.0, B=None, buffers=None):
+    """The scored router plus ``moe_forward_w8``: logits fp32 [T, E] -> (Out
+    bf16 [T, H], ids, weights, buffers)."""
+    ids, w = w4_moe_route_scored(logits, k, sigmoid, bias, groups, topk_groups, group_top, renorm,
+                                 scale, *((buffers.ids, buffers.weights) if buffers else ()))
+    out, b = moe_forward_w8(X, ids, w, gate_up, down, B, buffers)
     return out, ids, w, b
