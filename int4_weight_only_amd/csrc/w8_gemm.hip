@@ -3,6 +3,8 @@
 //   Y[m, n] = bf16( sum_k X8[m, k] 2^SX[m, k/128] W8[n, k] 2^SW[n/128, k/128] )
 //
 // dense (w8a8_gemm) and grouped over aligned expert blocks (w8a8_moe_gemm).
+#include <type_traits>
+
 #include "w8.h"
 
 namespace w4 {
@@ -16,6 +18,21 @@ struct Grouped {
   const int32_t* ntpp;
   int P, E, B, div;     // pairs T k, experts, rows per aligned block, pairs per X row
 };
+
+// Four consecutive outputs n .. n + 3 of a row; vec: whole and aligned.
+__device__ __forceinline__ void store4(uint16_t* row, int64_t n, int64_t N, f32x4 s, bool vec) {
+  if (n >= N) return;
+  const u32x2 o = {pk_bf16(s.x, s.y), pk_bf16(s.z, s.w)};
+  uint16_t* y = row + n;
+  if (vec) {
+    *(u32x2*)y = o;
+    return;
+  }
+  y[0] = (uint16_t)o.x;
+  if (n + 1 < N) y[1] = (uint16_t)(o.x >> 16);
+  if (n + 2 < N) y[2] = (uint16_t)o.y;
+  if (n + 3 < N) y[3] = (uint16_t)(o.y >> 16);
+}
 
 }  // namespace
 
@@ -133,18 +150,224 @@ __global__ __launch_bounds__(NW * 64) void k_w8_split(const uint8_t* __restrict_
     int64_t row = -1;
 #pragma unroll
     for (int q = 0; q < MT; ++q) row = q == i ? yrow[q] : row;
-    const int64_t n = n0 + 16 * j + 4 * h;
-    if (row < 0 || n >= N) continue;
-    uint16_t* y = Y + row * N + n;
-    const u32x2 o = {pk_bf16(s.x, s.y), pk_bf16(s.z, s.w)};
-    if (vec) {
-      *(u32x2*)y = o;
-    } else {
-      y[0] = (uint16_t)o.x;
-      if (n + 1 < N) y[1] = (uint16_t)(o.x >> 16);
-      if (n + 2 < N) y[2] = (uint16_t)o.y;
-      if (n + 3 < N) y[3] = (uint16_t)(o.y >> 16);
+    if (row >= 0) store4(Y + row * N, n0 + 16 * j + 4 * h, N, s, vec);
+  }
+}
+
+// ------------------------------------------------------------- LDS tile --
+// A workgroup of four waves computes BM = 32 MI rows of X times BN = 32 NI
+// rows of W, wave (wm, wn) of the 2 x 2 waves 16 MI x 16 NI of them as
+// MI x NI tiles of v_mfma_scale_f32_16x16x128.  Both operands go from memory
+// straight into LDS (16-byte buffer_load ... lds), one 128-byte K block per
+// step, two stages; a row's eight 16-byte pieces are stored XOR-swizzled by
+// (row / 2) % 8, so that an operand read of 16 rows spreads over the banks.
+//
+// One barrier per step.  A wave holds all MI operand tiles of X and four of W:
+// while tile j of W multiplies, tile j + 3 is read.  Three W tiles before the
+// end of a step the waves meet: the next stage has landed and everyone has read
+// the last of this one, so its buffer takes the loads of two steps ahead,
+// spread over the step's last MFMAs, and each X tile is replaced by the next
+// step's right after its last use.  The loads have most of a step to land and
+// no MFMA waits for the start of a step.  An odd number of steps is made even
+// by one of zeros (pieces past K read zero).
+//
+// The scales of four K blocks are one dword a row; they pass through a small
+// LDS ring the same way.
+namespace {
+
+constexpr uint32_t kOOB = 0x80000000u;   // byte offset past any buffer: reads 0
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off,
+                                           uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 16, off, soff, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off,
+                                          uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 4, off, soff, 0, 0);
+}
+
+}  // namespace
+
+template <int MI, int NI>
+__global__ __launch_bounds__(256, 1) void k_w8_tile(const uint8_t* __restrict__ X8,
+                                                    const uint8_t* __restrict__ SX,
+                                                    const uint8_t* __restrict__ W8,
+                                                    const uint8_t* __restrict__ SW,
+                                                    uint16_t* __restrict__ Y, int M, int N, int K) {
+  constexpr int BM = 32 * MI, BN = 32 * NI;
+  constexpr int XA = BM / 32, XB = BN / 32;        // 1 KB loads per wave and stage
+  static_assert(NI == 4 || NI == 8, "a wave's rows of W share a scale, four W tiles in flight");
+  static_assert(MI == 4 || MI == 8, "scale ring");
+  __shared__ __attribute__((aligned(16))) uint8_t as0[BM * 128], as1[BM * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t bs0[BN * 128], bs1[BN * 128];
+  __shared__ __attribute__((aligned(16))) uint32_t rx[2][256], rw[2][64];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int r16 = lane & 15, h = lane >> 4;
+  // tile order: XCD x (workgroups round-robin over 8) walks a contiguous
+  // range of tiles in groups of 8 row blocks of X, which share operands in
+  // its L2
+  const int mt = (M + BM - 1) / BM, nt = (N + BN - 1) / BN;
+  const int tiles = mt * nt, per = (tiles + 7) / 8;
+  const int t = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  if (t >= tiles || (int)(blockIdx.x / 8) >= per) return;
+  const int group = t / (8 * nt), gm = min(8, mt - group * 8), in_group = t - group * 8 * nt;
+  const int64_t m0 = (int64_t)(group * 8 + in_group % gm) * BM, n0 = (int64_t)(in_group / gm) * BN;
+
+  const int cols = (int)w8_cols(K);
+  const int steps = (K + 127) / 128;
+  const int rows_x = (int)min((int64_t)BM, M - m0), rows_w = (int)min((int64_t)BN, N - n0);
+  const __amdgpu_buffer_rsrc_t ar = rsrc(X8 + m0 * K, (int64_t)rows_x * K);
+  const __amdgpu_buffer_rsrc_t br = rsrc(W8 + n0 * K, (int64_t)rows_w * K);
+  const __amdgpu_buffer_rsrc_t sar = rsrc(SX + m0 * cols, (int64_t)rows_x * cols);
+  const __amdgpu_buffer_rsrc_t sbr =
+      rsrc(SW + (n0 >> 7) * cols, (((n0 + rows_w - 1) >> 7) - (n0 >> 7) + 1) * cols);
+
+  // load I of a stage fills its rows 8 I .. 8 I + 7: lane l writes slot l % 8
+  // of row l / 8, which holds piece (l % 8) ^ ((row / 2) % 8)
+  auto piece = [&](int I) { return (lane & 7) ^ ((4 * I + (lane >> 4)) & 7); };
+  uint32_t aoff[XA], boff[XB];
+#pragma unroll
+  for (int i = 0; i < XA; ++i) {
+    const int I = wave * XA + i, r = 8 * I + (lane >> 3);
+    aoff[i] = r < rows_x ? (uint32_t)r * (uint32_t)K + 16u * piece(I) : kOOB;
+  }
+#pragma unroll
+  for (int i = 0; i < XB; ++i) {
+    const int I = wave * XB + i, r = 8 * I + (lane >> 3);
+    boff[i] = r < rows_w ? (uint32_t)r * (uint32_t)K + 16u * piece(I) : kOOB;
+  }
+  const int srow = 64 * wave + lane;               // row of the scale ring this lane fills
+  const uint32_t sxoff = srow < rows_x ? (uint32_t)(srow * cols) : kOOB;
+  const uint32_t swoff = lane < 2 ? (uint32_t)(lane * cols) : kOOB;   // past the end: 0
+
+  // part q of 3 of a stage's loads
+  auto load_part = [&](int q, int step, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
+    const uint32_t k0 = (uint32_t)step * 128u;
+    const int left = K - (int)k0;                  // pieces past K read zero
+#pragma unroll
+    for (int i = q * XA / 3; i < (q + 1) * XA / 3; ++i)
+      load_lds16(ar, sa + (wave * XA + i) * 1024, 16 * piece(wave * XA + i) < left ? aoff[i] : kOOB,
+                 k0);
+#pragma unroll
+    for (int i = q * XB / 3; i < (q + 1) * XB / 3; ++i)
+      load_lds16(br, sb + (wave * XB + i) * 1024, 16 * piece(wave * XB + i) < left ? boff[i] : kOOB,
+                 k0);
+  };
+  auto load_scales = [&](int quad) __attribute__((always_inline)) {
+    if (BM == 256 || wave < 2) load_lds4(sar, rx[quad & 1] + 64 * wave, sxoff, (uint32_t)quad * 4u);
+    load_lds4(sbr, rw[quad & 1], swoff, (uint32_t)quad * 4u);   // by every wave, the same bytes
+  };
+  // operand tile i of a wave's rows (16 rows keep the swizzle of the first)
+  auto read = [&](const uint8_t* s, int at, int i) __attribute__((always_inline)) {
+    return join16(*(const u32x4*)(s + at + 2048 * i), *(const u32x4*)(s + (at ^ 64) + 2048 * i));
+  };
+  const int xrow = wm * 16 * MI + r16;
+  const int swz = 16 * (h ^ (r16 >> 1));
+  const int xat = xrow * 128 + swz, wat = (wn * 16 * NI + r16) * 128 + swz;
+
+  // a zero that the compiler does not see as constant: it would split loop
+  // variables that start at one into single registers
+  f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  asm("" : "+v"(zero));
+  f32x4 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j) acc[i][j] = zero;
+  i32x8 x[MI], w[4];
+  uint32_t sx[MI], sw;
+  // the dword that holds a step's scale (the added step repeats the last
+  // one's), and its place in it
+  auto scale_at = [&](int step) { return min(step, steps - 1); };
+  auto read_sx = [&](int step, int i) __attribute__((always_inline)) {
+    return rx[(scale_at(step) >> 2) & 1][xrow + 16 * i];
+  };
+  auto read_sw = [&](int step) __attribute__((always_inline)) {
+    return rw[(scale_at(step) >> 2) & 1][(wn * 16 * NI) >> 7];
+  };
+  auto shift = [&](int step) { return 8 * (scale_at(step) & 3); };
+  auto fence = [] __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // one step on stage (sa, sb); (na, nb) is the next one's
+  auto body = [&](int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
+      __attribute__((always_inline)) {
+    uint32_t nsx[MI], nsw;
+    const int sh = shift(step + 1);
+    load_scales(step / 4 + 1);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      if (j == NI - 3) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        fence();
+      }
+      if (j < NI - 3) {
+        w[(j + 3) & 3] = read(sb, wat, j + 3);
+      } else {
+        w[(j + 3) & 3] = read(nb, wat, j + 3 - NI);
+        load_part(j - (NI - 3), step + 2, sa, sb);
+      }
+      if (j == NI - 2) {
+        nsw = read_sw(step + 1);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) nsx[i] = read_sx(step + 1, i);
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        acc[i][j] = mfma8_16(w[j & 3], x[i], acc[i][j], sw, sx[i]);
+        if (j == NI - 1) {
+          x[i] = read(na, xat, i);
+          sx[i] = nsx[i] >> sh;
+        }
+      }
+      fence();
     }
+    sw = nsw >> sh;
+  };
+
+  load_scales(0);
+#pragma unroll
+  for (int q = 0; q < 3; ++q) load_part(q, 0, as0, bs0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  fence();
+#pragma unroll
+  for (int q = 0; q < 3; ++q) load_part(q, 1, as1, bs1);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    x[i] = read(as0, xat, i);
+    sx[i] = read_sx(0, i);
+  }
+  sw = read_sw(0);
+#pragma unroll
+  for (int j = 0; j < 3; ++j) w[j] = read(bs0, wat, j);
+  fence();
+  for (int step = 0; step < steps; step += 2) {
+    body(step, as0, bs0, as1, bs1);
+    body(step + 1, as1, bs1, as0, bs0);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // loads past the end drained
+
+  const bool vec = (N & 3) == 0 && ((uintptr_t)Y & 7) == 0;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t m = m0 + xrow + 16 * i;
+    if (m >= M) continue;
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+      store4(Y + m * N, n0 + wn * 16 * NI + 16 * j + 4 * h, N, acc[i][j], vec);
   }
 }
 
@@ -160,6 +383,15 @@ hipError_t split(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const 
   return hipGetLastError();
 }
 
+template <int MI, int NI>
+hipError_t tile(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const uint8_t* SW,
+                uint16_t* Y, int64_t M, int64_t N, int64_t K, hipStream_t st) {
+  const int64_t tiles = ((M + 32 * MI - 1) / (32 * MI)) * ((N + 32 * NI - 1) / (32 * NI));
+  hipLaunchKernelGGL((k_w8_tile<MI, NI>), dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256), 0, st,
+                     X8, SX, W8, SW, Y, (int)M, (int)N, (int)K);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 int64_t w8_gemm_threads(int64_t M, int64_t N, int64_t K) {
@@ -172,7 +404,9 @@ hipError_t launch_w8_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W
   const Grouped none = {};
   if (M <= 16) return split<1, 2, 8, false>(X8, SX, W8, SW, Y, M, N, K, 1, none, st);
   if (M <= 32) return split<2, 2, 8, false>(X8, SX, W8, SW, Y, M, N, K, 1, none, st);
-  return split<4, 2, 8, false>(X8, SX, W8, SW, Y, M, N, K, (M + 63) / 64, none, st);
+  if (M <= 256) return split<4, 2, 8, false>(X8, SX, W8, SW, Y, M, N, K, (M + 63) / 64, none, st);
+  if (M <= 512) return tile<4, 4>(X8, SX, W8, SW, Y, M, N, K, st);
+  return tile<8, 8>(X8, SX, W8, SW, Y, M, N, K, st);
 }
 
 int64_t w8_moe_threads(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B) {
