@@ -162,14 +162,17 @@ __global__ __launch_bounds__(NW * 64) void k_w8_split(const uint8_t* __restrict_
 // step, two stages; a row's eight 16-byte pieces are stored XOR-swizzled by
 // (row / 2) % 8, so that an operand read of 16 rows spreads over the banks.
 //
-// One barrier per step.  A wave holds all MI operand tiles of X and four of W:
-// while tile j of W multiplies, tile j + 3 is read.  Three W tiles before the
-// end of a step the waves meet: the next stage has landed and everyone has read
-// the last of this one, so its buffer takes the loads of two steps ahead,
-// spread over the step's last MFMAs, and each X tile is replaced by the next
-// step's right after its last use.  The loads have most of a step to land and
-// no MFMA waits for the start of a step.  An odd number of steps is made even
-// by one of zeros (pieces past K read zero).
+// A step multiplies four quarters, (X low, W low), (X low, W high), (X high,
+// W high), (X high, W low), so that a wave needs its operands once and four at a
+// time: the halves for the next quarter, at last the next step's low halves,
+// are read during the one before, into registers whose half is done (W's two
+// sets swap roles every step).  LDS reads are spread evenly over the MFMAs that
+// way, eight per sixteen; reading all of X at the end of a step kept the LDS
+// busy twice as long as the MFMAs of that time (8192^3: 464 us).  After the
+// second quarter the waves meet, once a step: the next stage has landed and
+// everyone has read this one, so its buffer takes the loads of two steps ahead,
+// which have three quarters of a step to a whole one to land.  An odd number of
+// steps is made even by one of zeros (pieces past K read zero).
 //
 // The scales of four K blocks are one dword a row; they pass through a small
 // LDS ring the same way.
@@ -249,18 +252,17 @@ __global__ __launch_bounds__(256, 1) void k_w8_tile(const uint8_t* __restrict__ 
   const uint32_t sxoff = srow < rows_x ? (uint32_t)(srow * cols) : kOOB;
   const uint32_t swoff = lane < 2 ? (uint32_t)(lane * cols) : kOOB;   // past the end: 0
 
-  // part q of 3 of a stage's loads
-  auto load_part = [&](int q, int step, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
+  // load i of a wave's XA + XB of a stage
+  auto load_one = [&](int i, int step, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
     const uint32_t k0 = (uint32_t)step * 128u;
     const int left = K - (int)k0;                  // pieces past K read zero
-#pragma unroll
-    for (int i = q * XA / 3; i < (q + 1) * XA / 3; ++i)
-      load_lds16(ar, sa + (wave * XA + i) * 1024, 16 * piece(wave * XA + i) < left ? aoff[i] : kOOB,
-                 k0);
-#pragma unroll
-    for (int i = q * XB / 3; i < (q + 1) * XB / 3; ++i)
-      load_lds16(br, sb + (wave * XB + i) * 1024, 16 * piece(wave * XB + i) < left ? boff[i] : kOOB,
-                 k0);
+    if (i < XA) {
+      const int I = wave * XA + i;
+      load_lds16(ar, sa + I * 1024, 16 * piece(I) < left ? aoff[i] : kOOB, k0);
+    } else {
+      const int I = wave * XB + i - XA;
+      load_lds16(br, sb + I * 1024, 16 * piece(I) < left ? boff[i - XA] : kOOB, k0);
+    }
   };
   auto load_scales = [&](int quad) __attribute__((always_inline)) {
     if (BM == 256 || wave < 2) load_lds4(sar, rx[quad & 1] + 64 * wave, sxoff, (uint32_t)quad * 4u);
@@ -283,7 +285,8 @@ __global__ __launch_bounds__(256, 1) void k_w8_tile(const uint8_t* __restrict__ 
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = zero;
-  i32x8 x[MI], w[4];
+  constexpr int HI = MI / 2, HJ = NI / 2;
+  i32x8 x[2][HI], w[2][HJ];
   uint32_t sx[MI], sw;
   // the dword that holds a step's scale (the added step repeats the last
   // one's), and its place in it
@@ -300,63 +303,78 @@ __global__ __launch_bounds__(256, 1) void k_w8_tile(const uint8_t* __restrict__ 
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  // one step on stage (sa, sb); (na, nb) is the next one's
-  auto body = [&](int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
+  // one quarter: rows hi of X, hj of W (in register set set); READ(i) reads
+  // operand tile i for a later quarter, LOADS calls load LOAD(i) per MFMA
+  auto quarter = [&](auto HX, auto HW, int set, auto read_one, int reads, auto load, int loads)
       __attribute__((always_inline)) {
+    constexpr int hx = decltype(HX)::value, hw = decltype(HW)::value;
+#pragma unroll
+    for (int i = 0; i < reads; ++i) read_one(i);
+#pragma unroll
+    for (int i = 0; i < loads; ++i) load(i);
+#pragma unroll
+    for (int q = 0; q < HI * HJ; ++q) {
+      // the operand that arrives last goes slowest
+      const int i = hx == 0 ? q % HI : q / HJ, j = hx == 0 ? q / HI : q % HJ;
+      f32x4& d = acc[hx * HI + i][hw * HJ + j];
+      d = mfma8_16(w[set][j], x[hx][i], d, sw, sx[hx * HI + i]);
+    }
+#pragma unroll
+    for (int q = 0; q < HI * HJ; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // one MFMA
+      if (q < 2 * reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+      if (q < loads) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);       // one load
+    }
+    fence();
+  };
+  using std::integral_constant;
+  constexpr integral_constant<int, 0> lo{};
+  constexpr integral_constant<int, 1> hi{};
+  auto none = [](int) {};
+
+  // one step on stage (sa, sb); (na, nb) is the next one's; the step's low
+  // half of W is in set S
+  auto body = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
+      __attribute__((always_inline)) {
+    constexpr int s = decltype(S)::value;
     uint32_t nsx[MI], nsw;
     const int sh = shift(step + 1);
     load_scales(step / 4 + 1);
+    quarter(lo, lo, s, [&](int i) { w[1 - s][i] = read(sb, wat, HJ + i); }, HJ, none, 0);
+    quarter(lo, hi, 1 - s, [&](int i) { x[1][i] = read(sa, xat, HI + i); }, HI, none, 0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    fence();
+    quarter(hi, hi, 1 - s, [&](int i) { x[0][i] = read(na, xat, i); }, HI,
+            [&](int i) { load_one(i, step + 2, sa, sb); }, XA + XB);
+    nsw = read_sw(step + 1);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      if (j == NI - 3) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        fence();
-      }
-      if (j < NI - 3) {
-        w[(j + 3) & 3] = read(sb, wat, j + 3);
-      } else {
-        w[(j + 3) & 3] = read(nb, wat, j + 3 - NI);
-        load_part(j - (NI - 3), step + 2, sa, sb);
-      }
-      if (j == NI - 2) {
-        nsw = read_sw(step + 1);
+    for (int i = 0; i < MI; ++i) nsx[i] = read_sx(step + 1, i);
+    quarter(hi, lo, s, [&](int i) { w[1 - s][i] = read(nb, wat, i); }, HJ, none, 0);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) nsx[i] = read_sx(step + 1, i);
-      }
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        acc[i][j] = mfma8_16(w[j & 3], x[i], acc[i][j], sw, sx[i]);
-        if (j == NI - 1) {
-          x[i] = read(na, xat, i);
-          sx[i] = nsx[i] >> sh;
-        }
-      }
-      fence();
-    }
+    for (int i = 0; i < MI; ++i) sx[i] = nsx[i] >> sh;
     sw = nsw >> sh;
   };
 
   load_scales(0);
 #pragma unroll
-  for (int q = 0; q < 3; ++q) load_part(q, 0, as0, bs0);
+  for (int i = 0; i < XA + XB; ++i) load_one(i, 0, as0, bs0);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   fence();
 #pragma unroll
-  for (int q = 0; q < 3; ++q) load_part(q, 1, as1, bs1);
+  for (int i = 0; i < XA + XB; ++i) load_one(i, 1, as1, bs1);
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    x[i] = read(as0, xat, i);
-    sx[i] = read_sx(0, i);
-  }
+  for (int i = 0; i < MI; ++i) sx[i] = read_sx(0, i);
   sw = read_sw(0);
 #pragma unroll
-  for (int j = 0; j < 3; ++j) w[j] = read(bs0, wat, j);
+  for (int i = 0; i < HI; ++i) x[0][i] = read(as0, xat, i);
+#pragma unroll
+  for (int j = 0; j < HJ; ++j) w[0][j] = read(bs0, wat, j);
   fence();
   for (int step = 0; step < steps; step += 2) {
-    body(step, as0, bs0, as1, bs1);
-    body(step + 1, as1, bs1, as0, bs0);
+    body(lo, step, as0, bs0, as1, bs1);
+    body(hi, step + 1, as1, bs1, as0, bs0);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // loads past the end drained
 
