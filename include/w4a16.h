@@ -578,9 +578,10 @@ int w8a8_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const uin
               uint16_t* Y, int64_t M, int64_t N, int64_t K, void* stream);
 
 /*
- * w8_pick_block_size -- alignment block size of the grouped W8A8 product:
- * the smallest power of two that holds the mean number of pairs per expert,
- * from 16 to 64.  0 if T < 0, k < 1 or E < 1.
+ * w8_pick_block_size -- alignment block size of the grouped W8A8 product: 16
+ * up to 8 pairs per expert on average, else the smallest of 64, 128 and 256
+ * that holds one and a half times that average (256 beyond).  0 if T < 0,
+ * k < 1 or E < 1.
  */
 int32_t w8_pick_block_size(int64_t T, int32_t k, int32_t E);
 

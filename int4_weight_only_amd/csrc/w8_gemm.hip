@@ -176,12 +176,27 @@ __global__ __launch_bounds__(NW * 64) void k_w8_split(const uint8_t* __restrict_
 //
 // The scales of four K blocks are one dword a row; they pass through a small
 // LDS ring the same way.
+//
+// KG > 1: KG such groups of four waves share the tile and split the steps
+// between them, each with stages of its own, where too few tiles would leave
+// CUs idle; their sums are joined through LDS in group order.
+// GROUPED: the rows of a tile are sorted pairs of one expert, gathered by the
+// loads.
 namespace {
 
 constexpr uint32_t kOOB = 0x80000000u;   // byte offset past any buffer: reads 0
 
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+
+// p and bytes are the same in every lane; said so, or each load would loop
+// over the resources of the lanes
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
+  const uint64_t a = (uint64_t)p;
+  const uint64_t u = (uint64_t)uniform((uint32_t)(a >> 32)) << 32 | uniform((uint32_t)a);
+  return __builtin_amdgcn_make_buffer_rsrc((void*)u, (short)0, (int)uniform((uint32_t)bytes),
+                                           0x00020000);
 }
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -197,42 +212,83 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, void* lds, u
 
 }  // namespace
 
-template <int MI, int NI>
-__global__ __launch_bounds__(256, 1) void k_w8_tile(const uint8_t* __restrict__ X8,
-                                                    const uint8_t* __restrict__ SX,
-                                                    const uint8_t* __restrict__ W8,
-                                                    const uint8_t* __restrict__ SW,
-                                                    uint16_t* __restrict__ Y, int M, int N, int K) {
+template <int MI, int NI, int KG, int NST, bool GROUPED>
+__global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restrict__ X8,
+                                                         const uint8_t* __restrict__ SX,
+                                                         const uint8_t* __restrict__ W8,
+                                                         const uint8_t* __restrict__ SW,
+                                                         uint16_t* __restrict__ Y, int64_t M,
+                                                         int64_t N, int K, Grouped gr) {
   constexpr int BM = 32 * MI, BN = 32 * NI;
   constexpr int XA = BM / 32, XB = BN / 32;        // 1 KB loads per wave and stage
-  static_assert(NI == 4 || NI == 8, "a wave's rows of W share a scale, four W tiles in flight");
-  static_assert(MI == 4 || MI == 8, "scale ring");
-  __shared__ __attribute__((aligned(16))) uint8_t as0[BM * 128], as1[BM * 128];
-  __shared__ __attribute__((aligned(16))) uint8_t bs0[BN * 128], bs1[BN * 128];
-  __shared__ __attribute__((aligned(16))) uint32_t rx[2][256], rw[2][64];
+  static_assert(MI % 2 == 0 && NI % 2 == 0 && MI <= 8 && NI <= 8, "halves; one scale of W a wave");
+  static_assert(NST == 2 || NST == 4, "stages");
+  // each stage an object of its own: the compiler then knows which loads an
+  // operand read has to wait for
+  constexpr int SA = BM * 128, SB = BN * 128, S4 = NST == 4;
+  __shared__ __attribute__((aligned(16))) uint8_t as0_[KG][SA], as1_[KG][SA];
+  __shared__ __attribute__((aligned(16))) uint8_t bs0_[KG][SB], bs1_[KG][SB];
+  __shared__ __attribute__((aligned(16))) uint8_t as2_[KG][S4 ? SA : 16], as3_[KG][S4 ? SA : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t bs2_[KG][S4 ? SB : 16], bs3_[KG][S4 ? SB : 16];
+  __shared__ __attribute__((aligned(16))) uint32_t rx_[KG][2][256], rw_[KG][2][64];
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
   const int wm = wave >> 1, wn = wave & 1;
   const int r16 = lane & 15, h = lane >> 4;
+  uint8_t* const as0 = as0_[kg];
+  uint8_t* const as1 = as1_[kg];
+  uint8_t* const as2 = as2_[kg];
+  uint8_t* const as3 = as3_[kg];
+  uint8_t* const bs0 = bs0_[kg];
+  uint8_t* const bs1 = bs1_[kg];
+  uint8_t* const bs2 = bs2_[kg];
+  uint8_t* const bs3 = bs3_[kg];
+  auto& rx = rx_[kg];
+  auto& rw = rw_[kg];
   // tile order: XCD x (workgroups round-robin over 8) walks a contiguous
   // range of tiles in groups of 8 row blocks of X, which share operands in
   // its L2
-  const int mt = (M + BM - 1) / BM, nt = (N + BN - 1) / BN;
-  const int tiles = mt * nt, per = (tiles + 7) / 8;
-  const int t = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-  if (t >= tiles || (int)(blockIdx.x / 8) >= per) return;
-  const int group = t / (8 * nt), gm = min(8, mt - group * 8), in_group = t - group * 8 * nt;
-  const int64_t m0 = (int64_t)(group * 8 + in_group % gm) * BM, n0 = (int64_t)(in_group / gm) * BN;
+  if constexpr (GROUPED) M = min(M, (int64_t)gr.ntpp[0]);
+  const int64_t mt = (M + BM - 1) / BM, nt = (N + BN - 1) / BN;
+  const int64_t tiles = mt * nt, per = (tiles + 7) / 8;
+  const int64_t t = (blockIdx.x % 8) * per + blockIdx.x / 8;
+  if (t >= tiles || blockIdx.x / 8 >= per) return;
+  const int64_t band = t / (8 * nt), in_band = t - band * 8 * nt;
+  const int gm = (int)min((int64_t)8, mt - band * 8);
+  const int64_t m0 = (band * 8 + in_band % gm) * BM, n0 = in_band / gm * BN;
 
   const int cols = (int)w8_cols(K);
   const int steps = (K + 127) / 128;
-  const int rows_x = (int)min((int64_t)BM, M - m0), rows_w = (int)min((int64_t)BN, N - n0);
-  const __amdgpu_buffer_rsrc_t ar = rsrc(X8 + m0 * K, (int64_t)rows_x * K);
+  // this group's steps, a multiple of the stages for every group (those past
+  // its own part of K are zeros)
+  const int share = ((steps + KG - 1) / KG + NST - 1) / NST * NST;
+  const int first = kg * share, last = first + share;
+  const int k_end = min(K, last * 128);
+  if constexpr (GROUPED) {
+    const int e = gr.expert_ids[m0 / gr.B];
+    if (e < 0 || e >= gr.E || (uint32_t)gr.sorted_ids[m0] >= (uint32_t)gr.P) return;
+    W8 += (int64_t)e * N * K;
+    SW += (int64_t)e * w8_blocks(N) * cols;
+  }
+  const int rows_x = GROUPED ? BM : (int)min((int64_t)BM, M - m0);
+  const int rows_w = (int)min((int64_t)BN, N - n0);
+  const int64_t x0 = GROUPED ? 0 : m0, all_x = GROUPED ? gr.P / gr.div : rows_x;
+  const __amdgpu_buffer_rsrc_t ar = rsrc(X8 + x0 * K, all_x * K);
   const __amdgpu_buffer_rsrc_t br = rsrc(W8 + n0 * K, (int64_t)rows_w * K);
-  const __amdgpu_buffer_rsrc_t sar = rsrc(SX + m0 * cols, (int64_t)rows_x * cols);
+  const __amdgpu_buffer_rsrc_t sar = rsrc(SX + x0 * cols, all_x * cols);
   const __amdgpu_buffer_rsrc_t sbr =
       rsrc(SW + (n0 >> 7) * cols, (((n0 + rows_w - 1) >> 7) - (n0 >> 7) + 1) * cols);
+  // row of X, from x0, that tile row r stands for; -1: none
+  auto x_row = [&](int r) {
+    if constexpr (GROUPED) {
+      const int f = gr.sorted_ids[m0 + r];
+      return (uint32_t)f < (uint32_t)gr.P ? f / gr.div : -1;
+    } else {
+      return r < rows_x ? r : -1;
+    }
+  };
 
   // load I of a stage fills its rows 8 I .. 8 I + 7: lane l writes slot l % 8
   // of row l / 8, which holds piece (l % 8) ^ ((row / 2) % 8)
@@ -240,22 +296,23 @@ __global__ __launch_bounds__(256, 1) void k_w8_tile(const uint8_t* __restrict__ 
   uint32_t aoff[XA], boff[XB];
 #pragma unroll
   for (int i = 0; i < XA; ++i) {
-    const int I = wave * XA + i, r = 8 * I + (lane >> 3);
-    aoff[i] = r < rows_x ? (uint32_t)r * (uint32_t)K + 16u * piece(I) : kOOB;
+    const int I = wave * XA + i, r = x_row(8 * I + (lane >> 3));
+    aoff[i] = r >= 0 ? (uint32_t)r * (uint32_t)K + 16u * piece(I) : kOOB;
   }
 #pragma unroll
   for (int i = 0; i < XB; ++i) {
     const int I = wave * XB + i, r = 8 * I + (lane >> 3);
     boff[i] = r < rows_w ? (uint32_t)r * (uint32_t)K + 16u * piece(I) : kOOB;
   }
-  const int srow = 64 * wave + lane;               // row of the scale ring this lane fills
-  const uint32_t sxoff = srow < rows_x ? (uint32_t)(srow * cols) : kOOB;
+  // row of the scale ring this lane fills
+  const int srow = 64 * wave < BM ? x_row(64 * wave + lane) : -1;
+  const uint32_t sxoff = srow >= 0 ? (uint32_t)(srow * cols) : kOOB;
   const uint32_t swoff = lane < 2 ? (uint32_t)(lane * cols) : kOOB;   // past the end: 0
 
   // load i of a wave's XA + XB of a stage
   auto load_one = [&](int i, int step, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
     const uint32_t k0 = (uint32_t)step * 128u;
-    const int left = K - (int)k0;                  // pieces past K read zero
+    const int left = k_end - (int)k0;              // pieces past the end read zero
     if (i < XA) {
       const int I = wave * XA + i;
       load_lds16(ar, sa + I * 1024, 16 * piece(I) < left ? aoff[i] : kOOB, k0);
@@ -265,7 +322,7 @@ __global__ __launch_bounds__(256, 1) void k_w8_tile(const uint8_t* __restrict__ 
     }
   };
   auto load_scales = [&](int quad) __attribute__((always_inline)) {
-    if (BM == 256 || wave < 2) load_lds4(sar, rx[quad & 1] + 64 * wave, sxoff, (uint32_t)quad * 4u);
+    load_lds4(sar, rx[quad & 1] + 64 * wave, sxoff, (uint32_t)quad * 4u);
     load_lds4(sbr, rw[quad & 1], swoff, (uint32_t)quad * 4u);   // by every wave, the same bytes
   };
   // operand tile i of a wave's rows (16 rows keep the swizzle of the first)
@@ -285,7 +342,10 @@ __global__ __launch_bounds__(256, 1) void k_w8_tile(const uint8_t* __restrict__ 
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = zero;
-  constexpr int HI = MI / 2, HJ = NI / 2;
+  // small tiles hold two steps' operands (WHOLE), large ones halves
+  constexpr bool WHOLE = MI + NI <= 8;
+  static_assert(NST == (WHOLE ? 4 : 2), "stages of the two schedules");
+  constexpr int HI = WHOLE ? MI : MI / 2, HJ = WHOLE ? NI : NI / 2;
   i32x8 x[2][HI], w[2][HJ];
   uint32_t sx[MI], sw;
   // the dword that holds a step's scale (the added step repeats the last
@@ -332,21 +392,60 @@ __global__ __launch_bounds__(256, 1) void k_w8_tile(const uint8_t* __restrict__ 
   constexpr integral_constant<int, 1> hi{};
   auto none = [](int) {};
 
+  // small tiles, one step: its operands are in set S; the next one's are read
+  // into the other while they multiply
+  auto body_whole = [&](auto Q, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
+      __attribute__((always_inline)) {
+    constexpr int q = decltype(Q)::value, s = q & 1;
+    uint32_t nsx[MI], nsw;
+    const int sh = shift(step + 1);
+    // the loads of the two steps after the next may be in flight (the scales
+    // came with the quad's first step)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NST - 2) * (XA + XB) + (q == 1 || q == 2 ? 2 : 0))
+                 : "memory");
+    __builtin_amdgcn_s_barrier();
+    fence();
+    if (q == 0) load_scales(step / 4 + 1);
+    nsw = read_sw(step + 1);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) nsx[i] = read_sx(step + 1, i);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) w[1 - s][j] = read(nb, wat, j);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) x[1 - s][i] = read(na, xat, i);
+    fence();
+#pragma unroll
+    for (int i = 0; i < XA + XB; ++i) load_one(i, step + NST, sa, sb);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] = mfma8_16(w[s][j], x[s][i], acc[i][j], sw, sx[i]);
+#pragma unroll
+    for (int q = 0; q < MI * NI; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                    // one MFMA
+      if (q < XA + XB) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // one load
+    }
+    fence();
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sx[i] = nsx[i] >> sh;
+    sw = nsw >> sh;
+  };
+
   // one step on stage (sa, sb); (na, nb) is the next one's; the step's low
   // half of W is in set S
-  auto body = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
+  auto body_halves = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
       __attribute__((always_inline)) {
     constexpr int s = decltype(S)::value;
     uint32_t nsx[MI], nsw;
     const int sh = shift(step + 1);
-    load_scales(step / 4 + 1);
     quarter(lo, lo, s, [&](int i) { w[1 - s][i] = read(sb, wat, HJ + i); }, HJ, none, 0);
     quarter(lo, hi, 1 - s, [&](int i) { x[1][i] = read(sa, xat, HI + i); }, HI, none, 0);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     fence();
+    load_scales((step + 1) / 4 + 1);
     quarter(hi, hi, 1 - s, [&](int i) { x[0][i] = read(na, xat, i); }, HI,
-            [&](int i) { load_one(i, step + 2, sa, sb); }, XA + XB);
+            [&](int i) { load_one(i, step + NST, sa, sb); }, XA + XB);
     nsw = read_sw(step + 1);
 #pragma unroll
     for (int i = 0; i < MI; ++i) nsx[i] = read_sx(step + 1, i);
@@ -356,36 +455,75 @@ __global__ __launch_bounds__(256, 1) void k_w8_tile(const uint8_t* __restrict__ 
     sw = nsw >> sh;
   };
 
-  load_scales(0);
+  // (the scales of the first two quads, some of them more than once)
+  auto load_stage = [&](int step, int quad, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
+    load_scales(quad);
 #pragma unroll
-  for (int i = 0; i < XA + XB; ++i) load_one(i, 0, as0, bs0);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (int i = 0; i < XA + XB; ++i) load_one(i, step, sa, sb);
+  };
+  load_stage(first, first / 4, as0, bs0);
+  load_stage(first + 1, first / 4 + 1, as1, bs1);
+  if constexpr (NST == 4) {
+    load_stage(first + 2, first / 4 + 1, as2, bs2);
+    load_stage(first + 3, first / 4 + 1, as3, bs3);
+  }
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 1) * (XA + XB + 2)) : "memory");
   __builtin_amdgcn_s_barrier();
   fence();
 #pragma unroll
-  for (int i = 0; i < XA + XB; ++i) load_one(i, 1, as1, bs1);
-#pragma unroll
-  for (int i = 0; i < MI; ++i) sx[i] = read_sx(0, i);
-  sw = read_sw(0);
+  for (int i = 0; i < MI; ++i) sx[i] = read_sx(first, i) >> shift(first);
+  sw = read_sw(first) >> shift(first);
 #pragma unroll
   for (int i = 0; i < HI; ++i) x[0][i] = read(as0, xat, i);
 #pragma unroll
   for (int j = 0; j < HJ; ++j) w[0][j] = read(bs0, wat, j);
   fence();
-  for (int step = 0; step < steps; step += 2) {
-    body(lo, step, as0, bs0, as1, bs1);
-    body(hi, step + 1, as1, bs1, as0, bs0);
+  for (int step = first; step < last; step += NST) {
+    if constexpr (WHOLE) {
+      body_whole(lo, step, as0, bs0, as1, bs1);
+      body_whole(hi, step + 1, as1, bs1, as2, bs2);
+      body_whole(integral_constant<int, 2>{}, step + 2, as2, bs2, as3, bs3);
+      body_whole(integral_constant<int, 3>{}, step + 3, as3, bs3, as0, bs0);
+    } else {
+      body_halves(lo, step, as0, bs0, as1, bs1);
+      body_halves(hi, step + 1, as1, bs1, as0, bs0);
+    }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // loads past the end drained
 
+  if constexpr (KG > 1) {
+    // one column of tiles per round through the stages that are done with
+    f32x4(*part)[4][MI][64] = (f32x4(*)[4][MI][64])as0_;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      __syncthreads();
+      if (kg > 0) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) part[kg][wave][i][lane] = acc[i][j];
+      }
+      __syncthreads();
+      if (kg == 0) {
+#pragma unroll
+        for (int g = 1; g < KG; ++g)
+#pragma unroll
+          for (int i = 0; i < MI; ++i) acc[i][j] += part[g][wave][i][lane];
+      }
+    }
+    if (kg > 0) return;
+  }
   const bool vec = (N & 3) == 0 && ((uintptr_t)Y & 7) == 0;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int64_t m = m0 + xrow + 16 * i;
-    if (m >= M) continue;
+    int64_t row = m0 + xrow + 16 * i;
+    if constexpr (GROUPED) {
+      row = gr.sorted_ids[row];
+      if ((uint32_t)row >= (uint32_t)gr.P) continue;
+    } else if (row >= M) {
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < NI; ++j)
-      store4(Y + m * N, n0 + wn * 16 * NI + 16 * j + 4 * h, N, acc[i][j], vec);
+      store4(Y + row * N, n0 + wn * 16 * NI + 16 * j + 4 * h, N, acc[i][j], vec);
   }
 }
 
@@ -401,34 +539,95 @@ hipError_t split(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const 
   return hipGetLastError();
 }
 
-template <int MI, int NI>
+template <int MI, int NI, int KG, int NST, bool GROUPED>
 hipError_t tile(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const uint8_t* SW,
-                uint16_t* Y, int64_t M, int64_t N, int64_t K, hipStream_t st) {
+                uint16_t* Y, int64_t M, int64_t N, int64_t K, const Grouped& gr, hipStream_t st) {
   const int64_t tiles = ((M + 32 * MI - 1) / (32 * MI)) * ((N + 32 * NI - 1) / (32 * NI));
-  hipLaunchKernelGGL((k_w8_tile<MI, NI>), dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256), 0, st,
-                     X8, SX, W8, SW, Y, (int)M, (int)N, (int)K);
+  hipLaunchKernelGGL((k_w8_tile<MI, NI, KG, NST, GROUPED>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                     dim3(256 * KG), 0, st, X8, SX, W8, SW, Y, M, N, (int)K, gr);
   return hipGetLastError();
+}
+
+// The tiles and what they cost: a round of one workgroup per CU takes
+// `step_us` per 128-wide step and `fixed_us` besides (launch, first loads,
+// stores), measured with every CU busy and operands that come from memory.
+struct TileKind {
+  int bm, bn, kg;
+  float step_us, fixed_us;
+};
+constexpr TileKind kTiles[] = {
+    {64, 64, 2, 0.32f, 6.0f},
+    {64, 128, 1, 0.40f, 6.0f},
+    {128, 128, 1, 0.60f, 6.0f},
+    {256, 256, 1, 1.45f, 12.0f},
+};
+
+int64_t tiles_of(const TileKind& t, int64_t M, int64_t N) {
+  return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+}
+
+// The tile that the estimate says is done first.  Few large tiles move the
+// least data, but leave CUs idle where they are too few: 4096 x 14336 x 4096
+// takes 233 us in 896 tiles of 256 x 256 and 354 us in 3584 of 128 x 128;
+// 1024 x 4096 x 4096 takes 51 us in 64 of the former and 24 us in 256 of the
+// latter.
+int pick_tile(int64_t M, int64_t N, int64_t K) {
+  const int64_t steps = (K + 127) / 128, cus = cu_count();
+  int best = 0;
+  float best_us = 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    const TileKind& t = kTiles[i];
+    const int64_t rounds = (tiles_of(t, M, N) + cus - 1) / cus;
+    const float us = (float)rounds * ((float)((steps + t.kg - 1) / t.kg) * t.step_us + t.fixed_us);
+    if (i == 0 || us < best_us) {
+      best = i;
+      best_us = us;
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 int64_t w8_gemm_threads(int64_t M, int64_t N, int64_t K) {
-  return ((M + 63) / 64) * ((N + 31) / 32) * 512;
+  if (M <= 16) return (N + 15) / 16 * 1024;
+  const TileKind& t = kTiles[pick_tile(M, N, K)];
+  return (tiles_of(t, M, N) + 7) * 256 * t.kg;
 }
 
 hipError_t launch_w8_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
                           const uint8_t* SW, uint16_t* Y, int64_t M, int64_t N, int64_t K,
                           hipStream_t st) {
   const Grouped none = {};
-  if (M <= 16) return split<1, 2, 8, false>(X8, SX, W8, SW, Y, M, N, K, 1, none, st);
-  if (M <= 32) return split<2, 2, 8, false>(X8, SX, W8, SW, Y, M, N, K, 1, none, st);
-  if (M <= 256) return split<4, 2, 8, false>(X8, SX, W8, SW, Y, M, N, K, (M + 63) / 64, none, st);
-  if (M <= 512) return tile<4, 4>(X8, SX, W8, SW, Y, M, N, K, st);
-  return tile<8, 8>(X8, SX, W8, SW, Y, M, N, K, st);
+  if (M <= 16) return split<1, 1, 16, false>(X8, SX, W8, SW, Y, M, N, K, 1, none, st);
+  switch (pick_tile(M, N, K)) {
+    case 0: return tile<2, 2, 2, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
+    case 1: return tile<2, 4, 1, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
+    case 2: return tile<4, 4, 1, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
+    default: return tile<8, 8, 1, 2, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
+  }
 }
 
+namespace {
+
+int64_t moe_rows(int64_t T, int32_t k, int32_t E, int32_t B) {
+  return (T * k + (int64_t)E * (B - 1) + B - 1) / B * B;
+}
+
+// Rows of the grouped product's tiles: a divisor of B.  The tiles gather with
+// 32-bit offsets into X; where X is larger, the split kernel (64-bit
+// addresses) takes the blocks 16 rows at a time.
+int moe_tile_rows(int64_t rows_x, int64_t K, int32_t B) {
+  if (rows_x * K >= (int64_t)kOOB) return 16;
+  for (int bm = 256; bm >= 64; bm /= 2)
+    if (B % bm == 0) return bm;
+  return B % 32 == 0 ? 32 : 16;
+}
+
+}  // namespace
+
 int64_t w8_moe_threads(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B) {
-  return (T * k + (int64_t)E * (B - 1) + 15) / 16 * ((N + 31) / 32) * 256;
+  return moe_rows(T, k, E, B) / 16 * ((N + 31) / 32) * 256;
 }
 
 hipError_t launch_w8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
@@ -437,12 +636,14 @@ hipError_t launch_w8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_
                               int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B,
                               int32_t x_row_div, hipStream_t st) {
   const Grouped gr = {sorted_ids, expert_ids, ntpp, (int)(T * k), E, B, x_row_div};
-  const int64_t cap = (T * k + (int64_t)E * (B - 1) + B - 1) / B * B;
-  if (B % 64 == 0)
-    return split<4, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 64, gr, st);
-  if (B % 32 == 0)
-    return split<2, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 32, gr, st);
-  return split<1, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 16, gr, st);
+  const int64_t cap = moe_rows(T, k, E, B);
+  switch (moe_tile_rows(T * k / x_row_div, K, B)) {
+    case 16: return split<1, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 16, gr, st);
+    case 32: return split<2, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 32, gr, st);
+    case 64: return tile<2, 4, 1, 4, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
+    case 128: return tile<4, 4, 1, 4, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
+    default: return tile<8, 8, 1, 2, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
+  }
 }
 
 }  // namespace w4

@@ -26,10 +26,10 @@ def test_scale_cols(lib):
 
 
 def test_pick_block_size(lib):
-    for T, k, E in ((1, 1, 1), (256, 8, 128), (2048, 8, 32), (0, 8, 4), (33, 2, 3), (10 ** 6, 8, 64)):
-        B = lib.w8_pick_block_size(T, k, E)
-        assert B % 16 == 0 and B & (B - 1) == 0 and 16 <= B <= 256
-        assert B == 16 or B // 2 < -(-T * k // E)
+    for T, k, E, B in ((1, 1, 1, 16), (256, 8, 128, 64), (2048, 8, 32, 256), (0, 8, 4, 16), (64, 8, 64, 16),
+                       (65, 8, 64, 64), (43, 1, 1, 128), (42, 1, 1, 64), (85, 1, 1, 128), (86, 1, 1, 256),
+                       (1 << 50, 8, 64, 256)):
+        assert lib.w8_pick_block_size(T, k, E) == B
     assert lib.w8_pick_block_size(-1, 1, 1) == lib.w8_pick_block_size(1, 0, 1) == 0
     assert lib.w8_pick_block_size(1, 1, 0) == 0
 
