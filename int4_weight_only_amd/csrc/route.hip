@@ -5,7 +5,8 @@
 // Scores, choice values, group sums and weights are held in 64 bits: two
 // choice values of a row are often closer than 32 bits of an exponential
 // tell apart (sixteen thousand rows of 384 hold several such pairs), and a
-// swapped expert is another result, not a rounding.  One wave per token.
+// swapped expert is another result, not a rounding.  Rows whose values 32 bits
+// do tell apart, nearly all, are chosen by those.  One wave per token.
 #include <cfloat>
 
 #include "w8.h"
@@ -73,7 +74,179 @@ __device__ __forceinline__ double score(float x, bool sigmoid, const RowSum& rs)
 
 }  // namespace
 
-// NPER: experts per lane; expert lane + 64 i is the lane's i-th
+// ------------------------------------------------------------- selection --
+// NPER experts per lane; expert lane + 64 i is the lane's i-th.
+// v: choice values, -Inf for masked experts.  Lane j < k gets pick j: its id, and
+// whether it is one (slots without an expert left hold the lowest untaken
+// indices).
+//
+// The quick form lets choice values from 32-bit exponentials decide where they
+// are further apart than their errors can be; where some are not, the row is
+// done again in 64 bits, where equal values also tie to the lower index.  A 32-bit score errs by less than 2.5e-7 (v_exp
+// and v_rcp, one unit in the last place each; the rounding of the exponent's
+// product counts by s (1 - s) |x| <= 0.23) and the sum with the bias by 2^-24
+// of itself; softmax scores carry the error of their sum too, at most 1.7e-6 of
+// a score for 1024 experts, and two of them add to at most one.  So two values are
+// told apart if they differ by kApart (1 + |c|), and two groups, whose worth
+// may be the sum of two values, by twice that.
+namespace {
+
+constexpr float kApart = 2e-6f;
+
+__device__ __forceinline__ float wave_max_of(float a) {
+  const auto x = [](int v, int w) { return fmaxf(__int_as_float(v), __int_as_float(w)); };
+  a = x(__float_as_int(a), __builtin_amdgcn_mov_dpp(__float_as_int(a), 0xB1, 0xF, 0xF, false));
+  a = x(__float_as_int(a), __builtin_amdgcn_mov_dpp(__float_as_int(a), 0x4E, 0xF, 0xF, false));
+  a = x(__float_as_int(a), __builtin_amdgcn_mov_dpp(__float_as_int(a), 0x141, 0xF, 0xF, false));
+  a = x(__float_as_int(a), __builtin_amdgcn_mov_dpp(__float_as_int(a), 0x140, 0xF, 0xF, false));
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(a), false, false);
+  a = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(a), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ double wave_max_of(double a) { return wave_max64(a); }
+
+// the value of one lane, the same one for the whole wave
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Groups that stay, as a mask of groups; also whether that is certain.
+// `mine`: the row's choice values in LDS.  2^n lanes share a group.
+template <class F>
+__device__ __forceinline__ uint64_t kept_groups(const F* mine, int E, const RouteRule& rule, int lane,
+                                                bool& sure) {
+  const F none = (F)-INFINITY;
+  const int per = E / rule.groups;
+  int share = 1;
+  while (2 * share * rule.groups <= 64) share *= 2;
+  const int g = lane / share;
+  F a = none, b = none;                        // the two largest
+  if (g < rule.groups)
+    for (int q = lane % share; q < per; q += share) {
+      const F v = mine[g * per + q];
+      b = max(b, min(a, v));
+      a = max(a, v);
+    }
+  for (int d = 1; d < share; d *= 2) {
+    const F a2 = __shfl_xor(a, d), b2 = __shfl_xor(b, d);
+    b = max(max(b, b2), min(a, a2));
+    a = max(a, a2);
+  }
+  F worth = rule.group_top == 2 && b > none ? a + b : a;
+  worth = __shfl(worth, (lane * share) & 63);  // lane g: group g
+  int rank = 0;
+  for (int o = 0; o < rule.groups; ++o) {
+    const F other = lane_value(worth, o);
+    rank += other > worth || (other == worth && o < lane);
+  }
+  const bool group = lane < rule.groups;
+  if (sizeof(F) == 4 && rule.topk_groups < rule.groups) {
+    // the worth of the last that stays and of the first that goes
+    const uint64_t last = __ballot(group && rank == rule.topk_groups - 1);
+    const uint64_t next = __ballot(group && rank == rule.topk_groups);
+    const F in = lane_value(worth, (int)__builtin_ctzll(last));
+    const F out = lane_value(worth, (int)__builtin_ctzll(next));
+    if (out > none && !(in - out > (F)(2 * kApart) * (1 + fabs(in) + fabs(out)))) sure = false;
+  }
+  return __ballot(group && rank < rule.topk_groups);
+}
+
+// Masks the experts of the groups that go; whether that is certain.
+template <int NPER, class F>
+__device__ __forceinline__ bool limit_to_groups(F (&v)[NPER], F* mine, int E, const RouteRule& rule,
+                                                int lane) {
+  if (rule.groups == 1) return true;
+  bool sure = true;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i)
+    if (lane + 64 * i < E) mine[lane + 64 * i] = v[i];
+  __builtin_amdgcn_wave_barrier();             // the wave's own LDS, in order
+  const uint64_t keep = kept_groups(mine, E, rule, lane, sure);
+  __builtin_amdgcn_wave_barrier();
+  // e / per as a product: exact for e, per <= 1024
+  const uint32_t m = ((1u << 20) + E / rule.groups - 1) / (E / rule.groups);
+#pragma unroll
+  for (int i = 0; i < NPER; ++i)
+    if (!((keep >> (((lane + 64 * i) * m) >> 20 & 63)) & 1)) v[i] = (F)-INFINITY;
+  return sure;
+}
+
+// The quick form: false where values are too close or the masks leave fewer
+// than k experts.
+template <int NPER>
+__device__ __forceinline__ bool choose(float (&v)[NPER], float* mine, int E, int k,
+                                       const RouteRule& rule, int lane, int& my_id) {
+  if (!limit_to_groups<NPER, float>(v, mine, E, rule, lane)) return false;
+  float my_value = -INFINITY;
+  // one round more than picks: the first that stays out has to be apart too
+  for (int j = 0; j <= k; ++j) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < NPER; ++i) m = fmaxf(m, v[i]);
+    const float local = m;
+    m = wave_max_of(m);
+    const int w = (int)__builtin_ctzll(__ballot(local == m));
+    // one expert goes: an equal one stays, and shows as too close a call
+    int at = lane == w ? -1 : 0;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      const bool hit = at < 0 && v[i] == m;
+      at = hit ? 64 * i : at;
+      v[i] = hit ? -INFINITY : v[i];
+    }
+    const int win = __builtin_amdgcn_readlane(at, w) + w;
+    my_id = lane == j ? win : my_id;
+    my_value = lane == j ? m : my_value;
+  }
+  const float next = __shfl_down(my_value, 1);
+  const bool apart = next == -INFINITY
+                         ? lane == k - 1 && my_value > -INFINITY    // none left to be close to
+                         : my_value - next > kApart * (1.0f + fabsf(my_value) + fabsf(next));
+  return __ballot(lane < k && !apart) == 0;
+}
+
+template <int NPER>
+__device__ __forceinline__ void choose_exactly(double (&v)[NPER], double* mine, int E, int k,
+                                               const RouteRule& rule, int lane, int& my_id,
+                                               bool& my_live) {
+  limit_to_groups<NPER, double>(v, mine, E, rule, lane);
+  uint32_t free = 0;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) free |= lane + 64 * i < E ? 1u << i : 0u;
+  for (int j = 0; j < k; ++j) {
+    double m = v[0];
+#pragma unroll
+    for (int i = 1; i < NPER; ++i) m = fmax(m, v[i]);
+    m = wave_max64(m);
+    const bool any = m > -INFINITY;
+    int win = -1;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      const uint64_t b = __ballot(any ? v[i] == m : (free >> i) & 1u);
+      if (win < 0 && b) win = 64 * i + (int)__builtin_ctzll(b);
+    }
+#pragma unroll
+    for (int i = 0; i < NPER; ++i)
+      if (win == lane + 64 * i) {
+        v[i] = -INFINITY;
+        free &= ~(1u << i);
+      }
+    if (lane == j) {
+      my_id = win;
+      my_live = any;
+    }
+  }
+}
+
+}  // namespace
+
 template <int NPER>
 __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ logits,
                                                       const float* __restrict__ bias, int T, int E,
@@ -85,77 +258,58 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
   const int t = blockIdx.x * 4 + wave;
   if (t >= T) return;                          // whole waves; no barrier below
   const float* row = logits + (int64_t)t * E;
-  float x[NPER];
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) x[i] = lane + 64 * i < E ? row[lane + 64 * i] : -INFINITY;
-  RowSum rs = {0.0, 1.0};
-  if (!rule.sigmoid) rs = row_sum<NPER>(x, E, lane);
-  double c[NPER];
-  uint32_t live = 0, free = 0;
+  double* mine = choice + (int64_t)wave * E;
+  float x[NPER], add[NPER];
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
     const int e = lane + 64 * i;
-    c[i] = -INFINITY;
-    if (e >= E) continue;
-    free |= 1u << i;
-    const double v = score(x[i], rule.sigmoid, rs) + (bias ? (double)bias[e] : 0.0);
-    if (!masked(x[i]) && v > -INFINITY) {      // a NaN bias masks too
-      c[i] = v;
-      live |= 1u << i;
-    }
-  }
-  if (rule.groups > 1) {
-    // lane g values group g; then its rank among the groups (ties to the
-    // lower index) decides whether its experts stay
-    double* mine = choice + (int64_t)wave * E;
-#pragma unroll
-    for (int i = 0; i < NPER; ++i)
-      if (lane + 64 * i < E) mine[lane + 64 * i] = c[i];
-    __builtin_amdgcn_wave_barrier();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    const int per = E / rule.groups;
-    double a = -INFINITY, b = -INFINITY;       // the two largest
-    if (lane < rule.groups)
-      for (int q = 0; q < per; ++q) {
-        const double v = mine[lane * per + q];
-        b = fmax(b, fmin(a, v));
-        a = fmax(a, v);
-      }
-    const double value = rule.group_top == 2 && b > -INFINITY ? a + b : a;
-    int rank = 0;
-    for (int g = 0; g < rule.groups; ++g) {
-      const double other = __shfl(value, g);
-      rank += other > value || (other == value && g < lane);
-    }
-    const uint64_t keep = __ballot(lane < rule.groups && rank < rule.topk_groups);
-#pragma unroll
-    for (int i = 0; i < NPER; ++i)
-      if (!((keep >> ((lane + 64 * i) / per)) & 1)) live &= ~(1u << i);
+    x[i] = e < E ? row[e] : -INFINITY;
+    add[i] = bias && e < E ? bias[e] : 0.0f;
+    // masked: by its logit or its bias
+    if (masked(x[i]) || masked(add[i])) add[i] = -INFINITY;
   }
   int my_id = 0;
-  bool my_live = false;
-  for (int j = 0; j < k; ++j) {
-    double m = -INFINITY;
+  bool my_live = false, sure;
+  {
+    float c[NPER], sum = 1.0f, top = 0.0f;
+    if (!rule.sigmoid) {
+      top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NPER; ++i)
-      if ((live >> i) & 1u) m = fmax(m, c[i]);
-    m = wave_max64(m);
-    const bool any = m > -INFINITY;
-    int win = -1;
+      for (int i = 0; i < NPER; ++i)
+        if (!masked(x[i])) top = fmaxf(top, fminf(x[i], FLT_MAX));
+      top = wave_max_of(top);
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NPER; ++i)
+        if (!masked(x[i])) sum += __expf(fminf(x[i], FLT_MAX) - top);
+      for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+    }
 #pragma unroll
     for (int i = 0; i < NPER; ++i) {
-      // no live expert left: the lowest index that no slot has taken
-      const uint64_t b = __ballot(any ? ((live >> i) & 1u) && c[i] == m : (free >> i) & 1u);
-      if (win < 0 && b) win = 64 * i + (int)__builtin_ctzll(b);
+      const float y = fminf(x[i], FLT_MAX);
+      const float s = rule.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-y))
+                                   : __expf(y - top) * __builtin_amdgcn_rcpf(sum);
+      c[i] = masked(add[i]) ? -INFINITY : s + add[i];
     }
-    if (lane == (win & 63)) {
-      live &= ~(1u << (win >> 6));
-      free &= ~(1u << (win >> 6));
+    sure = choose<NPER>(c, (float*)mine, E, k, rule, lane, my_id);
+    my_live = sure;
+  }
+  RowSum rs = {0.0, 1.0};
+  if (!rule.sigmoid) {
+    if (!sure || !rule.renorm) {
+      rs = row_sum<NPER>(x, E, lane);
+    } else {
+      // renormalised: the picks' own largest logit will do
+      const float y = lane < k && my_live ? fminf(row[my_id], FLT_MAX) : -INFINITY;
+      rs.top = (double)wave_max_of(y);
     }
-    if (lane == j) {
-      my_id = win;
-      my_live = any;
-    }
+  }
+  if (!sure) {
+    double c[NPER];
+#pragma unroll
+    for (int i = 0; i < NPER; ++i)
+      c[i] = masked(add[i]) ? -INFINITY : score(x[i], rule.sigmoid, rs) + (double)add[i];
+    choose_exactly<NPER>(c, mine, E, k, rule, lane, my_id, my_live);
   }
   double s = 0.0;
   if (lane < k && my_live) s = score(row[my_id], rule.sigmoid, rs);
@@ -169,8 +323,10 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
   }
 }
 
-// Gradient: p over the picks (slots whose weight is zero took no part), then
-// every expert sums the slots that name it, in slot order.
+// -------------------------------------------------------------- gradient --
+// p over the picks (slots whose weight is zero took no part); the row is put
+// together in LDS and written once.  Slots that name one expert twice add up in
+// slot order.
 template <int NPER>
 __global__ __launch_bounds__(256) void k_route_scored_bwd(const float* __restrict__ logits,
                                                           const int32_t* __restrict__ ids,
@@ -178,49 +334,68 @@ __global__ __launch_bounds__(256) void k_route_scored_bwd(const float* __restric
                                                           const float* __restrict__ dw, int T,
                                                           int E, int k, RouteRule rule,
                                                           float* __restrict__ dlogits) {
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  __shared__ __attribute__((aligned(16))) float rows[4][64 * NPER];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.x * 4 + wave;
   if (t >= T) return;
   const float* row = logits + (int64_t)t * E;
+  float* mine = rows[wave];
   const bool dense = !rule.sigmoid && !rule.renorm;   // every score moves every weight
   float x[NPER];
   RowSum rs = {0.0, 1.0};
-  if (!rule.sigmoid) {
+  if (dense) {
 #pragma unroll
     for (int i = 0; i < NPER; ++i) x[i] = lane + 64 * i < E ? row[lane + 64 * i] : -INFINITY;
     rs = row_sum<NPER>(x, E, lane);
   }
   int id = -1;
-  double s = 0.0, g = 0.0, rest = 1.0;
+  float y = -INFINITY;
+  double g = 0.0;
   if (lane < k) {
     const int e = ids[(int64_t)t * k + lane];
     if (e >= 0 && e < E && wts[(int64_t)t * k + lane] != 0.0f) {
       id = e;
-      s = score(row[e], rule.sigmoid, rs);
-      rest = score(-row[e], true, rs);         // 1 - sigmoid without its cancellation
+      y = row[e];
       g = (double)rule.scale * (double)dw[(int64_t)t * k + lane];
     }
   }
+  // renormalised softmax: only the picks' ratios count
+  if (!rule.sigmoid && rule.renorm) rs.top = (double)wave_max_of(masked(y) ? -INFINITY : fminf(y, FLT_MAX));
+  const double s = score(y, rule.sigmoid, rs);
+  const double rest = rule.sigmoid ? score(-y, true, rs) : 1.0;   // 1 - sigmoid without its cancellation
   double d, all = 0.0;
   if (rule.renorm) {
     const double sum = wave_sum64(s);
     const double p = sum > 0.0 ? s / sum : 0.0;
-    d = p * (g - wave_sum64(g * p)) * (rule.sigmoid ? rest : 1.0);
+    d = p * (g - wave_sum64(g * p)) * rest;
   } else if (rule.sigmoid) {
     d = g * s * rest;
   } else {
     d = g * s;
     all = wave_sum64(d);
   }
+  // the first slot of an expert sums those after it
+  bool first = id >= 0;
+  double v = 0.0;
+  for (int j = 0; j < k; ++j) {
+    const bool same = __builtin_amdgcn_readlane(id, j) == id;
+    const double dj = __shfl(d, j);
+    if (same) v += dj;
+    if (same && j < lane) first = false;
+  }
 #pragma unroll
-  for (int i = 0; i < NPER; ++i) {
-    const int e = lane + 64 * i;
-    double v = dense && e < E ? -score(x[i], false, rs) * all : 0.0;
-    for (int j = 0; j < k; ++j) {
-      const double dj = __shfl(d, j);
-      if (__shfl(id, j) == e) v += dj;
-    }
-    if (e < E) dlogits[(int64_t)t * E + e] = (float)v;
+  for (int i = 0; i < NPER; ++i)
+    mine[lane + 64 * i] = dense ? (float)(-score(x[i], false, rs) * all) : 0.0f;
+  __builtin_amdgcn_wave_barrier();             // the wave's own LDS, in order
+  if (first) mine[id] = (float)(dense ? v - s * all : v);
+  __builtin_amdgcn_wave_barrier();
+  float* out = dlogits + (int64_t)t * E;
+  if ((E & 3) == 0 && ((uintptr_t)dlogits & 15) == 0) {
+    for (int q = lane; q < E / 4; q += 64) ((f32x4*)out)[q] = ((const f32x4*)mine)[q];
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i)
+      if (lane + 64 * i < E) out[lane + 64 * i] = mine[lane + 64 * i];
   }
 }
 
