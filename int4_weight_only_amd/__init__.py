@@ -774,61 +774,88 @@ def w4a16_moe_gemm_combine_noalloc(A, Wq, S, sorted_token_ids, expert_ids,
 
 
 # ------------------------------------------------- W8A8 and the scored router --
+#
+# A small call (a decode step's routing or quantization) takes the GPU less
+# time than the host: the launch itself is about 3 us, each output's
+# allocation 1.5.  So the checks below test everything at once and look for
+# the reason only when something is wrong, and entry points are looked up once.
 
-_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_E4M3, _E8M0, _BF16, _F32, _I32 = (torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.bfloat16,
+                                   torch.float32, torch.int32)
+_Tensor = torch.Tensor
+_entries = {}
 
 
-def _call(name, tensors, *args):
-    """The entry point ``name`` on the device of ``tensors`` (all one device,
-    which need not be the current one) and that device's current stream."""
-    index = tensors[0].device.index
-    for t in tensors:
-        if t is not None and t.device.index != index:
-            raise ValueError(f"{name}: operands on different GPUs")
-    fn = getattr(_lib.load(), name)
-    if index == torch.cuda.current_device():
-        _lib.check(name, fn(*args, _stream(tensors[0])))
+def _call(name, device, *args):
+    """The entry point ``name`` on GPU ``device`` (which need not be the
+    current one) and its current stream."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(_lib.load(), name)
+    if device == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(device) if _raw_stream is not None
+                    else torch.cuda.current_stream(device).cuda_stream)
     else:
-        with torch.cuda.device(index):
-            _lib.check(name, fn(*args, _stream(tensors[0])))
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status:
+        raise _lib.W4Error(name, status)
+
+
+def _in(t, name, dtype, ndim, device=None):
+    """The GPU that ``t`` is on, checked: type, dims, contiguity, and that it
+    is ``device`` where given."""
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == ndim
+            and t.is_contiguous()):
+        index = t.get_device()
+        if device is None or index == device:
+            return index
+        raise ValueError(f"{name} is on GPU {index}, other operands on GPU {device}")
+    _need(t, name, dtype, ndim)
+    raise ValueError(f"{name} is not a usable tensor")
+
+
+def _shape(t, name, dtype, shape, device):
+    _in(t, name, dtype, len(shape), device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _out(t, name, shape, dtype, like):
     """``t`` checked, or a new tensor."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     _need(t, name, dtype)
     if t.numel() != math.prod(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} is on another GPU than the inputs")
     return t
 
 
-def _shape(t, name, dtype, shape):
-    _need(t, name, dtype, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
-def _w8_blocks(n):
-    return (n + 127) // 128
+def _ints(t, name, size, device):
+    _need(t, name, _I32)
+    if t.numel() < size:
+        raise ValueError(f"{name} needs {size} entries")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another GPU than the other operands")
 
 
 def w8_scale_cols(K):
     """Scale bytes of a row of K codes: 4 * ceil(K / 512)."""
-    n = int(_lib.load().w8_scale_cols(K))
-    if n < 0:
+    if K < 0:
         raise ValueError("invalid K")
-    return n
+    return (K + 511) // 512 * 4
 
 
 def w8_quantize_rows(X, X8=None, SX=None):
     """bf16 X [M, K] -> (X8 [M, K], SX [M, C]): e4m3 codes with one
     power-of-two scale per 128 consecutive k (K % 16 == 0)."""
-    _need(X, "X", torch.bfloat16, 2)
+    device = _in(X, "X", _BF16, 2)
     M, K = X.shape
-    X8 = _out(X8, "X8", (M, K), _E4M3, X)
+    X8 = torch.empty_like(X, dtype=_E4M3) if X8 is None else _out(X8, "X8", (M, K), _E4M3, X)
     SX = _out(SX, "SX", (M, w8_scale_cols(K)), _E8M0, X)
-    _call("w8_quantize_rows", (X, X8, SX), _ptr(X), M, K, _ptr(X8), _ptr(SX))
+    _call("w8_quantize_rows", device, X.data_ptr(), M, K, X8.data_ptr(), SX.data_ptr())
     return X8, SX
 
 
@@ -836,16 +863,16 @@ def w8_quantize_blocks(W, transposed=False, W8=None, SW=None, WT8=None, ST=None)
     """bf16 W [N, K] -> (W8 [N, K], SW [ceil(N/128), C], WT8, ST): one scale
     per 128 x 128 block.  ``transposed``: also the same codes as WT8 [K, N]
     with ST [ceil(K/128), w8_scale_cols(N)] (N % 16 == 0); else None, None."""
-    _need(W, "W", torch.bfloat16, 2)
+    device = _in(W, "W", _BF16, 2)
     N, K = W.shape
-    W8 = _out(W8, "W8", (N, K), _E4M3, W)
-    SW = _out(SW, "SW", (_w8_blocks(N), w8_scale_cols(K)), _E8M0, W)
+    W8 = torch.empty_like(W, dtype=_E4M3) if W8 is None else _out(W8, "W8", (N, K), _E4M3, W)
+    SW = _out(SW, "SW", ((N + 127) // 128, w8_scale_cols(K)), _E8M0, W)
     if transposed:
         WT8 = _out(WT8, "WT8", (K, N), _E4M3, W)
-        ST = _out(ST, "ST", (_w8_blocks(K), w8_scale_cols(N)), _E8M0, W)
+        ST = _out(ST, "ST", ((K + 127) // 128, w8_scale_cols(N)), _E8M0, W)
     elif WT8 is not None or ST is not None:
         raise ValueError("WT8 and ST are outputs of transposed=True")
-    _call("w8_quantize_blocks", (W, W8, SW, WT8, ST), _ptr(W), N, K, _ptr(W8), _ptr(SW), _ptr(WT8),
+    _call("w8_quantize_blocks", device, W.data_ptr(), N, K, W8.data_ptr(), SW.data_ptr(), _ptr(WT8),
           _ptr(ST))
     return W8, SW, WT8, ST
 
@@ -853,31 +880,31 @@ def w8_quantize_blocks(W, transposed=False, W8=None, SW=None, WT8=None, ST=None)
 def w8_silu_mul_quantize(H1, A8=None, SA=None):
     """bf16 H1 [R, 2I] -> (A8 [R, I], SA [R, w8_scale_cols(I)]): silu(H1[:, :I])
     * H1[:, I:] in fp32, quantized as w8_quantize_rows does (I % 16 == 0)."""
-    _need(H1, "H1", torch.bfloat16, 2)
+    device = _in(H1, "H1", _BF16, 2)
     R, I2 = H1.shape
     if I2 % 2:
         raise ValueError("H1 must have an even number of columns")
     I = I2 // 2
     A8 = _out(A8, "A8", (R, I), _E4M3, H1)
     SA = _out(SA, "SA", (R, w8_scale_cols(I)), _E8M0, H1)
-    _call("w8_silu_mul_quantize", (H1, A8, SA), _ptr(H1), R, I, _ptr(A8), _ptr(SA))
+    _call("w8_silu_mul_quantize", device, H1.data_ptr(), R, I, A8.data_ptr(), SA.data_ptr())
     return A8, SA
 
 
 def w8a8_gemm(X8, SX, W8, SW, out=None):
     """Y bf16 [M, N] = (X8, SX) * (W8, SW)^T with fp32 accumulation."""
-    _need(X8, "X8", _E4M3, 2)
-    _need(W8, "W8", _E4M3, 2)
+    device = _in(X8, "X8", _E4M3, 2)
+    _in(W8, "W8", _E4M3, 2, device)
     M, K = X8.shape
-    N = W8.shape[0]
-    if W8.shape[1] != K:
+    N, KW = W8.shape
+    if KW != K:
         raise ValueError(f"shape mismatch: X8 {tuple(X8.shape)} W8 {tuple(W8.shape)}")
     cols = w8_scale_cols(K)
-    _shape(SX, "SX", _E8M0, (M, cols))
-    _shape(SW, "SW", _E8M0, (_w8_blocks(N), cols))
-    out = _out(out, "out", (M, N), torch.bfloat16, X8)
-    _call("w8a8_gemm", (X8, SX, W8, SW, out), _ptr(X8), _ptr(SX), _ptr(W8), _ptr(SW), _ptr(out), M,
-          N, K)
+    _shape(SX, "SX", _E8M0, (M, cols), device)
+    _shape(SW, "SW", _E8M0, ((N + 127) // 128, cols), device)
+    out = _out(out, "out", (M, N), _BF16, X8)
+    _call("w8a8_gemm", device, X8.data_ptr(), SX.data_ptr(), W8.data_ptr(), SW.data_ptr(),
+          out.data_ptr(), M, N, K)
     return out
 
 
@@ -893,30 +920,27 @@ def w8a8_moe_gemm(X8, SX, W8, SW, sorted_token_ids, expert_ids, num_tokens_post_
     expert e of (W8 [E, N, K], SW [E, ceil(N/128), C]) for every valid slot f
     of every block with e = expert_ids[b].  Other rows are not written.
     """
-    _need(X8, "X8", _E4M3, 2)
-    _need(W8, "W8", _E4M3, 3)
+    device = _in(X8, "X8", _E4M3, 2)
+    _in(W8, "W8", _E4M3, 3, device)
     E, N, K = W8.shape
     cols = w8_scale_cols(K)
     if x_row_div not in (1, k):
         raise ValueError("x_row_div must be 1 or k")
     rows = (T * k) // x_row_div
-    if tuple(X8.shape) != (rows, K):
+    if X8.shape != (rows, K):
         raise ValueError(f"X8 must be [{rows}, {K}], got {list(X8.shape)}")
-    _shape(SX, "SX", _E8M0, (rows, cols))
-    _shape(SW, "SW", _E8M0, (E, _w8_blocks(N), cols))
+    _shape(SX, "SX", _E8M0, (rows, cols), device)
+    _shape(SW, "SW", _E8M0, (E, (N + 127) // 128, cols), device)
     cap = w4_moe_align_capacity(T, k, E, B)
     if cap < 0:
         raise ValueError("invalid T, k, E or B")
-    for t, n, size in ((sorted_token_ids, "sorted_token_ids", cap),
-                       (expert_ids, "expert_ids", cap // B),
-                       (num_tokens_post_padded, "num_tokens_post_padded", 1)):
-        _need(t, n, torch.int32)
-        if t.numel() < size:
-            raise ValueError(f"{n} needs {size} entries")
-    out = _out(out, "out", (T * k, N), torch.bfloat16, X8)
-    _call("w8a8_moe_gemm", (X8, SX, W8, SW, sorted_token_ids, expert_ids, num_tokens_post_padded, out),
-          _ptr(X8), _ptr(SX), _ptr(W8), _ptr(SW), _ptr(sorted_token_ids), _ptr(expert_ids),
-          _ptr(num_tokens_post_padded), _ptr(out), T, k, E, N, K, B, x_row_div)
+    _ints(sorted_token_ids, "sorted_token_ids", cap, device)
+    _ints(expert_ids, "expert_ids", cap // B, device)
+    _ints(num_tokens_post_padded, "num_tokens_post_padded", 1, device)
+    out = _out(out, "out", (T * k, N), _BF16, X8)
+    _call("w8a8_moe_gemm", device, X8.data_ptr(), SX.data_ptr(), W8.data_ptr(), SW.data_ptr(),
+          sorted_token_ids.data_ptr(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(),
+          out.data_ptr(), T, k, E, N, K, B, x_row_div)
     return out
 
 
@@ -930,15 +954,16 @@ def w4_moe_route_scored(logits, k, sigmoid=False, bias=None, groups=1, topk_grou
     times the chosen scores, which ``renorm`` makes sum to one.  Ties go to
     the lower index; NaN and -Inf mask an expert.
     """
-    _need(logits, "logits", torch.float32, 2)
+    device = _in(logits, "logits", _F32, 2)
     T, E = logits.shape
     if bias is not None:
-        _shape(bias, "bias", torch.float32, (E,))
-    topk_ids = _out(topk_ids, "topk_ids", (T, k), torch.int32, logits)
-    topk_weights = _out(topk_weights, "topk_weights", (T, k), torch.float32, logits)
-    _call("w4_moe_route_scored", (logits, bias, topk_ids, topk_weights), _ptr(logits), _ptr(bias), T,
-          E, k, int(sigmoid), groups, topk_groups, group_top, int(renorm), scale, _ptr(topk_ids),
-          _ptr(topk_weights))
+        _shape(bias, "bias", _F32, (E,), device)
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    topk_ids = _out(topk_ids, "topk_ids", (T, k), _I32, logits)
+    topk_weights = _out(topk_weights, "topk_weights", (T, k), _F32, logits)
+    _call("w4_moe_route_scored", device, logits.data_ptr(), _ptr(bias), T, E, k, int(sigmoid), groups,
+          topk_groups, group_top, int(renorm), scale, topk_ids.data_ptr(), topk_weights.data_ptr())
     return topk_ids, topk_weights
 
 
@@ -946,15 +971,15 @@ def w4_moe_route_scored_bwd(logits, topk_ids, topk_weights, grad_weights, sigmoi
                             scale=1.0, grad_logits=None):
     """Gradient of w4_moe_route_scored's weights to the logits (the choice held
     fixed): fp32 [T, E] from the forward's outputs and grad_weights [T, k]."""
-    _need(logits, "logits", torch.float32, 2)
+    device = _in(logits, "logits", _F32, 2)
     T, E = logits.shape
-    _need(topk_ids, "topk_ids", torch.int32, 2)
-    k = topk_ids.shape[1]
-    _shape(topk_ids, "topk_ids", torch.int32, (T, k))
-    _shape(topk_weights, "topk_weights", torch.float32, (T, k))
-    _shape(grad_weights, "grad_weights", torch.float32, (T, k))
-    grad_logits = _out(grad_logits, "grad_logits", (T, E), torch.float32, logits)
-    _call("w4_moe_route_scored_bwd", (logits, topk_ids, topk_weights, grad_weights, grad_logits),
-          _ptr(logits), _ptr(topk_ids), _ptr(topk_weights), _ptr(grad_weights), T, E, k,
-          int(sigmoid), int(renorm), scale, _ptr(grad_logits))
+    _in(topk_ids, "topk_ids", _I32, 2, device)
+    shape = (T, topk_ids.shape[1])
+    _shape(topk_ids, "topk_ids", _I32, shape, device)
+    _shape(topk_weights, "topk_weights", _F32, shape, device)
+    _shape(grad_weights, "grad_weights", _F32, shape, device)
+    grad_logits = _out(grad_logits, "grad_logits", (T, E), _F32, logits)
+    _call("w4_moe_route_scored_bwd", device, logits.data_ptr(), topk_ids.data_ptr(),
+          topk_weights.data_ptr(), grad_weights.data_ptr(), T, E, shape[1], int(sigmoid), int(renorm),
+          scale, grad_logits.data_ptr())
     return grad_logits
