@@ -3,6 +3,7 @@
 //   Y[m, n] = bf16( sum_k X8[m, k] 2^SX[m, k/128] W8[n, k] 2^SW[n/128, k/128] )
 //
 // dense (w8a8_gemm) and grouped over aligned expert blocks (w8a8_moe_gemm).
+#include <algorithm>
 #include <type_traits>
 
 #include "w8.h"
@@ -162,17 +163,22 @@ __global__ __launch_bounds__(NW * 64) void k_w8_split(const uint8_t* __restrict_
 // step, two stages; a row's eight 16-byte pieces are stored XOR-swizzled by
 // (row / 2) % 8, so that an operand read of 16 rows spreads over the banks.
 //
-// A step multiplies four quarters, (X low, W low), (X low, W high), (X high,
-// W high), (X high, W low), so that a wave needs its operands once and four at a
-// time: the halves for the next quarter, at last the next step's low halves,
-// are read during the one before, into registers whose half is done (W's two
-// sets swap roles every step).  LDS reads are spread evenly over the MFMAs that
-// way, eight per sixteen; reading all of X at the end of a step kept the LDS
-// busy twice as long as the MFMAs of that time (8192^3: 464 us).  After the
-// second quarter the waves meet, once a step: the next stage has landed and
-// everyone has read this one, so its buffer takes the loads of two steps ahead,
-// which have three quarters of a step to a whole one to land.  An odd number of
-// steps is made even by one of zeros (pieces past K read zero).
+// Large tiles (NST 2 or 3 stages) multiply a step in four quarters, (X low, W
+// low), (X low, W high), (X high, W high), (X high, W low), so that a wave holds
+// its operands once and reads them during the quarters before: the high halves
+// in the first, then, when the next stage has landed, its low halves in the
+// third and fourth, into registers whose half is done (W's two sets swap roles
+// every step).  After the first quarter a stage has been read and its buffer
+// takes the loads of NST steps ahead, spread over the other three quarters: in
+// one burst they queue behind each other and land too late (4096 x 14336 x
+// 4096: 223 us with the loads in the third quarter, 209 spread; 157 us of
+// 4096 x 4096 x 16384's 224 are left without the traffic).  Reading all of X at
+// the end of a step keeps the LDS busy twice as long as the MFMAs of that time
+// (8192^3: 464 us, 400 in quarters).  An odd number of steps is made even by one
+// of zeros (pieces past K read zero).
+//
+// Small tiles (four stages) hold two steps' operands: one multiplies while the
+// next is read, one barrier a step, and loads have three steps to land.
 //
 // The scales of four K blocks are one dword a row; they pass through a small
 // LDS ring the same way.
@@ -222,14 +228,15 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
   constexpr int BM = 32 * MI, BN = 32 * NI;
   constexpr int XA = BM / 32, XB = BN / 32;        // 1 KB loads per wave and stage
   static_assert(MI % 2 == 0 && NI % 2 == 0 && MI <= 8 && NI <= 8, "halves; one scale of W a wave");
-  static_assert(NST == 2 || NST == 4, "stages");
+  static_assert(NST >= 2 && NST <= 4, "stages");
   // each stage an object of its own: the compiler then knows which loads an
   // operand read has to wait for
-  constexpr int SA = BM * 128, SB = BN * 128, S4 = NST == 4;
+  constexpr int SA = BM * 128, SB = BN * 128;
+  constexpr bool S3 = NST > 2, S4 = NST > 3;
   __shared__ __attribute__((aligned(16))) uint8_t as0_[KG][SA], as1_[KG][SA];
   __shared__ __attribute__((aligned(16))) uint8_t bs0_[KG][SB], bs1_[KG][SB];
-  __shared__ __attribute__((aligned(16))) uint8_t as2_[KG][S4 ? SA : 16], as3_[KG][S4 ? SA : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t bs2_[KG][S4 ? SB : 16], bs3_[KG][S4 ? SB : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t as2_[KG][S3 ? SA : 16], as3_[KG][S4 ? SA : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t bs2_[KG][S3 ? SB : 16], bs3_[KG][S4 ? SB : 16];
   __shared__ __attribute__((aligned(16))) uint32_t rx_[KG][2][256], rw_[KG][2][64];
 
   const int lane = threadIdx.x & 63;
@@ -263,7 +270,8 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
   const int steps = (K + 127) / 128;
   // this group's steps, a multiple of the stages for every group (those past
   // its own part of K are zeros)
-  const int share = ((steps + KG - 1) / KG + NST - 1) / NST * NST;
+  constexpr int ROUND = NST == 3 ? 2 : NST;
+  const int share = ((steps + KG - 1) / KG + ROUND - 1) / ROUND * ROUND;
   const int first = kg * share, last = first + share;
   const int k_end = min(K, last * 128);
   if constexpr (GROUPED) {
@@ -344,7 +352,8 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
     for (int j = 0; j < NI; ++j) acc[i][j] = zero;
   // small tiles hold two steps' operands (WHOLE), large ones halves
   constexpr bool WHOLE = MI + NI <= 8;
-  static_assert(NST == (WHOLE ? 4 : 2), "stages of the two schedules");
+  static_assert(WHOLE == (NST == 4), "stages of the two schedules");
+  static_assert(NST != 3 || KG == 1, "three stages: any even number of steps");
   constexpr int HI = WHOLE ? MI : MI / 2, HJ = WHOLE ? NI : NI / 2;
   i32x8 x[2][HI], w[2][HJ];
   uint32_t sx[MI], sw;
@@ -436,20 +445,35 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
   auto body_halves = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
       __attribute__((always_inline)) {
     constexpr int s = decltype(S)::value;
+    constexpr int L2 = (XA + XB) * 3 / 8, L3 = (XA + XB) * 3 / 8;   // loads per quarter
     uint32_t nsx[MI], nsw;
     const int sh = shift(step + 1);
-    quarter(lo, lo, s, [&](int i) { w[1 - s][i] = read(sb, wat, HJ + i); }, HJ, none, 0);
-    quarter(lo, hi, 1 - s, [&](int i) { x[1][i] = read(sa, xat, HI + i); }, HI, none, 0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // read the rest of this stage; when everyone has, its buffer is free
+    quarter(lo, lo, s,
+            [&](int i) {
+              if (i < HJ)
+                w[1 - s][i] = read(sb, wat, HJ + i);
+              else
+                x[1][i - HJ] = read(sa, xat, HI + i - HJ);
+            },
+            HJ + HI, none, 0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     fence();
     load_scales((step + 1) / 4 + 1);
+    quarter(lo, hi, 1 - s, none, 0, [&](int i) { load_one(i, step + NST, sa, sb); }, L2);
+    // the next stage has landed; the loads just issued, and with three stages
+    // those of the step before, may be in flight
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * (XA + XB + 2) + 2 + L2) : "memory");
+    __builtin_amdgcn_s_barrier();
+    fence();
     quarter(hi, hi, 1 - s, [&](int i) { x[0][i] = read(na, xat, i); }, HI,
-            [&](int i) { load_one(i, step + NST, sa, sb); }, XA + XB);
+            [&](int i) { load_one(L2 + i, step + NST, sa, sb); }, L3);
     nsw = read_sw(step + 1);
 #pragma unroll
     for (int i = 0; i < MI; ++i) nsx[i] = read_sx(step + 1, i);
-    quarter(hi, lo, s, [&](int i) { w[1 - s][i] = read(nb, wat, i); }, HJ, none, 0);
+    quarter(hi, lo, s, [&](int i) { w[1 - s][i] = read(nb, wat, i); }, HJ,
+            [&](int i) { load_one(L2 + L3 + i, step + NST, sa, sb); }, XA + XB - L2 - L3);
 #pragma unroll
     for (int i = 0; i < MI; ++i) sx[i] = nsx[i] >> sh;
     sw = nsw >> sh;
@@ -463,10 +487,8 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
   };
   load_stage(first, first / 4, as0, bs0);
   load_stage(first + 1, first / 4 + 1, as1, bs1);
-  if constexpr (NST == 4) {
-    load_stage(first + 2, first / 4 + 1, as2, bs2);
-    load_stage(first + 3, first / 4 + 1, as3, bs3);
-  }
+  if constexpr (S3) load_stage(first + 2, first / 4 + 1, as2, bs2);
+  if constexpr (S4) load_stage(first + 3, first / 4 + 1, as3, bs3);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 1) * (XA + XB + 2)) : "memory");
   __builtin_amdgcn_s_barrier();
   fence();
@@ -478,8 +500,17 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
 #pragma unroll
   for (int j = 0; j < HJ; ++j) w[0][j] = read(bs0, wat, j);
   fence();
-  for (int step = first; step < last; step += NST) {
-    if constexpr (WHOLE) {
+  for (int step = first; step < last; step += NST == 3 ? 6 : NST) {
+    if constexpr (NST == 3) {
+      body_halves(lo, step, as0, bs0, as1, bs1);
+      body_halves(hi, step + 1, as1, bs1, as2, bs2);
+      if (step + 2 >= last) break;
+      body_halves(lo, step + 2, as2, bs2, as0, bs0);
+      body_halves(hi, step + 3, as0, bs0, as1, bs1);
+      if (step + 4 >= last) break;
+      body_halves(lo, step + 4, as1, bs1, as2, bs2);
+      body_halves(hi, step + 5, as2, bs2, as0, bs0);
+    } else if constexpr (WHOLE) {
       body_whole(lo, step, as0, bs0, as1, bs1);
       body_whole(hi, step + 1, as1, bs1, as2, bs2);
       body_whole(integral_constant<int, 2>{}, step + 2, as2, bs2, as3, bs3);
@@ -548,64 +579,104 @@ hipError_t tile(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const u
   return hipGetLastError();
 }
 
-// The tiles and what they cost: a round of one workgroup per CU takes
-// `step_us` per 128-wide step and `fixed_us` besides (launch, first loads,
-// stores), measured with every CU busy and operands that come from memory.
-struct TileKind {
+// The kernels and what they cost.  Tiles: a round of one workgroup per CU takes
+// step_us per 128-wide step and fixed_us besides (launch, first loads, stores),
+// measured with every CU busy and operands that come from memory.  The split
+// kernel reads 16 rows of X and 16 of W per workgroup at 12 TB/s (L2) after
+// 3.5 us.
+struct Kind {
   int bm, bn, kg;
   float step_us, fixed_us;
 };
-constexpr TileKind kTiles[] = {
+constexpr Kind kKinds[] = {
+    {16, 16, 0, 0.0f, 3.5f},     // split
     {64, 64, 2, 0.32f, 6.0f},
     {64, 128, 1, 0.40f, 6.0f},
     {128, 128, 1, 0.60f, 6.0f},
-    {256, 256, 1, 1.45f, 12.0f},
+    {128, 256, 1, 1.05f, 10.0f},
+    {256, 256, 1, 1.35f, 12.0f},
 };
 
-int64_t tiles_of(const TileKind& t, int64_t M, int64_t N) {
+int64_t tiles_of(const Kind& t, int64_t M, int64_t N) {
   return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
 }
 
-// The tile that the estimate says is done first.  Few large tiles move the
+float estimate(int kind, int64_t M, int64_t N, int64_t K) {
+  const Kind& t = kKinds[kind];
+  const int64_t tiles = tiles_of(t, M, N), steps = (K + 127) / 128;
+  if (kind == 0) return t.fixed_us + (float)tiles * (float)K * (32.0f / 12e6f);
+  const int64_t cus = cu_count(), rounds = (tiles + cus - 1) / cus;
+  return (float)rounds * ((float)((steps + t.kg - 1) / t.kg) * t.step_us + t.fixed_us);
+}
+
+// The kernel that the estimate says is done first.  Few large tiles move the
 // least data, but leave CUs idle where they are too few: 4096 x 14336 x 4096
-// takes 233 us in 896 tiles of 256 x 256 and 354 us in 3584 of 128 x 128;
-// 1024 x 4096 x 4096 takes 51 us in 64 of the former and 24 us in 256 of the
-// latter.
-int pick_tile(int64_t M, int64_t N, int64_t K) {
-  const int64_t steps = (K + 127) / 128, cus = cu_count();
-  int best = 0;
-  float best_us = 0.0f;
-  for (int i = 0; i < 4; ++i) {
-    const TileKind& t = kTiles[i];
-    const int64_t rounds = (tiles_of(t, M, N) + cus - 1) / cus;
-    const float us = (float)rounds * ((float)((steps + t.kg - 1) / t.kg) * t.step_us + t.fixed_us);
-    if (i == 0 || us < best_us) {
+// takes 209 us in 896 tiles of 256 x 256, 278 in 1792 of 128 x 256 and 356 in
+// 3584 of 128 x 128; 1024 x 4096 x 4096 takes 51, 36 and 26 us.
+int pick(int64_t M, int64_t N, int64_t K, float& us) {
+  int best = -1;
+  for (int i = M <= 64 ? 0 : 1; i < 6; ++i) {
+    const float e = estimate(i, M, N, K);
+    if (best < 0 || e < us) {
       best = i;
-      best_us = us;
+      us = e;
     }
   }
   return best;
 }
 
+hipError_t run_kind(int kind, const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
+                    const uint8_t* SW, uint16_t* Y, int64_t M, int64_t N, int64_t K,
+                    hipStream_t st) {
+  const Grouped none = {};
+  switch (kind) {
+    case 0:
+      return split<1, 1, 16, false>(X8, SX, W8, SW, Y, M, N, K, (M + 15) / 16, none, st);
+    case 1: return tile<2, 2, 2, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
+    case 2: return tile<2, 4, 1, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
+    case 3: return tile<4, 4, 1, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
+    case 4: return tile<4, 8, 1, 3, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
+    default: return tile<8, 8, 1, 2, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
+  }
+}
+
+// Rows to leave to a launch of their own: up to 16 past a multiple of 128,
+// where a row of tiles for them would cost more (2050 x 4096 x 5120: 2048 rows
+// and 2 instead of 9 x 256).
+int64_t rest_rows(int64_t M, int64_t N, int64_t K) {
+  const int64_t rest = M % 128;
+  if (M <= 128 || rest == 0 || rest > 16) return 0;
+  float whole, main, few;
+  pick(M, N, K, whole);
+  pick(M - rest, N, K, main);
+  pick(rest, N, K, few);
+  return main + few < whole ? rest : 0;
+}
+
 }  // namespace
 
 int64_t w8_gemm_threads(int64_t M, int64_t N, int64_t K) {
-  if (M <= 16) return (N + 15) / 16 * 1024;
-  const TileKind& t = kTiles[pick_tile(M, N, K)];
-  return (tiles_of(t, M, N) + 7) * 256 * t.kg;
+  const int64_t rest = rest_rows(M, N, K);
+  int64_t most = 0;
+  for (const int64_t rows : {M - rest, rest}) {
+    if (rows == 0) continue;
+    float us;
+    const Kind& t = kKinds[pick(rows, N, K, us)];
+    most = std::max(most, t.kg == 0 ? tiles_of(t, rows, N) * 1024
+                                    : (tiles_of(t, rows, N) + 7) * 256 * t.kg);
+  }
+  return most;
 }
 
 hipError_t launch_w8_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
                           const uint8_t* SW, uint16_t* Y, int64_t M, int64_t N, int64_t K,
                           hipStream_t st) {
-  const Grouped none = {};
-  if (M <= 16) return split<1, 1, 16, false>(X8, SX, W8, SW, Y, M, N, K, 1, none, st);
-  switch (pick_tile(M, N, K)) {
-    case 0: return tile<2, 2, 2, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
-    case 1: return tile<2, 4, 1, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
-    case 2: return tile<4, 4, 1, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
-    default: return tile<8, 8, 1, 2, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
-  }
+  float us;
+  const int64_t rest = rest_rows(M, N, K), main = M - rest;
+  const hipError_t e = run_kind(pick(main, N, K, us), X8, SX, W8, SW, Y, main, N, K, st);
+  if (e != hipSuccess || rest == 0) return e;
+  return run_kind(pick(rest, N, K, us), X8 + main * K, SX + main * w8_cols(K), W8, SW, Y + main * N,
+                  rest, N, K, st);
 }
 
 namespace {
@@ -641,7 +712,7 @@ hipError_t launch_w8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_
     case 16: return split<1, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 16, gr, st);
     case 32: return split<2, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 32, gr, st);
     case 64: return tile<2, 4, 1, 4, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
-    case 128: return tile<4, 4, 1, 4, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
+    case 128: return tile<4, 8, 1, 3, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
     default: return tile<8, 8, 1, 2, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
   }
 }
