@@ -602,6 +602,23 @@ int w8a8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const
                   int32_t E, int64_t N, int64_t K, int32_t B, int32_t x_row_div, void* stream);
 
 /*
+ * w8a8_moe_gemm_swiglu -- the gate_up product with the SwiGLU and the
+ * quantization of w8_silu_mul_quantize in its epilogue: for every valid slot,
+ *   (A8, SA)[f] = w8_silu_mul_quantize( bf16 row f of w8a8_moe_gemm, N = 2I )
+ * the same bits, without the [T*k, 2I] intermediate.  A8 [T*k, I], 16-byte
+ * aligned, SA [T*k, w8_scale_cols(I)], 4-byte aligned; rows that no slot names
+ * are not written.  Covers I % 128 == 0 (a row's 128 values of a tile are one
+ * block), B a multiple of 256 and X8 below 2 GiB: W4_ERR_UNSUPPORTED otherwise
+ * (small blocks are bound by the weights, and the pair of calls costs no more).
+ * Other arguments as w8a8_moe_gemm with N = 2I.
+ */
+int w8a8_moe_gemm_swiglu(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
+                         const uint8_t* SW, const int32_t* sorted_token_ids,
+                         const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
+                         uint8_t* A8, uint8_t* SA, int64_t T, int32_t k, int32_t E, int64_t I,
+                         int64_t K, int32_t B, int32_t x_row_div, void* stream);
+
+/*
  * w4_moe_route_scored -- routing by scores, with a bias that only the choice
  * sees and a limit to the best groups of experts (a reading: the pages name
  * gating and routing but give no formula; w4_moe_route is the plain softmax

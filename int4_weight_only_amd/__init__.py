@@ -41,7 +41,8 @@ __all__ = [
     "w4_repack_groups", "w4_restore_groups", "w4a16_gemm_tiled",
     "w4a16_moe_gemm_tiled", "w4a16_moe_gemm_swiglu_tiled",
     "w8_scale_cols", "w8_quantize_rows", "w8_quantize_blocks", "w8_silu_mul_quantize", "w8a8_gemm",
-    "w8_pick_block_size", "w8a8_moe_gemm", "w4_moe_route_scored", "w4_moe_route_scored_bwd",
+    "w8_pick_block_size", "w8a8_moe_gemm", "w8a8_moe_gemm_swiglu", "w4_moe_route_scored",
+    "w4_moe_route_scored_bwd",
 ]
 
 
@@ -912,14 +913,10 @@ def w8_pick_block_size(T, k, E):
     return int(_lib.load().w8_pick_block_size(T, k, E))
 
 
-def w8a8_moe_gemm(X8, SX, W8, SW, sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, B,
-                  x_row_div, out=None):
-    """Grouped W8A8 expert product over aligned blocks of B (a multiple of 16).
-
-    Row f of ``out`` bf16 [T*k, N] = row f // x_row_div of (X8, SX) times
-    expert e of (W8 [E, N, K], SW [E, ceil(N/128), C]) for every valid slot f
-    of every block with e = expert_ids[b].  Other rows are not written.
-    """
+def _w8_moe(X8, SX, W8, SW, sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, B,
+            x_row_div):
+    """Checks shared by the grouped products: (device, E, N, K, the operands'
+    pointers)."""
     device = _in(X8, "X8", _E4M3, 2)
     _in(W8, "W8", _E4M3, 3, device)
     E, N, K = W8.shape
@@ -937,11 +934,40 @@ def w8a8_moe_gemm(X8, SX, W8, SW, sorted_token_ids, expert_ids, num_tokens_post_
     _ints(sorted_token_ids, "sorted_token_ids", cap, device)
     _ints(expert_ids, "expert_ids", cap // B, device)
     _ints(num_tokens_post_padded, "num_tokens_post_padded", 1, device)
+    return device, E, N, K, tuple(t.data_ptr() for t in (
+        X8, SX, W8, SW, sorted_token_ids, expert_ids, num_tokens_post_padded))
+
+
+def w8a8_moe_gemm(X8, SX, W8, SW, sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, B,
+                  x_row_div, out=None):
+    """Grouped W8A8 expert product over aligned blocks of B (a multiple of 16).
+
+    Row f of ``out`` bf16 [T*k, N] = row f // x_row_div of (X8, SX) times
+    expert e of (W8 [E, N, K], SW [E, ceil(N/128), C]) for every valid slot f
+    of every block with e = expert_ids[b].  Other rows are not written.
+    """
+    device, E, N, K, operands = _w8_moe(X8, SX, W8, SW, sorted_token_ids, expert_ids,
+                                        num_tokens_post_padded, T, k, B, x_row_div)
     out = _out(out, "out", (T * k, N), _BF16, X8)
-    _call("w8a8_moe_gemm", device, X8.data_ptr(), SX.data_ptr(), W8.data_ptr(), SW.data_ptr(),
-          sorted_token_ids.data_ptr(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(),
-          out.data_ptr(), T, k, E, N, K, B, x_row_div)
+    _call("w8a8_moe_gemm", device, *operands, out.data_ptr(), T, k, E, N, K, B, x_row_div)
     return out
+
+
+def w8a8_moe_gemm_swiglu(X8, SX, W8, SW, sorted_token_ids, expert_ids, num_tokens_post_padded, T, k,
+                         B, x_row_div, A8=None, SA=None):
+    """gate_up product with SwiGLU and quantization in its epilogue: (A8 [T*k,
+    I], SA), the bits of w8_silu_mul_quantize(w8a8_moe_gemm(...)).  W8 holds
+    2I rows per expert; I % 128 == 0 and B % 256 == 0."""
+    device, E, N, K, operands = _w8_moe(X8, SX, W8, SW, sorted_token_ids, expert_ids,
+                                        num_tokens_post_padded, T, k, B, x_row_div)
+    if N % 2:
+        raise ValueError("W8 must hold 2I rows per expert")
+    I = N // 2
+    A8 = _out(A8, "A8", (T * k, I), _E4M3, X8)
+    SA = _out(SA, "SA", (T * k, w8_scale_cols(I)), _E8M0, X8)
+    _call("w8a8_moe_gemm_swiglu", device, *operands, A8.data_ptr(), SA.data_ptr(), T, k, E, I, K, B,
+          x_row_div)
+    return A8, SA
 
 
 def w4_moe_route_scored(logits, k, sigmoid=False, bias=None, groups=1, topk_groups=1, group_top=1,

@@ -67,6 +67,8 @@ SIGNATURES = {
     "w8_pick_block_size": (_i32, [_i64, _i32, _i32]),
     "w8a8_moe_gemm": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i64, _i64,
                                      _i32, _i32, _p]),
+    "w8a8_moe_gemm_swiglu": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i32, _i32,
+                                            _i64, _i64, _i32, _i32, _p]),
     "w4_moe_route_scored": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                                            ctypes.c_float, _p, _p, _p]),
     "w4_moe_route_scored_bwd": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, _i32,

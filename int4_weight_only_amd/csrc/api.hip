@@ -599,6 +599,31 @@ int w8_shape(int64_t R, int64_t K) {
   return W4_OK;
 }
 
+// Checks shared by the grouped products (Y: their output, of that alignment);
+// W4_OK, -1 for a valid call with nothing to do (T == 0), or an error status.
+int w8_moe_validate(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const uint8_t* SW,
+                    const int32_t* sorted_token_ids, const int32_t* expert_ids,
+                    const int32_t* num_tokens_post_padded, const void* Y, uintptr_t align,
+                    int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B,
+                    int32_t x_row_div) {
+  if (T < 0 || k < 1 || E < 1 || N < 1 || K < 16 || K % 16 != 0 || B < 16 || B % 16 != 0)
+    return W4_ERR_SHAPE;
+  if (x_row_div != 1 && x_row_div != k) return W4_ERR_SHAPE;
+  if (B > 1024 || E > 1024 || T > kMaxI32 || N > kMaxI32 || K > w4::kW8MaxK ||
+      T * k + (int64_t)E * B >= kMaxI32 || T * k * N > kMaxElems || N * K > kMaxElems ||
+      E * (N * K) > kMaxElems)
+    return W4_ERR_UNSUPPORTED;
+  if (w4::w8_moe_threads(T, k, E, N, K, B) >= kMaxGrid) return W4_ERR_UNSUPPORTED;
+  if (T == 0) return -1;
+  if (!X8 || !SX || !W8 || !SW || !sorted_token_ids || !expert_ids || !num_tokens_post_padded || !Y)
+    return W4_ERR_NULL;
+  if (!aligned(X8, 16) || !aligned(W8, 16) || !aligned(SX, 4) || !aligned(SW, 4) ||
+      !aligned(Y, align) || !aligned(sorted_token_ids, 4) || !aligned(expert_ids, 4) ||
+      !aligned(num_tokens_post_padded, 4))
+    return W4_ERR_MISALIGNED;
+  return W4_OK;
+}
+
 int route_rule(int32_t E, int32_t k, int32_t groups, int32_t topk_groups, int32_t group_top) {
   if (E < 1 || k < 1 || groups < 1 || topk_groups < 1 || topk_groups > groups || E % groups != 0)
     return W4_ERR_SHAPE;
@@ -688,24 +713,31 @@ int w8a8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const
                   const int32_t* sorted_token_ids, const int32_t* expert_ids,
                   const int32_t* num_tokens_post_padded, uint16_t* Y, int64_t T, int32_t k,
                   int32_t E, int64_t N, int64_t K, int32_t B, int32_t x_row_div, void* stream) {
-  if (T < 0 || k < 1 || E < 1 || N < 1 || K < 16 || K % 16 != 0 || B < 16 || B % 16 != 0)
-    return W4_ERR_SHAPE;
-  if (x_row_div != 1 && x_row_div != k) return W4_ERR_SHAPE;
-  if (B > 1024 || E > 1024 || T > kMaxI32 || N > kMaxI32 || K > w4::kW8MaxK ||
-      T * k + (int64_t)E * B >= kMaxI32 || T * k * N > kMaxElems || N * K > kMaxElems ||
-      E * (N * K) > kMaxElems)
-    return W4_ERR_UNSUPPORTED;
-  if (w4::w8_moe_threads(T, k, E, N, K, B) >= kMaxGrid) return W4_ERR_UNSUPPORTED;
-  if (T == 0) return W4_OK;
-  if (!X8 || !SX || !W8 || !SW || !sorted_token_ids || !expert_ids || !num_tokens_post_padded || !Y)
-    return W4_ERR_NULL;
-  if (!aligned(X8, 16) || !aligned(W8, 16) || !aligned(SX, 4) || !aligned(SW, 4) ||
-      !aligned(Y, 2) || !aligned(sorted_token_ids, 4) || !aligned(expert_ids, 4) ||
-      !aligned(num_tokens_post_padded, 4))
-    return W4_ERR_MISALIGNED;
+  const int v = w8_moe_validate(X8, SX, W8, SW, sorted_token_ids, expert_ids,
+                                num_tokens_post_padded, Y, 2, T, k, E, N, K, B, x_row_div);
+  if (v != W4_OK) return v < 0 ? W4_OK : v;
   return hip_status(w4::launch_w8_moe_gemm(X8, SX, W8, SW, sorted_token_ids, expert_ids,
                                            num_tokens_post_padded, Y, T, k, E, N, K, B, x_row_div,
                                            as_stream(stream)));
+}
+
+int w8a8_moe_gemm_swiglu(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
+                         const uint8_t* SW, const int32_t* sorted_token_ids,
+                         const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
+                         uint8_t* A8, uint8_t* SA, int64_t T, int32_t k, int32_t E, int64_t I,
+                         int64_t K, int32_t B, int32_t x_row_div, void* stream) {
+  if (I < 1 || I % 16 != 0) return W4_ERR_SHAPE;
+  const int64_t N = I > kMaxI32 / 2 ? kMaxI32 + 1 : 2 * I;   // past the limit: unsupported
+  const int v = w8_moe_validate(X8, SX, W8, SW, sorted_token_ids, expert_ids,
+                                num_tokens_post_padded, A8, 16, T, k, E, N, K, B, x_row_div);
+  if (v > 0) return v;
+  if (!w4::w8_moe_swiglu_fits(T * k / x_row_div, I, K, B)) return W4_ERR_UNSUPPORTED;
+  if (v < 0) return W4_OK;
+  if (!SA) return W4_ERR_NULL;
+  if (!aligned(SA, 4)) return W4_ERR_MISALIGNED;
+  return hip_status(w4::launch_w8_moe_gemm_swiglu(X8, SX, W8, SW, sorted_token_ids, expert_ids,
+                                                  num_tokens_post_padded, A8, SA, T, k, E, I, K, B,
+                                                  x_row_div, as_stream(stream)));
 }
 
 int w4_moe_route_scored(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k,

@@ -44,6 +44,44 @@ __device__ __forceinline__ i32x8 join16(u32x4 lo, u32x4 hi) {
                (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
+// ---------------------------------------------------- quantization, shared --
+
+// Scale byte of a block from the bits of its amax (fp32, sign cleared): with
+// amax = m * 2^p, 1 <= m < 2, the exponent is p - 8, or p - 7 when m > 1.75
+// (448 = 1.75 * 2^8), at least -127; Inf and NaN (which rank on top): 255.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  if (amax >= 0x7F800000u) return 255u;
+  if (amax == 0u) return 127u;
+  const int e = (int)(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return (uint32_t)max(e, 0);
+}
+
+// 2^(127 - byte); the byte of a block is at most 247 (or 255: unused)
+__device__ __forceinline__ float inv_scale(uint32_t byte) {
+  return __uint_as_float((254u - min(byte, 253u)) << 23);
+}
+
+// four values times inv -> four e4m3 codes
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, r, true);
+  return (uint32_t)r;
+}
+
+// silu(g) * u = g / (1 + e^-g) * u.  The exponential is 2^t with t = -g log2 e
+// as a product and its remainder, so that it holds to about two units in the
+// last place for every g; v_exp_f32 and v_rcp_f32 give one unit each.  (The
+// rounding to e4m3 that follows is 2^19 times coarser; the exactly rounded
+// division and expf cost the quantizer 10 us of 78 at 32775 x 2000.)
+__device__ __forceinline__ float silu_mul_fast(float g, float u) {
+  constexpr float kLog2e = 1.44269502f, kRest = 1.92596299e-8f, kLn2 = 0.693147182f;
+  const float t = -g * kLog2e;
+  const float r = __builtin_fmaf(-g, kLog2e, -t) - g * kRest;
+  float e = __builtin_amdgcn_exp2f(t);
+  e = e < INFINITY && e > 0.0f ? __builtin_fmaf(e, r * kLn2, e) : e;
+  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
+
 hipError_t launch_w8_quantize_rows(const uint16_t* X, int64_t M, int64_t K, uint8_t* X8,
                                    uint8_t* SX, hipStream_t st);
 hipError_t launch_w8_quantize_blocks(const uint16_t* W, int64_t N, int64_t K, uint8_t* W8,
@@ -61,6 +99,14 @@ hipError_t launch_w8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_
                               const int32_t* expert_ids, const int32_t* ntpp, uint16_t* Y,
                               int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B,
                               int32_t x_row_div, hipStream_t st);
+// the same for gate and up rows, SwiGLU and quantization in the epilogue; B a
+// multiple of 256, I of 128, and X8 below 2 GiB
+bool w8_moe_swiglu_fits(int64_t rows_x, int64_t I, int64_t K, int32_t B);
+hipError_t launch_w8_moe_gemm_swiglu(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
+                                     const uint8_t* SW, const int32_t* sorted_ids,
+                                     const int32_t* expert_ids, const int32_t* ntpp, uint8_t* A8,
+                                     uint8_t* SA, int64_t T, int32_t k, int32_t E, int64_t I,
+                                     int64_t K, int32_t B, int32_t x_row_div, hipStream_t st);
 // the scored router
 struct RouteRule {
   bool sigmoid;                     // scores: sigmoid, or softmax over the row

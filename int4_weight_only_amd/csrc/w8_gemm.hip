@@ -188,6 +188,12 @@ __global__ __launch_bounds__(NW * 64) void k_w8_split(const uint8_t* __restrict_
 // CUs idle; their sums are joined through LDS in group order.
 // GROUPED: the rows of a tile are sorted pairs of one expert, gathered by the
 // loads.
+//
+// SWIGLU (256 x 256, grouped): W's 2 I rows are gate, then up; a tile takes 128
+// of each, in the waves wn = 0 and 1, which exchange half of their bf16
+// products through LDS; the row's 128 values of silu(g) * u are one scale
+// block, so the tile quantizes them itself and writes codes and scales (Y is
+// A8, one byte a value).
 namespace {
 
 constexpr uint32_t kOOB = 0x80000000u;   // byte offset past any buffer: reads 0
@@ -218,14 +224,16 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, void* lds, u
 
 }  // namespace
 
-template <int MI, int NI, int KG, int NST, bool GROUPED>
+template <int MI, int NI, int KG, int NST, bool GROUPED, bool SWIGLU = false>
 __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restrict__ X8,
                                                          const uint8_t* __restrict__ SX,
                                                          const uint8_t* __restrict__ W8,
                                                          const uint8_t* __restrict__ SW,
                                                          uint16_t* __restrict__ Y, int64_t M,
-                                                         int64_t N, int K, Grouped gr) {
+                                                         int64_t N, int K, Grouped gr,
+                                                         uint8_t* __restrict__ SA_out) {
   constexpr int BM = 32 * MI, BN = 32 * NI;
+  static_assert(!SWIGLU || (GROUPED && MI == 8 && NI == 8), "128 gate and 128 up rows");
   constexpr int XA = BM / 32, XB = BN / 32;        // 1 KB loads per wave and stage
   static_assert(MI % 2 == 0 && NI % 2 == 0 && MI <= 8 && NI <= 8, "halves; one scale of W a wave");
   static_assert(NST >= 2 && NST <= 4, "stages");
@@ -258,13 +266,14 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
   // range of tiles in groups of 8 row blocks of X, which share operands in
   // its L2
   if constexpr (GROUPED) M = min(M, (int64_t)gr.ntpp[0]);
-  const int64_t mt = (M + BM - 1) / BM, nt = (N + BN - 1) / BN;
+  const int64_t inner = N / 2;                     // SWIGLU: gate rows, up rows
+  const int64_t mt = (M + BM - 1) / BM, nt = SWIGLU ? inner / 128 : (N + BN - 1) / BN;
   const int64_t tiles = mt * nt, per = (tiles + 7) / 8;
   const int64_t t = (blockIdx.x % 8) * per + blockIdx.x / 8;
   if (t >= tiles || blockIdx.x / 8 >= per) return;
   const int64_t band = t / (8 * nt), in_band = t - band * 8 * nt;
   const int gm = (int)min((int64_t)8, mt - band * 8);
-  const int64_t m0 = (band * 8 + in_band % gm) * BM, n0 = in_band / gm * BN;
+  const int64_t m0 = (band * 8 + in_band % gm) * BM, n0 = in_band / gm * (SWIGLU ? 128 : BN);
 
   const int cols = (int)w8_cols(K);
   const int steps = (K + 127) / 128;
@@ -284,10 +293,14 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
   const int rows_w = (int)min((int64_t)BN, N - n0);
   const int64_t x0 = GROUPED ? 0 : m0, all_x = GROUPED ? gr.P / gr.div : rows_x;
   const __amdgpu_buffer_rsrc_t ar = rsrc(X8 + x0 * K, all_x * K);
-  const __amdgpu_buffer_rsrc_t br = rsrc(W8 + n0 * K, (int64_t)rows_w * K);
+  // SWIGLU: waves 0 and 1 load the gate rows, 2 and 3 the up rows
+  const int64_t w0 = SWIGLU && wave >= 2 ? inner + n0 : n0;
+  const __amdgpu_buffer_rsrc_t br = rsrc(W8 + w0 * K, (int64_t)(SWIGLU ? 128 : rows_w) * K);
   const __amdgpu_buffer_rsrc_t sar = rsrc(SX + x0 * cols, all_x * cols);
+  const int64_t up = SWIGLU ? inner / 128 : 1;     // the second scale's distance from the first
   const __amdgpu_buffer_rsrc_t sbr =
-      rsrc(SW + (n0 >> 7) * cols, (((n0 + rows_w - 1) >> 7) - (n0 >> 7) + 1) * cols);
+      rsrc(SW + (n0 >> 7) * cols,
+           (SWIGLU ? up + 1 : ((n0 + rows_w - 1) >> 7) - (n0 >> 7) + 1) * cols);
   // row of X, from x0, that tile row r stands for; -1: none
   auto x_row = [&](int r) {
     if constexpr (GROUPED) {
@@ -309,13 +322,13 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
   }
 #pragma unroll
   for (int i = 0; i < XB; ++i) {
-    const int I = wave * XB + i, r = 8 * I + (lane >> 3);
-    boff[i] = r < rows_w ? (uint32_t)r * (uint32_t)K + 16u * piece(I) : kOOB;
+    const int I = wave * XB + i, r = SWIGLU ? (8 * I + (lane >> 3)) & 127 : 8 * I + (lane >> 3);
+    boff[i] = SWIGLU || r < rows_w ? (uint32_t)r * (uint32_t)K + 16u * piece(I) : kOOB;
   }
   // row of the scale ring this lane fills
   const int srow = 64 * wave < BM ? x_row(64 * wave + lane) : -1;
   const uint32_t sxoff = srow >= 0 ? (uint32_t)(srow * cols) : kOOB;
-  const uint32_t swoff = lane < 2 ? (uint32_t)(lane * cols) : kOOB;   // past the end: 0
+  const uint32_t swoff = lane < 2 ? (uint32_t)(lane * up * cols) : kOOB;   // past the end: 0
 
   // load i of a wave's XA + XB of a stage
   auto load_one = [&](int i, int step, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
@@ -542,6 +555,69 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
     }
     if (kg > 0) return;
   }
+  if constexpr (SWIGLU) {
+    // wave wn keeps the row tiles 4 wn .. 4 wn + 3 and gives the others away, two
+    // tiles a round
+    uint32_t(*give)[2][NI][64][2] = (uint32_t(*)[2][NI][64][2])as0_;
+    auto half = [&](auto WN) __attribute__((always_inline)) {
+      constexpr int own = decltype(WN)::value;
+      const int64_t cols_i = w8_cols(inner);
+#pragma unroll
+      for (int rd = 0; rd < 2; ++rd) {
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int j = 0; j < NI; ++j) {
+            const f32x4 v = acc[4 * (1 - own) + 2 * rd + q][j];
+            *(u32x2*)give[2 * wm + own][q][j][lane] = u32x2{pk_bf16(v.x, v.y), pk_bf16(v.z, v.w)};
+          }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int i = 4 * own + 2 * rd + q;
+          const int row = gr.sorted_ids[m0 + xrow + 16 * i];
+          float a[NI][4];
+          uint32_t top = 0;
+#pragma unroll
+          for (int j = 0; j < NI; ++j) {
+            const f32x4 v = acc[i][j];
+            const u32x2 mine = {pk_bf16(v.x, v.y), pk_bf16(v.z, v.w)};
+            const u32x2 other = *(const u32x2*)give[2 * wm + 1 - own][q][j][lane];
+            const u32x2 g = own == 0 ? mine : other, u = own == 0 ? other : mine;
+            a[j][0] = silu_mul_fast(bf16_lo(g.x), bf16_lo(u.x));
+            a[j][1] = silu_mul_fast(bf16_hi(g.x), bf16_hi(u.x));
+            a[j][2] = silu_mul_fast(bf16_lo(g.y), bf16_lo(u.y));
+            a[j][3] = silu_mul_fast(bf16_hi(g.y), bf16_hi(u.y));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) top = max(top, __float_as_uint(a[j][r]) & 0x7FFFFFFFu);
+          }
+          // the row's other values are in lanes 16, 32 and 48 further
+          top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+          top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+          if ((uint32_t)row >= (uint32_t)gr.P) continue;
+          const uint32_t byte = scale_byte(top);
+          const float inv = inv_scale(byte);
+          uint8_t* out = (uint8_t*)Y + (int64_t)row * inner + n0 + 4 * h;
+#pragma unroll
+          for (int j = 0; j < NI; ++j)
+            *(uint32_t*)(out + 16 * j) =
+                byte == 255u ? 0x7F7F7F7Fu : codes4(a[j][0], a[j][1], a[j][2], a[j][3], inv);
+          if (h == 0) {
+            uint8_t* s = SA_out + (int64_t)row * cols_i;
+            s[n0 >> 7] = (uint8_t)byte;
+            if (n0 + 128 == inner)
+              for (int64_t c = inner / 128; c < cols_i; ++c) s[c] = 127;   // padding
+          }
+        }
+      }
+    };
+    if (wn == 0)
+      half(lo);
+    else
+      half(hi);
+    return;
+  }
   const bool vec = (N & 3) == 0 && ((uintptr_t)Y & 7) == 0;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
@@ -575,7 +651,7 @@ hipError_t tile(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const u
                 uint16_t* Y, int64_t M, int64_t N, int64_t K, const Grouped& gr, hipStream_t st) {
   const int64_t tiles = ((M + 32 * MI - 1) / (32 * MI)) * ((N + 32 * NI - 1) / (32 * NI));
   hipLaunchKernelGGL((k_w8_tile<MI, NI, KG, NST, GROUPED>), dim3((unsigned)((tiles + 7) / 8 * 8)),
-                     dim3(256 * KG), 0, st, X8, SX, W8, SW, Y, M, N, (int)K, gr);
+                     dim3(256 * KG), 0, st, X8, SX, W8, SW, Y, M, N, (int)K, gr, nullptr);
   return hipGetLastError();
 }
 
@@ -715,6 +791,22 @@ hipError_t launch_w8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_
     case 128: return tile<4, 8, 1, 3, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
     default: return tile<8, 8, 1, 2, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
   }
+}
+
+bool w8_moe_swiglu_fits(int64_t rows_x, int64_t I, int64_t K, int32_t B) {
+  return I % 128 == 0 && moe_tile_rows(rows_x, K, B) == 256;
+}
+
+hipError_t launch_w8_moe_gemm_swiglu(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
+                                     const uint8_t* SW, const int32_t* sorted_ids,
+                                     const int32_t* expert_ids, const int32_t* ntpp, uint8_t* A8,
+                                     uint8_t* SA, int64_t T, int32_t k, int32_t E, int64_t I,
+                                     int64_t K, int32_t B, int32_t x_row_div, hipStream_t st) {
+  const Grouped gr = {sorted_ids, expert_ids, ntpp, (int)(T * k), E, B, x_row_div};
+  const int64_t cap = moe_rows(T, k, E, B), tiles = cap / 256 * (I / 128);
+  hipLaunchKernelGGL((k_w8_tile<8, 8, 1, 2, true, true>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                     dim3(256), 0, st, X8, SX, W8, SW, (uint16_t*)A8, cap, 2 * I, (int)K, gr, SA);
+  return hipGetLastError();
 }
 
 }  // namespace w4

@@ -5,9 +5,8 @@
 //   code = e4m3_rne(x * 2^-e)
 // amax of bf16 or fp32 values comes from an integer maximum of their bits
 // without the sign, which also ranks Inf and NaN on top: such a block gets
-// the NaN scale and NaN codes.  With amax = m * 2^p, 1 <= m < 2, the
-// exponent is p - 8, or p - 7 when m > 1.75 (448 = 1.75 * 2^8).  x * 2^-e is
-// exact and at most 448, so the only rounding is that of the conversion.
+// the NaN scale and NaN codes.  x * 2^-e is exact and at most 448, so the only
+// rounding is that of the conversion.
 #include "w8.h"
 
 namespace w4 {
@@ -39,26 +38,6 @@ __device__ __forceinline__ uint32_t amax8(u32x4 v) {
   constexpr uint32_t kAbs = 0x7FFF7FFFu;
   const uint32_t a = pk_max_u16(pk_max_u16(v.x & kAbs, v.y & kAbs), pk_max_u16(v.z & kAbs, v.w & kAbs));
   return max(a & 0xFFFFu, a >> 16);
-}
-
-// Scale byte of a block from the bits of its amax (fp32, sign cleared).
-__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
-  if (amax >= 0x7F800000u) return 255u;
-  if (amax == 0u) return 127u;
-  const int e = (int)(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return (uint32_t)max(e, 0);
-}
-
-// 2^(127 - byte); the byte of a block is at most 247 (or 255: unused)
-__device__ __forceinline__ float inv_scale(uint32_t byte) {
-  return __uint_as_float((254u - min(byte, 253u)) << 23);
-}
-
-// four values times inv -> four e4m3 codes
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
-  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
-  r = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, r, true);
-  return (uint32_t)r;
 }
 
 __device__ __forceinline__ u32x2 codes8(u32x4 v, uint32_t byte) {
@@ -206,8 +185,8 @@ __global__ __launch_bounds__(256) void k_w8_silu_mul_quantize(const uint16_t* __
       const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w};
   #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        a[2 * j] = silu_mul(bf16_lo(g[j]), bf16_lo(u[j]));
-        a[2 * j + 1] = silu_mul(bf16_hi(g[j]), bf16_hi(u[j]));
+        a[2 * j] = silu_mul_fast(bf16_lo(g[j]), bf16_lo(u[j]));
+        a[2 * j + 1] = silu_mul_fast(bf16_hi(g[j]), bf16_hi(u[j]));
       }
     }
     uint32_t amax = 0;

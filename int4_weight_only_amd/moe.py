@@ -24,8 +24,9 @@ of the pages' rollout comparison) behind the scored router:
 
     logits --w4_moe_route_scored--> ids, weights
     X --w8_quantize_rows--> X8, SX
-    X8 --w8a8_moe_gemm (gate_up, x_row_div = k)--> H1 [T*k, 2I]
-    H1 --w8_silu_mul_quantize--> A8, SA
+    X8 --w8a8_moe_gemm_swiglu (gate_up, x_row_div = k)--> A8, SA
+      (where that does not cover the sizes: w8a8_moe_gemm --> H1 [T*k, 2I],
+       then w8_silu_mul_quantize --> A8, SA: the same bits)
     A8 --w8a8_moe_gemm (down, x_row_div = 1)--> H2 [T*k, H]
     H2, weights --w4_moe_sum--> Out [T, H]
 """
@@ -41,7 +42,7 @@ from . import (moe_align_block_size, w4_moe_align_capacity, w4_moe_combine_works
                w4a16_moe_gemm_swiglu_asym, w4a16_moe_gemm_swiglu_tiled, w4a16_moe_gemm_tiled,
                w4_moe_route_scored, w4_moe_route_scored_bwd, w8_pick_block_size,
                w8_quantize_blocks, w8_quantize_rows, w8_scale_cols, w8_silu_mul_quantize,
-               w8a8_moe_gemm)
+               w8a8_moe_gemm, w8a8_moe_gemm_swiglu)
 
 
 @dataclass
@@ -306,11 +307,16 @@ class MoEBuffersW8:
     ntpp: torch.Tensor
     X8: torch.Tensor
     SX: torch.Tensor
-    H1: torch.Tensor
+    H1: torch.Tensor            # None where the SwiGLU is fused into gate_up
     A8: torch.Tensor
     SA: torch.Tensor
     H2: torch.Tensor
     out: torch.Tensor
+
+
+def _fuses_swiglu_w8(T, H, I, B):
+    """Whether w8a8_moe_gemm_swiglu covers these sizes."""
+    return B % 256 == 0 and I % 128 == 0 and T * H < 1 << 31
 
 
 def alloc_buffers_w8(T, k, E, H, I, B, device):
@@ -321,7 +327,8 @@ def alloc_buffers_w8(T, k, E, H, I, B, device):
     i32, bf, e4m3, e8m0 = torch.int32, torch.bfloat16, torch.float8_e4m3fn, torch.float8_e8m0fnu
     return MoEBuffersW8(new((T, k), i32), new((T, k), torch.float32), new(cap, i32),
                         new(cap // B, i32), new(1, i32), new((T, H), e4m3),
-                        new((T, w8_scale_cols(H)), e8m0), new((T * k, 2 * I), bf),
+                        new((T, w8_scale_cols(H)), e8m0),
+                        None if _fuses_swiglu_w8(T, H, I, B) else new((T * k, 2 * I), bf),
                         new((T * k, I), e4m3), new((T * k, w8_scale_cols(I)), e8m0),
                         new((T * k, H), bf), new((T, H), bf))
 
@@ -344,8 +351,11 @@ def moe_forward_w8(X, topk_ids, topk_weights, gate_up, down, B=None, buffers=Non
     b = buffers or alloc_buffers_w8(T, k, E, H, I, B, X.device)
     w8_quantize_rows(X, b.X8, b.SX)
     plan = moe_align_block_size(topk_ids, E, B, b.sorted_token_ids, b.expert_ids, b.ntpp)
-    w8a8_moe_gemm(b.X8, b.SX, gate_up.W8, gate_up.SW, *plan, T, k, B, k, out=b.H1)
-    w8_silu_mul_quantize(b.H1, b.A8, b.SA)
+    if _fuses_swiglu_w8(T, H, I, B):
+        w8a8_moe_gemm_swiglu(b.X8, b.SX, gate_up.W8, gate_up.SW, *plan, T, k, B, k, b.A8, b.SA)
+    else:
+        w8a8_moe_gemm(b.X8, b.SX, gate_up.W8, gate_up.SW, *plan, T, k, B, k, out=b.H1)
+        w8_silu_mul_quantize(b.H1, b.A8, b.SA)
     w8a8_moe_gemm(b.A8, b.SA, down.W8, down.SW, *plan, T, k, B, 1, out=b.H2)
     w4_moe_sum(b.H2, topk_weights, T, k, out=b.out)
     return b.out, b

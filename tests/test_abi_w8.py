@@ -98,6 +98,16 @@ def test_moe_gemm_refusals(lib):
     assert f(X=A4) == f(W=A4) == f(S=A2) == f(ids=A2) == f(Y=A1) == MISALIGNED
 
 
+def test_moe_gemm_swiglu_refusals(lib):
+    def f(T=4, k=2, E=3, I=128, K=32, B=256, div=2, X=A16, S=A4, A=A16, SA=A4):
+        return lib.w8a8_moe_gemm_swiglu(X, S, A16, S, A4, A4, A4, A, SA, T, k, E, I, K, B, div, None)
+    assert f(I=0) == f(I=24) == f(T=-1) == f(K=24) == f(B=8) == f(div=3) == SHAPE
+    assert f(I=144) == f(B=64) == f(B=320) == f(I=1 << 31, X=None) == f(T=1 << 26, K=1024) == UNSUPPORTED
+    assert f(T=0, X=None) == OK
+    assert f(X=None) == f(A=None) == f(SA=None) == NULL
+    assert f(X=A4) == f(A=A4) == f(SA=A2) == MISALIGNED
+
+
 def test_route_scored_refusals(lib):
     def f(T=4, E=16, k=2, groups=1, tg=1, top=1, lg=A4, bias=None, ids=A4, w=A4):
         return lib.w4_moe_route_scored(lg, bias, T, E, k, 1, groups, tg, top, 1, 1.0, ids, w, None)

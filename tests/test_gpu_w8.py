@@ -268,6 +268,32 @@ def test_moe_gemm_no_tokens():
     assert out.shape == (0, 32)
 
 
+@pytest.mark.parametrize("T,E,k,I,K,B,rows", [(3, 2, 2, 128, 16, 256, "k"), (300, 3, 2, 256, 400, 256, "k"), (700, 2, 1, 640, 272, 512, "1"),
+                                             (520, 5, 5, 384, 144, 1024, "1")])
+def test_moe_gemm_swiglu_is_the_pair(T, E, k, I, K, B, rows):
+    say(f"w8a8_moe_gemm_swiglu T={T} E={E} k={k} I={I} K={K} B={B} rows={rows}")
+    div = k if rows == "k" else 1
+    rng = np.random.default_rng(16)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    ids[T // 3, 0] = E + 3                       # a skipped pair
+    x = special_rows(T * k // div, K, 17)
+    x8, sx = w4.w8_quantize_rows(up_bits(x))
+    w8_, sw = experts(E, 2 * I, K, 18)
+    w8_, sw = codes(w8_), scales(sw)
+    plan = w4.moe_align_block_size(up(ids), E, B)
+    h1 = w4.w8a8_moe_gemm(x8, sx, w8_, sw, *plan, T, k, B, div)
+    q_ref, s_ref = w4.w8_silu_mul_quantize(h1)
+    room = torch.full((2, T * k, I), 3, dtype=torch.uint8, device=dev())
+    srt = torch.full((T * k, w4.w8_scale_cols(I)), 9, dtype=torch.uint8, device=dev())
+    w4.w8a8_moe_gemm_swiglu(x8, sx, w8_, sw, *plan, T, k, B, div, room[0].view(E4M3), srt.view(E8M0))
+    done = np.nonzero((ids.reshape(-1) >= 0) & (ids.reshape(-1) < E))[0]
+    np.testing.assert_array_equal(down(room[0])[done], bytes_of(q_ref)[done])
+    np.testing.assert_array_equal(down(srt)[done], bytes_of(s_ref)[done])
+    assert (room[1] == 3).all()
+    skipped = np.setdiff1d(np.arange(T * k), done)
+    assert len(skipped) and (down(room[0])[skipped] == 3).all() and (down(srt)[skipped] == 9).all()
+
+
 # ------------------------------------------------------- the layers on top --
 
 def layer_case(T, E, k, H, I, seed):
@@ -300,9 +326,16 @@ def test_layer(T, E, k, H, I):
         f = np.nonzero(flat == e)[0]
         if not len(f):
             continue
-        assert_product(b.H1[up(f)], x8[f // k], sx[f // k], *ow8.quantize_blocks(synth.bits(gu[e])))
+        if b.H1 is not None:
+            assert_product(b.H1[up(f)], x8[f // k], sx[f // k], *ow8.quantize_blocks(synth.bits(gu[e])))
         assert_product(b.H2[up(f)], a8[f], sa[f], *ow8.quantize_blocks(synth.bits(dn[e])))
-    q, s = w4.w8_silu_mul_quantize(b.H1)
+    assert (b.H1 is None) == (T == 700)          # blocks of 256: the fused form
+    if b.H1 is None:
+        plan = b.sorted_token_ids, b.expert_ids, b.ntpp
+        h1 = w4.w8a8_moe_gemm(b.X8, b.SX, g.W8, g.SW, *plan, T, k, w4.w8_pick_block_size(T, k, E), k)
+    else:
+        h1 = b.H1
+    q, s = w4.w8_silu_mul_quantize(h1)
     np.testing.assert_array_equal(bytes_of(q), a8)
     np.testing.assert_array_equal(bytes_of(s), sa)
     h2 = down(b.H2.float()).astype(np.float64).reshape(T, k, H)
