@@ -691,7 +691,7 @@ float estimate(int kind, int64_t M, int64_t N, int64_t K) {
 // 3584 of 128 x 128; 1024 x 4096 x 4096 takes 51, 36 and 26 us.
 int pick(int64_t M, int64_t N, int64_t K, float& us) {
   int best = -1;
-  for (int i = M <= 64 ? 0 : 1; i < 6; ++i) {
+  for (int i = M <= 64 ? 0 : 1; i < (M <= 16 ? 1 : 6); ++i) {
     const float e = estimate(i, M, N, K);
     if (best < 0 || e < us) {
       best = i;
@@ -706,8 +706,19 @@ hipError_t run_kind(int kind, const uint8_t* X8, const uint8_t* SX, const uint8_
                     hipStream_t st) {
   const Grouped none = {};
   switch (kind) {
-    case 0:
-      return split<1, 1, 16, false>(X8, SX, W8, SW, Y, M, N, K, (M + 15) / 16, none, st);
+    case 0: {
+      const int64_t slots = (M + 15) / 16, cus = cu_count();
+      // 64 rows of W per workgroup share their rows of X, which counts once
+      // there are some and N fills the CUs (16 x 12288 x 4096: 12.5 us, 15.9 in
+      // 16 rows); else 16, on 16 waves where there are few workgroups and 8
+      // where there are many (4096 x 7168: 7.6 and 9.2 us; 12288 x 4096: 10.7
+      // and 10.0, one row).
+      if (M > 2 && M <= 16 && N >= 48 * cus)
+        return split<1, 4, 8, false>(X8, SX, W8, SW, Y, M, N, K, slots, none, st);
+      if (N <= 32 * cus)
+        return split<1, 1, 16, false>(X8, SX, W8, SW, Y, M, N, K, slots, none, st);
+      return split<1, 1, 8, false>(X8, SX, W8, SW, Y, M, N, K, slots, none, st);
+    }
     case 1: return tile<2, 2, 2, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
     case 2: return tile<2, 4, 1, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
     case 3: return tile<4, 4, 1, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
