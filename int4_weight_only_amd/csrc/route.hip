@@ -247,6 +247,25 @@ __device__ __forceinline__ void choose_exactly(double (&v)[NPER], double* mine, 
 
 }  // namespace
 
+namespace {
+
+// A row's picks, for the wave that weighs them
+struct Picked {
+  RowSum rs;
+  float x[16];
+  int id[16];
+};
+
+// sum over each row of 16 lanes, in every lane of it, in one fixed order
+__device__ __forceinline__ double row16_sum64(double a) {
+  a += dpp64<0xB1>(a);
+  a += dpp64<0x4E>(a);
+  a += dpp64<0x141>(a);
+  return a + dpp64<0x140>(a);
+}
+
+}  // namespace
+
 template <int NPER>
 __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ logits,
                                                       const float* __restrict__ bias, int T, int E,
@@ -254,9 +273,10 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
                                                       int32_t* __restrict__ ids,
                                                       float* __restrict__ wts) {
   extern __shared__ double choice[];           // [4 waves][E]: only with groups
+  __shared__ Picked picked[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = blockIdx.x * 4 + wave;
-  if (t >= T) return;                          // whole waves; no barrier below
+  // rows past T: the last one again, not stored
+  const int t = min((int)blockIdx.x * 4 + wave, T - 1);
   const float* row = logits + (int64_t)t * E;
   double* mine = choice + (int64_t)wave * E;
   float x[NPER], add[NPER];
@@ -311,15 +331,26 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
       c[i] = masked(add[i]) ? -INFINITY : score(x[i], rule.sigmoid, rs) + (double)add[i];
     choose_exactly<NPER>(c, mine, E, k, rule, lane, my_id, my_live);
   }
-  double s = 0.0;
-  if (lane < k && my_live) s = score(row[my_id], rule.sigmoid, rs);
+  // the weights of four rows at once, 16 lanes each: their 64-bit exponentials
+  // and divisions would take a wave per row as long as the choice
+  if (lane < 16) {
+    picked[wave].id[lane] = my_id;
+    picked[wave].x[lane] = lane < k && my_live ? row[my_id] : -INFINITY;
+    if (lane == 0) picked[wave].rs = rs;
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  const Picked& p = picked[lane >> 4];
+  const int j = lane & 15;
+  double s = score(p.x[j], rule.sigmoid, p.rs);
   if (rule.renorm) {
-    const double sum = wave_sum64(s);
+    const double sum = row16_sum64(s);
     s = sum > 0.0 ? s / sum : 0.0;
   }
-  if (lane < k) {
-    ids[(int64_t)t * k + lane] = my_id;
-    wts[(int64_t)t * k + lane] = (float)((double)rule.scale * s);
+  const int64_t out = (int64_t)blockIdx.x * 4 + (lane >> 4);
+  if (j < k && out < T) {
+    ids[out * k + j] = p.id[j];
+    wts[out * k + j] = (float)((double)rule.scale * s);
   }
 }
 
@@ -335,9 +366,13 @@ __global__ __launch_bounds__(256) void k_route_scored_bwd(const float* __restric
                                                           int E, int k, RouteRule rule,
                                                           float* __restrict__ dlogits) {
   __shared__ __attribute__((aligned(16))) float rows[4][64 * NPER];
+  __shared__ RowSum sums[4];
+  __shared__ double all_of[4];
+  __shared__ float value[4][16];
+  __shared__ int place[4][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = blockIdx.x * 4 + wave;
-  if (t >= T) return;
+  // rows past T: the last one again, not stored
+  const int t = min((int)blockIdx.x * 4 + wave, T - 1);
   const float* row = logits + (int64_t)t * E;
   float* mine = rows[wave];
   const bool dense = !rule.sigmoid && !rule.renorm;   // every score moves every weight
@@ -347,48 +382,73 @@ __global__ __launch_bounds__(256) void k_route_scored_bwd(const float* __restric
 #pragma unroll
     for (int i = 0; i < NPER; ++i) x[i] = lane + 64 * i < E ? row[lane + 64 * i] : -INFINITY;
     rs = row_sum<NPER>(x, E, lane);
+    if (lane == 0) sums[wave] = rs;
+    __syncthreads();
   }
-  int id = -1;
-  float y = -INFINITY;
-  double g = 0.0;
-  if (lane < k) {
-    const int e = ids[(int64_t)t * k + lane];
-    if (e >= 0 && e < E && wts[(int64_t)t * k + lane] != 0.0f) {
-      id = e;
-      y = row[e];
-      g = (double)rule.scale * (double)dw[(int64_t)t * k + lane];
+  // the picks of four rows at once, 16 lanes each
+  if (wave == 0) {
+    const int w = lane >> 4, j = lane & 15;
+    const int64_t r = min((int64_t)blockIdx.x * 4 + w, (int64_t)T - 1);
+    int id = -1;
+    float y = -INFINITY;
+    double g = 0.0;
+    if (j < k) {
+      const int e = ids[r * k + j];
+      if (e >= 0 && e < E && wts[r * k + j] != 0.0f) {
+        id = e;
+        y = logits[r * E + e];
+        g = (double)rule.scale * (double)dw[r * k + j];
+      }
     }
+    RowSum of = {0.0, 1.0};
+    if (dense) {
+      of = sums[w];
+    } else if (!rule.sigmoid) {
+      // renormalised softmax: only the picks' ratios count
+      float top = masked(y) ? -INFINITY : fminf(y, FLT_MAX);
+      for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+      of.top = (double)top;
+    }
+    const double s = score(y, rule.sigmoid, of);
+    const double rest = rule.sigmoid ? score(-y, true, of) : 1.0;   // 1 - sigmoid, not cancelled
+    double d, all = 0.0;
+    if (rule.renorm) {
+      const double sum = row16_sum64(s);
+      const double p = sum > 0.0 ? s / sum : 0.0;
+      d = p * (g - row16_sum64(g * p)) * rest;
+    } else if (rule.sigmoid) {
+      d = g * s * rest;
+    } else {
+      d = g * s;
+      all = row16_sum64(d);
+    }
+    // the first slot of an expert sums those after it
+    bool first = id >= 0;
+    double v = 0.0;
+    for (int q = 0; q < k; ++q) {
+      const int other = __shfl(id, (lane & 48) + q);
+      const double dq = __shfl(d, (lane & 48) + q);
+      if (other == id) v += dq;
+      if (other == id && q < j) first = false;
+    }
+    place[w][j] = first ? id : -1;
+    value[w][j] = (float)(dense ? v - s * all : v);
+    if (j == 0) all_of[w] = all;
   }
-  // renormalised softmax: only the picks' ratios count
-  if (!rule.sigmoid && rule.renorm) rs.top = (double)wave_max_of(masked(y) ? -INFINITY : fminf(y, FLT_MAX));
-  const double s = score(y, rule.sigmoid, rs);
-  const double rest = rule.sigmoid ? score(-y, true, rs) : 1.0;   // 1 - sigmoid without its cancellation
-  double d, all = 0.0;
-  if (rule.renorm) {
-    const double sum = wave_sum64(s);
-    const double p = sum > 0.0 ? s / sum : 0.0;
-    d = p * (g - wave_sum64(g * p)) * rest;
-  } else if (rule.sigmoid) {
-    d = g * s * rest;
-  } else {
-    d = g * s;
-    all = wave_sum64(d);
-  }
-  // the first slot of an expert sums those after it
-  bool first = id >= 0;
-  double v = 0.0;
-  for (int j = 0; j < k; ++j) {
-    const bool same = __builtin_amdgcn_readlane(id, j) == id;
-    const double dj = __shfl(d, j);
-    if (same) v += dj;
-    if (same && j < lane) first = false;
-  }
+  if (!dense) {
 #pragma unroll
-  for (int i = 0; i < NPER; ++i)
-    mine[lane + 64 * i] = dense ? (float)(-score(x[i], false, rs) * all) : 0.0f;
-  __builtin_amdgcn_wave_barrier();             // the wave's own LDS, in order
-  if (first) mine[id] = (float)(dense ? v - s * all : v);
+    for (int i = 0; i < NPER; ++i) mine[lane + 64 * i] = 0.0f;
+  }
+  __syncthreads();
+  if (dense) {
+    const double all = all_of[wave];
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) mine[lane + 64 * i] = (float)(-score(x[i], false, rs) * all);
+    __builtin_amdgcn_wave_barrier();           // the wave's own LDS, in order
+  }
+  if (lane < 16 && place[wave][lane] >= 0) mine[place[wave][lane]] = value[wave][lane];
   __builtin_amdgcn_wave_barrier();
+  if ((int)blockIdx.x * 4 + wave >= T) return;
   float* out = dlogits + (int64_t)t * E;
   if ((E & 3) == 0 && ((uintptr_t)dlogits & 15) == 0) {
     for (int q = lane; q < E / 4; q += 64) ((f32x4*)out)[q] = ((const f32x4*)mine)[q];
