@@ -87,11 +87,15 @@ __device__ __forceinline__ double score(float x, bool sigmoid, const RowSum& rs)
 // product counts by s (1 - s) |x| <= 0.23) and the sum with the bias by 2^-24
 // of itself; softmax scores carry the error of their sum too, at most 1.7e-6 of
 // a score for 1024 experts, and two of them add to at most one.  So two values are
-// told apart if they differ by kApart (1 + |c|), and two groups, whose worth
-// may be the sum of two values, by twice that.
+// told apart if they differ by kApart (1 + |c|) and what their keys (below)
+// leave of them, and two groups, whose worth may be the sum of two values, by
+// 2 kApart (1 + |c|).
 namespace {
 
 constexpr float kApart = 2e-6f;
+
+// slots of a lane, as a power of two
+constexpr int slots_of(int nper) { return nper <= 1 ? 1 : nper <= 2 ? 2 : nper <= 4 ? 4 : nper <= 8 ? 8 : 16; }
 
 __device__ __forceinline__ float wave_max_of(float a) {
   const auto x = [](int v, int w) { return fmaxf(__int_as_float(v), __int_as_float(w)); };
@@ -178,37 +182,84 @@ __device__ __forceinline__ bool limit_to_groups(F (&v)[NPER], F* mine, int E, co
   return sure;
 }
 
-// The quick form: false where values are too close or the masks leave fewer
-// than k experts.
+// A choice value as an integer of the same order, its low bits replaced by the
+// slot it stands in: comparing, sorting and naming the winner are then integer
+// maxima.  The slot moves the value by less than NPER units in the last place.
+constexpr int kNone = INT32_MIN;
 template <int NPER>
-__device__ __forceinline__ bool choose(float (&v)[NPER], float* mine, int E, int k,
+__device__ __forceinline__ int to_key(float c, int slot) {
+  const int b = __float_as_int(c);
+  const int ordered = b ^ ((b >> 31) & 0x7FFFFFFF);
+  return c > -INFINITY ? ((ordered & ~(slots_of(NPER) - 1)) | slot) : kNone;
+}
+__device__ __forceinline__ float key_value(int key) {
+  return __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF));
+}
+
+template <int CTRL>
+__device__ __forceinline__ int max_with(int a) {
+  return max(a, __builtin_amdgcn_update_dpp(a, a, CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ int wave_max_of(int a) {
+  a = max_with<0xB1>(a);
+  a = max_with<0x4E>(a);
+  a = max_with<0x141>(a);
+  a = max_with<0x140>(a);
+  auto r = __builtin_amdgcn_permlane16_swap((uint32_t)a, (uint32_t)a, false, false);
+  a = max((int)r[0], (int)r[1]);
+  r = __builtin_amdgcn_permlane32_swap((uint32_t)a, (uint32_t)a, false, false);
+  return max((int)r[0], (int)r[1]);
+}
+
+// sorts a lane's keys, largest first: Batcher's odd-even merge network, without
+// the comparators that reach past the end
+template <int NPER>
+__device__ __forceinline__ void sort_keys(int (&v)[NPER]) {
+#pragma unroll
+  for (int p = 1; p < NPER; p *= 2)
+#pragma unroll
+    for (int q = p; q > 0; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < NPER; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < NPER && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const int hi = max(v[i + j], v[i + j + q]);
+            v[i + j + q] = min(v[i + j], v[i + j + q]);
+            v[i + j] = hi;
+          }
+}
+
+// The quick form: false where values are too close or the masks leave fewer
+// than k experts.  With each lane's keys sorted, a pick is the largest of the
+// lanes' first ones and a shift in the lane that had it.
+template <int NPER>
+__device__ __forceinline__ bool choose(float (&c)[NPER], float* mine, int E, int k,
                                        const RouteRule& rule, int lane, int& my_id) {
-  if (!limit_to_groups<NPER, float>(v, mine, E, rule, lane)) return false;
-  float my_value = -INFINITY;
+  if (!limit_to_groups<NPER, float>(c, mine, E, rule, lane)) return false;
+  int v[NPER];
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) v[i] = to_key<NPER>(c[i], i);
+  sort_keys<NPER>(v);
+  int my_key = kNone;
   // one round more than picks: the first that stays out has to be apart too
   for (int j = 0; j <= k; ++j) {
-    float m = v[0];
-#pragma unroll
-    for (int i = 1; i < NPER; ++i) m = fmaxf(m, v[i]);
-    const float local = m;
-    m = wave_max_of(m);
-    const int w = (int)__builtin_ctzll(__ballot(local == m));
+    const int m = wave_max_of(v[0]);
     // one expert goes: an equal one stays, and shows as too close a call
-    int at = lane == w ? -1 : 0;
+    const int w = (int)__builtin_ctzll(__ballot(v[0] == m));
+    // as masks: selections become an index into v, and that a chain of them
+    const int won = lane == w ? -1 : 0;
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-      const bool hit = at < 0 && v[i] == m;
-      at = hit ? 64 * i : at;
-      v[i] = hit ? -INFINITY : v[i];
-    }
-    const int win = __builtin_amdgcn_readlane(at, w) + w;
-    my_id = lane == j ? win : my_id;
-    my_value = lane == j ? m : my_value;
+    for (int i = 0; i < NPER; ++i) v[i] = ((i + 1 < NPER ? v[i + 1] : kNone) & won) | (v[i] & ~won);
+    my_id = lane == j ? w : my_id;
+    my_key = lane == j ? m : my_key;
   }
-  const float next = __shfl_down(my_value, 1);
-  const bool apart = next == -INFINITY
-                         ? lane == k - 1 && my_value > -INFINITY    // none left to be close to
-                         : my_value - next > kApart * (1.0f + fabsf(my_value) + fabsf(next));
+  my_id += 64 * (my_key & (slots_of(NPER) - 1));
+  const int next = __shfl_down(my_key, 1);
+  const float a = key_value(my_key), b = key_value(next);
+  const bool apart = next == kNone ? lane == k - 1 && my_key != kNone    // none left to be close to
+                                   : a - b > kApart * (1.0f + fabsf(a) + fabsf(b)) +
+                                                 slots_of(NPER) * 0x1p-23f * fmaxf(fabsf(a), fabsf(b));
   return __ballot(lane < k && !apart) == 0;
 }
 
@@ -274,43 +325,57 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
                                                       float* __restrict__ wts) {
   extern __shared__ double choice[];           // [4 waves][E]: only with groups
   __shared__ Picked picked[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // rows past T: the last one again, not stored
   const int t = min((int)blockIdx.x * 4 + wave, T - 1);
   const float* row = logits + (int64_t)t * E;
   double* mine = choice + (int64_t)wave * E;
   float x[NPER], add[NPER];
+  const uint32_t last = E - 1;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) x[i] = row[min((uint32_t)(lane + 64 * i), last)];
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) add[i] = 0.0f;
+  if (bias) {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) add[i] = bias[min((uint32_t)(lane + 64 * i), last)];
+  }
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
-    const int e = lane + 64 * i;
-    x[i] = e < E ? row[e] : -INFINITY;
-    add[i] = bias && e < E ? bias[e] : 0.0f;
+    x[i] = lane + 64 * i < E ? x[i] : -INFINITY;
     // masked: by its logit or its bias
-    if (masked(x[i]) || masked(add[i])) add[i] = -INFINITY;
+    add[i] = masked(x[i]) | masked(add[i]) ? -INFINITY : add[i];
   }
   int my_id = 0;
   bool my_live = false, sure;
   {
-    float c[NPER], sum = 1.0f, top = 0.0f;
-    if (!rule.sigmoid) {
-      top = -INFINITY;
+    float c[NPER];
+    if (rule.sigmoid) {
 #pragma unroll
       for (int i = 0; i < NPER; ++i)
-        if (!masked(x[i])) top = fmaxf(top, fminf(x[i], FLT_MAX));
+        c[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
+    } else {
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) {
+        c[i] = masked(x[i]) ? -INFINITY : fminf(x[i], FLT_MAX);
+        top = fmaxf(top, c[i]);
+      }
       top = wave_max_of(top);
-      sum = 0.0f;
+      float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NPER; ++i)
-        if (!masked(x[i])) sum += __expf(fminf(x[i], FLT_MAX) - top);
+      for (int i = 0; i < NPER; ++i) {
+        c[i] = __expf(c[i] - top);
+        sum += c[i];
+      }
       for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
-    }
+      const float inv = __builtin_amdgcn_rcpf(sum);
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-      const float y = fminf(x[i], FLT_MAX);
-      const float s = rule.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-y))
-                                   : __expf(y - top) * __builtin_amdgcn_rcpf(sum);
-      c[i] = masked(add[i]) ? -INFINITY : s + add[i];
+      for (int i = 0; i < NPER; ++i) c[i] *= inv;
     }
+    // a masked expert's score may be anything, its value is -Inf
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) c[i] = masked(add[i]) ? -INFINITY : c[i] + add[i];
     sure = choose<NPER>(c, (float*)mine, E, k, rule, lane, my_id);
     my_live = sure;
   }
@@ -370,7 +435,7 @@ __global__ __launch_bounds__(256) void k_route_scored_bwd(const float* __restric
   __shared__ double all_of[4];
   __shared__ float value[4][16];
   __shared__ int place[4][16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // rows past T: the last one again, not stored
   const int t = min((int)blockIdx.x * 4 + wave, T - 1);
   const float* row = logits + (int64_t)t * E;
