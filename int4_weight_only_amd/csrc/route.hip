@@ -75,7 +75,8 @@ __device__ __forceinline__ double score(float x, bool sigmoid, const RowSum& rs)
 }  // namespace
 
 // ------------------------------------------------------------- selection --
-// NPER experts per lane; expert lane + 64 i is the lane's i-th.
+// NPER experts per lane; expert lane + 64 i is the lane's i-th, or NPER lane + i
+// where the groups allow it.
 // v: choice values, -Inf for masked experts.  Lane j < k gets pick j: its id, and
 // whether it is one (slots without an expert left hold the lowest untaken
 // indices).
@@ -121,36 +122,74 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// Groups that stay, as a mask of groups; also whether that is certain.
-// `mine`: the row's choice values in LDS.  2^n lanes share a group.
-template <class F>
-__device__ __forceinline__ uint64_t kept_groups(const F* mine, int E, const RouteRule& rule, int lane,
-                                                bool& sure) {
+// a lane of the other half of 2 D lanes whose halves each hold one value
+template <int D, class F>
+__device__ __forceinline__ F from_other(F a) {
+  if constexpr (D >= 16) {
+    return __shfl_xor(a, D);
+  } else {
+    constexpr int ctrl = D == 1 ? 0xB1 : D == 2 ? 0x4E : D == 4 ? 0x141 : 0x140;
+    if constexpr (sizeof(F) == 8) {
+      return dpp64<ctrl>(a);
+    } else {
+      const int v = __float_as_int(a);
+      return __int_as_float(__builtin_amdgcn_update_dpp(v, v, ctrl, 0xF, 0xF, true));
+    }
+  }
+}
+// the two largest, a >= b, of this and the other half
+template <int D, class F>
+__device__ __forceinline__ void join_two(F& a, F& b) {
+  const F a2 = from_other<D>(a), b2 = from_other<D>(b);
+  b = max(max(b, b2), min(a, a2));
+  a = max(a, a2);
+}
+
+// Masks the experts of the groups that go; whether that is certain.
+// `share` lanes, a power of two, hold each group's worth.  A lane's experts are
+// `NPER` consecutive ones if `in_lanes`: its group is then `share` lanes' own
+// registers.  Otherwise they are 64 apart and go through LDS.
+template <int NPER, class F>
+__device__ __forceinline__ bool limit_to_groups(F (&v)[NPER], F* mine, int E, const RouteRule& rule,
+                                                int lane, bool in_lanes) {
+  if (rule.groups == 1) return true;
   const F none = (F)-INFINITY;
   const int per = E / rule.groups;
-  int share = 1;
-  while (2 * share * rule.groups <= 64) share *= 2;
-  const int g = lane / share;
+  const int bits = 31 - __builtin_clz(64 / rule.groups), share = 1 << bits;
+  const int g = lane >> bits;
   F a = none, b = none;                        // the two largest
-  if (g < rule.groups)
-    for (int q = lane % share; q < per; q += share) {
-      const F v = mine[g * per + q];
-      b = max(b, min(a, v));
-      a = max(a, v);
+  if (in_lanes) {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      b = max(b, min(a, v[i]));
+      a = max(a, v[i]);
     }
-  for (int d = 1; d < share; d *= 2) {
-    const F a2 = __shfl_xor(a, d), b2 = __shfl_xor(b, d);
-    b = max(max(b, b2), min(a, a2));
-    a = max(a, a2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i)
+      if (lane + 64 * i < E) mine[lane + 64 * i] = v[i];
+    __builtin_amdgcn_wave_barrier();           // the wave's own LDS, in order
+    if (g < rule.groups)
+      for (int q = lane & (share - 1); q < per; q += share) {
+        const F c = mine[g * per + q];
+        b = max(b, min(a, c));
+        a = max(a, c);
+      }
+    __builtin_amdgcn_wave_barrier();
   }
-  F worth = rule.group_top == 2 && b > none ? a + b : a;
-  worth = __shfl(worth, (lane * share) & 63);  // lane g: group g
+  if (share > 1) join_two<1>(a, b);
+  if (share > 2) join_two<2>(a, b);
+  if (share > 4) join_two<4>(a, b);
+  if (share > 8) join_two<8>(a, b);
+  if (share > 16) join_two<16>(a, b);
+  const F worth = rule.group_top == 2 && b > none ? a + b : a;
   int rank = 0;
   for (int o = 0; o < rule.groups; ++o) {
-    const F other = lane_value(worth, o);
-    rank += other > worth || (other == worth && o < lane);
+    const F other = lane_value(worth, o << bits);
+    rank += (other > worth) | ((other == worth) & (o < g));
   }
-  const bool group = lane < rule.groups;
+  const bool group = g < rule.groups;
+  bool sure = true;
   if (sizeof(F) == 4 && rule.topk_groups < rule.groups) {
     // the worth of the last that stays and of the first that goes
     const uint64_t last = __ballot(group && rank == rule.topk_groups - 1);
@@ -159,26 +198,20 @@ __device__ __forceinline__ uint64_t kept_groups(const F* mine, int E, const Rout
     const F out = lane_value(worth, (int)__builtin_ctzll(next));
     if (out > none && !(in - out > (F)(2 * kApart) * (1 + fabs(in) + fabs(out)))) sure = false;
   }
-  return __ballot(group && rank < rule.topk_groups);
-}
-
-// Masks the experts of the groups that go; whether that is certain.
-template <int NPER, class F>
-__device__ __forceinline__ bool limit_to_groups(F (&v)[NPER], F* mine, int E, const RouteRule& rule,
-                                                int lane) {
-  if (rule.groups == 1) return true;
-  bool sure = true;
+  const uint64_t keep = __ballot(rank < rule.topk_groups);
+  if (in_lanes) {
+    const F limit = rank < rule.topk_groups ? (F)INFINITY : none;
 #pragma unroll
-  for (int i = 0; i < NPER; ++i)
-    if (lane + 64 * i < E) mine[lane + 64 * i] = v[i];
-  __builtin_amdgcn_wave_barrier();             // the wave's own LDS, in order
-  const uint64_t keep = kept_groups(mine, E, rule, lane, sure);
-  __builtin_amdgcn_wave_barrier();
-  // e / per as a product: exact for e, per <= 1024
-  const uint32_t m = ((1u << 20) + E / rule.groups - 1) / (E / rule.groups);
+    for (int i = 0; i < NPER; ++i) v[i] = min(v[i], limit);
+  } else {
+    // e / per as a product: exact for e, per <= 1024
+    const uint32_t m = ((1u << 20) + per - 1) / per;
 #pragma unroll
-  for (int i = 0; i < NPER; ++i)
-    if (!((keep >> (((lane + 64 * i) * m) >> 20 & 63)) & 1)) v[i] = (F)-INFINITY;
+    for (int i = 0; i < NPER; ++i) {
+      const int of = (int)(((lane + 64 * i) * m) >> 20) << bits;
+      if (!((keep >> (of & 63)) & 1)) v[i] = none;
+    }
+  }
   return sure;
 }
 
@@ -235,8 +268,8 @@ __device__ __forceinline__ void sort_keys(int (&v)[NPER]) {
 // lanes' first ones and a shift in the lane that had it.
 template <int NPER>
 __device__ __forceinline__ bool choose(float (&c)[NPER], float* mine, int E, int k,
-                                       const RouteRule& rule, int lane, int& my_id) {
-  if (!limit_to_groups<NPER, float>(c, mine, E, rule, lane)) return false;
+                                       const RouteRule& rule, int lane, bool in_lanes, int& my_id) {
+  if (!limit_to_groups<NPER, float>(c, mine, E, rule, lane, in_lanes)) return false;
   int v[NPER];
 #pragma unroll
   for (int i = 0; i < NPER; ++i) v[i] = to_key<NPER>(c[i], i);
@@ -254,7 +287,8 @@ __device__ __forceinline__ bool choose(float (&c)[NPER], float* mine, int E, int
     my_id = lane == j ? w : my_id;
     my_key = lane == j ? m : my_key;
   }
-  my_id += 64 * (my_key & (slots_of(NPER) - 1));
+  const int slot = my_key & (slots_of(NPER) - 1);
+  my_id = in_lanes ? NPER * my_id + slot : my_id + 64 * slot;
   const int next = __shfl_down(my_key, 1);
   const float a = key_value(my_key), b = key_value(next);
   const bool apart = next == kNone ? lane == k - 1 && my_key != kNone    // none left to be close to
@@ -267,7 +301,7 @@ template <int NPER>
 __device__ __forceinline__ void choose_exactly(double (&v)[NPER], double* mine, int E, int k,
                                                const RouteRule& rule, int lane, int& my_id,
                                                bool& my_live) {
-  limit_to_groups<NPER, double>(v, mine, E, rule, lane);
+  limit_to_groups<NPER, double>(v, mine, E, rule, lane, false);
   uint32_t free = 0;
 #pragma unroll
   for (int i = 0; i < NPER; ++i) free |= lane + 64 * i < E ? 1u << i : 0u;
@@ -307,6 +341,28 @@ struct Picked {
   int id[16];
 };
 
+// A lane's logits and biases, experts first, first + step, ...; a masked expert's
+// bias is -Inf.
+template <int NPER>
+__device__ __forceinline__ void load_row(const float* row, const float* bias, int E, int first,
+                                         int step, float (&x)[NPER], float (&add)[NPER]) {
+  const uint32_t last = E - 1;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) x[i] = row[min((uint32_t)(first + step * i), last)];
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) add[i] = 0.0f;
+  if (bias) {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) add[i] = bias[min((uint32_t)(first + step * i), last)];
+  }
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    x[i] = first + step * i < E ? x[i] : -INFINITY;
+    // masked: by its logit or its bias
+    add[i] = masked(x[i]) | masked(add[i]) ? -INFINITY : add[i];
+  }
+}
+
 // sum over each row of 16 lanes, in every lane of it, in one fixed order
 __device__ __forceinline__ double row16_sum64(double a) {
   a += dpp64<0xB1>(a);
@@ -330,22 +386,10 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
   const int t = min((int)blockIdx.x * 4 + wave, T - 1);
   const float* row = logits + (int64_t)t * E;
   double* mine = choice + (int64_t)wave * E;
+  // whole groups in neighbouring lanes: a lane holds consecutive experts
+  const bool in_lanes = rule.groups > 1 && E == 64 * NPER && (rule.groups & (rule.groups - 1)) == 0;
   float x[NPER], add[NPER];
-  const uint32_t last = E - 1;
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) x[i] = row[min((uint32_t)(lane + 64 * i), last)];
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) add[i] = 0.0f;
-  if (bias) {
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) add[i] = bias[min((uint32_t)(lane + 64 * i), last)];
-  }
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) {
-    x[i] = lane + 64 * i < E ? x[i] : -INFINITY;
-    // masked: by its logit or its bias
-    add[i] = masked(x[i]) | masked(add[i]) ? -INFINITY : add[i];
-  }
+  load_row<NPER>(row, bias, E, in_lanes ? NPER * lane : lane, in_lanes ? 1 : 64, x, add);
   int my_id = 0;
   bool my_live = false, sure;
   {
@@ -368,7 +412,12 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
         c[i] = __expf(c[i] - top);
         sum += c[i];
       }
-      for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+      sum += from_other<1>(sum);
+      sum += from_other<2>(sum);
+      sum += from_other<4>(sum);
+      sum += from_other<8>(sum);
+      sum += from_other<16>(sum);
+      sum += from_other<32>(sum);
       const float inv = __builtin_amdgcn_rcpf(sum);
 #pragma unroll
       for (int i = 0; i < NPER; ++i) c[i] *= inv;
@@ -376,12 +425,13 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
     // a masked expert's score may be anything, its value is -Inf
 #pragma unroll
     for (int i = 0; i < NPER; ++i) c[i] = masked(add[i]) ? -INFINITY : c[i] + add[i];
-    sure = choose<NPER>(c, (float*)mine, E, k, rule, lane, my_id);
+    sure = choose<NPER>(c, (float*)mine, E, k, rule, lane, in_lanes, my_id);
     my_live = sure;
   }
   RowSum rs = {0.0, 1.0};
   if (!rule.sigmoid) {
     if (!sure || !rule.renorm) {
+      load_row<NPER>(row, bias, E, lane, 64, x, add);
       rs = row_sum<NPER>(x, E, lane);
     } else {
       // renormalised: the picks' own largest logit will do
@@ -390,6 +440,7 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
     }
   }
   if (!sure) {
+    if (rule.sigmoid) load_row<NPER>(row, bias, E, lane, 64, x, add);
     double c[NPER];
 #pragma unroll
     for (int i = 0; i < NPER; ++i)
