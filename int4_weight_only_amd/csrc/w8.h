@@ -24,7 +24,7 @@ __host__ __device__ __forceinline__ int64_t w8_cols(int64_t K) { return (K + 511
 __host__ __device__ __forceinline__ int64_t w8_blocks(int64_t n) { return (n + 127) / 128; }
 
 // D[16x16] += A[16x128] * B[128x16] of e4m3 codes, fp32 accumulation, one
-// scale byte per operand row (byte SA of sa, SB of sb).  Lane l supplies 32
+// scale byte per operand row (the low one of sa, sb).  Lane l supplies 32
 // bytes of A row (l % 16) and of B column (l % 16); lanes l / 16 = 0..3
 // split the 128 elements of the block between them, in any order that A and
 // B share (one scale covers the whole block).  It receives
@@ -34,9 +34,8 @@ __host__ __device__ __forceinline__ int64_t w8_blocks(int64_t n) { return (n + 1
 // (measured; the older 16x16x32 fp8 form does the same).  Exact products
 // would need the codes widened to bf16, at half the matrix rate and twice
 // the operand traffic, to move a result by less than its bf16 rounding.
-template <int SA = 0, int SB = 0>
 __device__ __forceinline__ f32x4 mfma8_16(i32x8 a, i32x8 b, f32x4 c, uint32_t sa, uint32_t sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, SA, (int)sa, SB, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, (int)sa, 0, (int)sb);
 }
 
 __device__ __forceinline__ i32x8 join16(u32x4 lo, u32x4 hi) {
@@ -71,15 +70,17 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
 // silu(g) * u = g / (1 + e^-g) * u.  The exponential is 2^t with t = -g log2 e
 // as a product and its remainder, so that it holds to about two units in the
 // last place for every g; v_exp_f32 and v_rcp_f32 give one unit each.  (The
-// rounding to e4m3 that follows is 2^19 times coarser; the exactly rounded
-// division and expf cost the quantizer 10 us of 78 at 32775 x 2000.)
+// rounding to e4m3 that follows is 2^19 times coarser; with the exactly rounded
+// division and expf the quantizer took 78 us at 32775 x 2000, 59 now.)  The
+// quarters keep the reciprocal of 1 + e^-g a normal number, which v_rcp_f32
+// would flush to zero from e^-g = 2^126 on.
 __device__ __forceinline__ float silu_mul_fast(float g, float u) {
   constexpr float kLog2e = 1.44269502f, kRest = 1.92596299e-8f, kLn2 = 0.693147182f;
   const float t = -g * kLog2e;
   const float r = __builtin_fmaf(-g, kLog2e, -t) - g * kRest;
   float e = __builtin_amdgcn_exp2f(t);
   e = e < INFINITY && e > 0.0f ? __builtin_fmaf(e, r * kLn2, e) : e;
-  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+  return 0.25f * g * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.25f, 0.25f)) * u;
 }
 
 hipError_t launch_w8_quantize_rows(const uint16_t* X, int64_t M, int64_t K, uint8_t* X8,

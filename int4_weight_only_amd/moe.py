@@ -34,6 +34,7 @@ of the pages' rollout comparison) behind the scored router:
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (moe_align_block_size, w4_moe_align_capacity, w4_moe_combine_workspace_words,
                w4_moe_route, w4_moe_sum, w4a16_moe_gemm_combine,
@@ -248,6 +249,7 @@ class RouteScored(torch.autograd.Function):
         return ids, w
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _, grad_w):
         logits, ids, w = ctx.saved_tensors
         return (w4_moe_route_scored_bwd(logits, ids, w, grad_w.contiguous(), *ctx.rule),
@@ -336,9 +338,9 @@ def alloc_buffers_w8(T, k, E, H, I, B, device):
 def moe_forward_w8(X, topk_ids, topk_weights, gate_up, down, B=None, buffers=None):
     """Expert part of the layer for routed tokens on 8-bit experts.
 
-    X bf16 [T, H]; topk_ids int32 [T, k]; topk_weights fp32 [T, k]; gate_up:
-    E experts of [2I, H]; down: E experts of [H, I] (``ExpertWeightsW8``).  B
-    defaults to ``w8_pick_block_size``.  Returns (Out bf16 [T, H], buffers).
+    X bf16 [T, H]; topk_ids int32 [T, k], all in [0, E); topk_weights fp32 [T,
+    k]; gate_up: E experts of [2I, H]; down: E experts of [H, I]
+    (``ExpertWeightsW8``).  B defaults to ``w8_pick_block_size``.  Returns (Out bf16 [T, H], buffers).
     """
     T, H = X.shape
     k = topk_ids.shape[1]
@@ -354,6 +356,8 @@ def moe_forward_w8(X, topk_ids, topk_weights, gate_up, down, B=None, buffers=Non
     if _fuses_swiglu_w8(T, H, I, B):
         w8a8_moe_gemm_swiglu(b.X8, b.SX, gate_up.W8, gate_up.SW, *plan, T, k, B, k, b.A8, b.SA)
     else:
+        if b.H1 is None:
+            raise ValueError("these sizes need buffers with H1 (allocated for the same B)")
         w8a8_moe_gemm(b.X8, b.SX, gate_up.W8, gate_up.SW, *plan, T, k, B, k, out=b.H1)
         w8_silu_mul_quantize(b.H1, b.A8, b.SA)
     w8a8_moe_gemm(b.A8, b.SA, down.W8, down.SW, *plan, T, k, B, 1, out=b.H2)

@@ -12,10 +12,13 @@ identity, so
                                     the same call
   dW = dY^T * X                     bf16, unquantized operands
                                     (``w4_bf16_transpose``, ``w4_bf16_gemm_nt``)
-The master weight stays bf16.
+The master weight stays bf16.  The backward is not differentiable again.  To
+capture a backward into a graph, take gradients with ``torch.autograd.grad``, or
+let no eager graph of the same leaves be alive.
 """
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (w4_bf16_gemm_nt, w4_bf16_transpose, w8_quantize_blocks, w8_quantize_rows, w8a8_gemm)
 
@@ -42,6 +45,7 @@ class W8Linear(torch.autograd.Function):
         return Y.reshape(*X.shape[:-1], N)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         X2, WT8, ST = ctx.saved_tensors
         dY = grad_out.reshape(-1, ctx.n).to(torch.bfloat16).contiguous()

@@ -76,6 +76,53 @@ def test_masks_infinities_and_ties(rule):
     assert all(len(set(r)) == k for r in ids)
 
 
+@pytest.mark.parametrize("E,k,groups,topk_groups", [(64, 4, 8, 3), (128, 8, 8, 4), (256, 8, 32, 3), (384, 6, 64, 2), (512, 16, 2, 1),
+                                                    (1024, 5, 16, 5), (24, 4, 3, 2), (384, 8, 6, 3), (64, 2, 64, 5), (90, 6, 10, 4)])
+@pytest.mark.parametrize("sigmoid,group_top", [(True, 2), (False, 1)])
+def test_groups_in_every_layout(E, k, groups, topk_groups, sigmoid, group_top):
+    # a group in neighbouring lanes' registers or in LDS, with masked experts,
+    # masked groups, equal groups and rows of few experts
+    rule = dict(sigmoid=sigmoid, groups=groups, topk_groups=topk_groups, group_top=group_top, bias=True)
+    say(f"route_scored groups E={E} k={k} {rule}")
+    lg = synth.router_logits(12, E, 6).numpy().copy()
+    per = E // groups
+    lg[1, :per] = -np.inf
+    lg[2, per:] = -np.inf
+    lg[3, ::2] = np.nan
+    lg[4] = 0
+    lg[5, :] = np.tile(lg[5, :per], groups)
+    lg[6, 1:] = -np.inf
+    lg[7, E - per:] += 50
+    lg[8, :] = -np.inf
+    lg[9, E - 1] = np.inf
+    check(lg, k, rule)
+    check(lg, k, dict(rule, bias=np.zeros(E, np.float32)))
+    assert topk_groups * per >= k
+
+
+def test_many_rows_with_groups_agree_with_64_bits():
+    T, E, k, groups, kept = 20000, 256, 8, 8, 4
+    lg = torch.randn(T, E, generator=torch.Generator().manual_seed(4)).to(dev())
+    b = (torch.randn(E, generator=torch.Generator().manual_seed(5)) * 0.05).to(dev())
+    say("route_scored many rows with groups")
+    ids, _ = w4.w4_moe_route_scored(lg, k, sigmoid=True, bias=b, groups=groups, topk_groups=kept, group_top=2)
+    c = (torch.sigmoid(lg.double()) + b.double()).view(T, groups, E // groups)
+    worth = torch.sort(c, dim=2, descending=True).values[:, :, :2].sum(2)
+    best = torch.sort(worth, dim=1, descending=True, stable=True).indices[:, :kept]
+    keep = torch.zeros(T, groups, dtype=torch.bool, device=dev()).scatter_(1, best, True)
+    c = torch.where(keep[:, :, None], c, -torch.inf).view(T, E)
+    ref = torch.sort(c, dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(ids.long(), ref)
+
+
+def test_refuses_second_derivatives():
+    x = synth.router_logits(3, 16, 7).to(dev()).requires_grad_()
+    say("route_scored second derivative")
+    g, = torch.autograd.grad(moe.route_scored(x, 2)[1].square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
 def test_single_expert_and_empty():
     say("route_scored E=1")
     ids, w = w4.w4_moe_route_scored(torch.zeros(3, 1, device=dev()), 1, sigmoid=True, renorm=False)

@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import int4_weight_only_amd as w4
-from int4_weight_only_amd import moe, w8
+from int4_weight_only_amd import _lib, moe, w8
 import synth
 from gpu_util import dev, down, say, up, up_bits
 from oracle import bf16, moe as omoe, w8 as ow8
@@ -136,6 +136,24 @@ def test_silu_mul_quantize(R, I):
             assert np.all(np.abs(y - v) <= np.maximum(np.abs(v) * 2.0 ** -4, step * 2.0 ** -10)
                           + slack * np.abs(v) + 2.0 ** -126)
     assert np.all(s[:, -(-I // 128):] == 127)
+
+
+def test_silu_far_negative_gates():
+    # 1 / (1 + e^-g) below the smallest normal number, times a large u
+    R, I = 3, 256
+    h = np.zeros((R, 2 * I), np.float32)
+    h[:, :I] = np.linspace(-88.5, -84.0, I)
+    h[:, I:] = np.array([1.0, 2.0 ** 60, 2.0 ** 120])[:, None]
+    b = synth.bits(torch.from_numpy(h).to(torch.bfloat16))
+    say("silu_mul_quantize far negative gates")
+    q, s = (bytes_of(t) for t in w4.w8_silu_mul_quantize(up_bits(b)))
+    a = ow8.silu_mul(b)
+    for r in range(R):
+        for c in range(0, I, 128):
+            v, step = a[r, c:c + 128], 2.0 ** (int(s[r, c // 128]) - 127.0)
+            y = ow8.e4m3_values(q[r, c:c + 128]) * step
+            # half a step of e4m3 and the slack of test_silu_mul_quantize
+            assert np.all(np.abs(y - v) <= np.maximum(np.abs(v) * 2.0 ** -4, step * 2.0 ** -10) + 2.0 ** -18 * np.abs(v))
 
 
 # ---------------------------------------------------------------- product --
@@ -461,3 +479,142 @@ def test_layer_graph_replay(T):
         torch.cuda.synchronize()
         got = buf.out.clone()
         assert torch.equal(got, call(None)), f"replay {r}"
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 144, 272), (300, 256, 512)])
+def test_linear_backward_graph_replay(M, N, K):
+    X, W = synth.activations(M, K, 18).to(dev()).requires_grad_(), synth.weights(N, K, 18).to(dev()).requires_grad_()
+    dY = synth.activations(M, N, 19).to(dev())
+
+    def call():
+        return torch.autograd.grad(w8.w8_linear(X, W), (X, W), dY)
+    say(f"w8_linear backward graph {M}x{N}x{K}")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = call()
+    for r in range(4):
+        with torch.no_grad():
+            X.copy_(synth.activations(M, K, 40 + r, device=dev()))
+            W.copy_(synth.weights(N, K, 40 + r, device=dev()))
+            dY.copy_(synth.activations(M, N, 50 + r, device=dev()))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured]
+        for a, b in zip(got, call()):
+            assert torch.equal(a, b), f"replay {r}"
+
+
+def test_layers_on_two_streams_at_once():
+    E, k, H, I = 6, 2, 256, 144
+    say("moe_layer_w8 on two streams at once")
+    cases = [layer_case(T, E, k, H, I, 20 + T) for T in (300, 257)]
+    cases = [(X.to(dev()), lg.to(dev()), g, d) for X, lg, _, _, g, d in cases]
+    want = [moe.moe_layer_w8(X, lg, k, g, d)[0].clone() for X, lg, g, d in cases]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cases], [[], []]
+    for _ in range(5):
+        for i, (X, lg, g, d) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(moe.moe_layer_w8(X, lg, k, g, d)[0])
+    torch.cuda.synchronize()
+    for i, w in enumerate(want):
+        assert all(torch.equal(t, w) for t in got[i])
+
+
+def test_linear_refuses_second_derivatives_and_takes_no_rows():
+    X, W = synth.activations(6, 64, 21).to(dev()).requires_grad_(), synth.weights(16, 64, 21).to(dev()).requires_grad_()
+    say("w8_linear second derivative, no rows")
+    dx, = torch.autograd.grad(w8.w8_linear(X, W).float().square().sum(), X, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.float().sum().backward()
+    x0 = torch.zeros(0, 64, dtype=torch.bfloat16, device=dev(), requires_grad=True)
+    y = w8.w8_linear(x0, W)
+    dx, dw = torch.autograd.grad(y, (x0, W), torch.zeros_like(y))
+    assert y.shape == (0, 16) and dx.shape == (0, 64) and not dw.any()
+
+
+def test_layer_refuses_buffers_of_another_block_size():
+    T, E, k, H, I = 700, 2, 2, 128, 256
+    X, lg, _, _, g, d = layer_case(T, E, k, H, I, 22)
+    ids, w = w4.w4_moe_route_scored(lg.to(dev()), k)
+    say("moe_forward_w8 buffers of another B")
+    with pytest.raises(ValueError):
+        moe.moe_forward_w8(X.to(dev()), ids, w, g, d, B=64, buffers=moe.alloc_buffers_w8(T, k, E, H, I, 256, dev()))
+    with pytest.raises(ValueError):
+        moe.moe_forward_w8(X.to(dev()), ids, w, g, d, B=256, buffers=moe.alloc_buffers_w8(T, k, E, H, I, 16, dev()))
+
+
+# ------------------------------------------------------ offsets past 32 bits --
+# One nonzero product per output: exact in any order.
+
+ONE = 0x38                                       # e4m3 1.0
+
+
+def test_wide_product_operands():
+    M, N, K = 600, 16, (1 << 22) - 16            # X8 2.5 GB
+    say("w8a8_gemm / w8a8_moe_gemm of 2.5 GB")
+    x = torch.zeros(M, K, dtype=torch.uint8, device=dev())
+    at = torch.arange(M, device=dev()) * 6991 + 5
+    x[torch.arange(M, device=dev()), at] = ONE
+    w = torch.zeros(N, K, dtype=torch.uint8, device=dev())
+    w[:, at] = torch.arange(N, device=dev(), dtype=torch.uint8)[:, None] + ONE
+    values = torch.from_numpy(ow8.e4m3_values(np.arange(ONE, ONE + N, dtype=np.uint8)).astype(np.float32)).to(dev())
+    sx = torch.full((M, w4.w8_scale_cols(K)), 127, dtype=torch.uint8, device=dev())
+    sx[M - 1] = 129
+    sw = torch.full((1, w4.w8_scale_cols(K)), 127, dtype=torch.uint8, device=dev())
+    want = values.expand(M, N).clone()
+    want[M - 1] *= 4
+    x, w, sx, sw = x.view(E4M3), w.view(E4M3), sx.view(E8M0), sw.view(E8M0)
+    assert torch.equal(w4.w8a8_gemm(x, sx, w, sw).float(), want)
+    ids = torch.zeros(M, 1, dtype=torch.int32, device=dev())
+    for B in (16, 64, 256):
+        plan = w4.moe_align_block_size(ids, 1, B)
+        assert torch.equal(w4.w8a8_moe_gemm(x, sx, w[None], sw[None], *plan, M, 1, B, 1).float(), want)
+    with pytest.raises(_lib.W4Error):              # past what its 32-bit offsets cover
+        w4.w8a8_moe_gemm_swiglu(x, sx, w[None], sw[None], *plan, M, 1, 256, 1)
+
+
+def test_wide_product_output():
+    M, N, K = 70000, 40000, 16                   # Y 2.8e9 elements
+    say("w8a8_gemm with 5.6 GB of output")
+    x = torch.zeros(M, K, dtype=torch.uint8, device=dev())
+    x[:, 3] = ONE + (torch.arange(M, device=dev()) % 8).to(torch.uint8)
+    w = torch.zeros(N, K, dtype=torch.uint8, device=dev())
+    w[:, 3] = ONE + 8 * (torch.arange(N, device=dev()) % 5).to(torch.uint8)
+    sx = torch.full((M, 4), 127, dtype=torch.uint8, device=dev()).view(E8M0)
+    sw = torch.full(((N + 127) // 128, 4), 127, dtype=torch.uint8, device=dev()).view(E8M0)
+    y = w4.w8a8_gemm(x.view(E4M3), sx, w.view(E4M3), sw)
+    wx, ww = x[:, 3].view(E4M3).float(), w[:, 3].view(E4M3).float()
+    for r in (0, 1, 53686, 53687, 53688, M - 1):
+        assert torch.equal(y[r].float(), wx[r] * ww), f"row {r}"
+
+
+def test_wide_quantization():
+    M, K = 70000, 40000                          # 2.8e9 elements
+    say("w8_quantize_rows / w8_silu_mul_quantize of 5.6 GB")
+    X = torch.zeros(M, K, dtype=torch.bfloat16, device=dev())
+    rows = [0, 53686, 53687, 53688, M - 1]
+    X[rows] = synth.activations(len(rows), K, 23).to(dev())
+    q, s = w4.w8_quantize_rows(X)
+    q1, s1 = w4.w8_quantize_rows(X[rows].contiguous())
+    assert torch.equal(q.view(torch.uint8)[rows], q1.view(torch.uint8))
+    assert torch.equal(s.view(torch.uint8)[rows], s1.view(torch.uint8))
+    del q, s
+    q, s = w4.w8_silu_mul_quantize(X)
+    q1, s1 = w4.w8_silu_mul_quantize(X[rows].contiguous())
+    assert torch.equal(q.view(torch.uint8)[rows], q1.view(torch.uint8))
+    assert torch.equal(s.view(torch.uint8)[rows], s1.view(torch.uint8))
+    del q, s
+    q, s, qt, st = w4.w8_quantize_blocks(X, transposed=True)
+    q1, s1, _, _ = w4.w8_quantize_blocks(X[M - 112:].contiguous())   # the last 128-row block: 546 x 128 + 112
+    assert torch.equal(q.view(torch.uint8)[M - 112:], q1.view(torch.uint8))
+    assert torch.equal(s.view(torch.uint8)[-1:], s1.view(torch.uint8))
+    assert torch.equal(qt.view(torch.uint8)[K - 16:].t(), q.view(torch.uint8)[:, K - 16:])
+    assert torch.equal(st.view(torch.uint8)[:313, 546], s.view(torch.uint8)[546, :313])
