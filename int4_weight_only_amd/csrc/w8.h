@@ -68,18 +68,19 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
 }
 
 // silu(g) * u = g / (1 + e^-g) * u.  The exponential is 2^t with t = -g log2 e
-// as a product and its remainder, so that it holds to about two units in the
-// last place for every g; v_exp_f32 and v_rcp_f32 give one unit each.  (The
-// rounding to e4m3 that follows is 2^19 times coarser; with the exactly rounded
-// division and expf the quantizer took 78 us at 32775 x 2000, 59 now.)  The
-// quarters keep the reciprocal of 1 + e^-g a normal number, which v_rcp_f32
-// would flush to zero from e^-g = 2^126 on.
+// as a product and its remainder, so that it holds to about three units in the
+// last place for every g (beyond the limits it is zero or infinite);
+// v_exp_f32 and v_rcp_f32 give one unit each.  (The rounding to e4m3 that
+// follows is 2^19 times coarser; with the exactly rounded division and expf the
+// quantizer took 78 us at 32775 x 2000, 59 now.)  The quarters keep the
+// reciprocal of 1 + e^-g a normal number, which v_rcp_f32 would flush to zero
+// from e^-g = 2^126 on.
 __device__ __forceinline__ float silu_mul_fast(float g, float u) {
   constexpr float kLog2e = 1.44269502f, kRest = 1.92596299e-8f, kLn2 = 0.693147182f;
-  const float t = -g * kLog2e;
-  const float r = __builtin_fmaf(-g, kLog2e, -t) - g * kRest;
-  float e = __builtin_amdgcn_exp2f(t);
-  e = e < INFINITY && e > 0.0f ? __builtin_fmaf(e, r * kLn2, e) : e;
+  const float c = __builtin_amdgcn_fmed3f(g, -1024.0f, 1024.0f);
+  const float t = -c * kLog2e;
+  const float r = __builtin_fmaf(-c, kLog2e, -t) - c * kRest;
+  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(r, kLn2, 1.0f);
   return 0.25f * g * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.25f, 0.25f)) * u;
 }
 
