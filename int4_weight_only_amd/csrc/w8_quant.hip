@@ -58,7 +58,9 @@ unsigned row_grid(int64_t units) {
 
 // ------------------------------------------------------------------- rows --
 // One wave per 512 elements of a row (four blocks, one dword of scales): 16
-// lanes hold a block, eight elements each.
+// lanes hold a block, eight elements each, so that a block's maximum is four
+// lane exchanges and each lane reads 16 bytes and writes 8.  Bound by bytes, and
+// by the launch where they are few: 2050 x 5120 (32 MB) 8 us, 32 x 4096 2.5 us.
 __global__ __launch_bounds__(256) void k_w8_quantize_rows(const uint16_t* __restrict__ X,
                                                           int64_t units, int quads, int64_t K,
                                                           uint8_t* __restrict__ X8,
@@ -88,7 +90,9 @@ hipError_t launch_w8_quantize_rows(const uint16_t* X, int64_t M, int64_t K, uint
 // One workgroup per 128 x 128 block: thread t holds eight elements of rows
 // t / 16 + 16 i, i = 0..7.  TR also writes the transposed codes through LDS.
 // The grid covers whole dwords of scales in both directions; workgroups past
-// the blocks write padding (1.0).
+// the blocks write padding (1.0).  The block stays in registers between its
+// maximum and its codes: W is read once.  Bound by bytes: 14336 x 4096 with the
+// transpose, 235 MB, 45 us (5.2 TB/s; 52 with the call and cold caches).
 template <bool TR>
 __global__ __launch_bounds__(256) void k_w8_quantize_blocks(const uint16_t* __restrict__ W,
                                                             int64_t N, int64_t K,
@@ -166,7 +170,8 @@ hipError_t launch_w8_quantize_blocks(const uint16_t* W, int64_t N, int64_t K, ui
 
 // ------------------------------------------------------ SwiGLU + quantize --
 // a = silu(g) * u in fp32, quantized per 128 elements of the row; one wave
-// per 512 outputs, as in the row quantizer.
+// per 512 outputs, as in the row quantizer.  Bound by bytes: 32775 x 2000,
+// 329 MB, 59 us (5.5 TB/s); 2048 x 2048 6 us.
 __global__ __launch_bounds__(256) void k_w8_silu_mul_quantize(const uint16_t* __restrict__ H1,
                                                               int64_t units, int quads, int64_t I,
                                                               uint8_t* __restrict__ A8,
@@ -177,20 +182,20 @@ __global__ __launch_bounds__(256) void k_w8_silu_mul_quantize(const uint16_t* __
     const int64_t r = unit / quads;
     const int64_t i = (unit - r * quads) * 512 + 8 * lane;
     float a[8];
-  #pragma unroll
+#pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = 0.0f;
     if (i < I) {
       const u32x4 gv = *(const u32x4*)(H1 + r * 2 * I + i);
       const u32x4 uv = *(const u32x4*)(H1 + r * 2 * I + I + i);
       const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w};
-  #pragma unroll
+#pragma unroll
       for (int j = 0; j < 4; ++j) {
         a[2 * j] = silu_mul_fast(bf16_lo(g[j]), bf16_lo(u[j]));
         a[2 * j + 1] = silu_mul_fast(bf16_hi(g[j]), bf16_hi(u[j]));
       }
     }
     uint32_t amax = 0;
-  #pragma unroll
+#pragma unroll
     for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(a[j]) & 0x7FFFFFFFu);
     const uint32_t byte = scale_byte(row16_max(amax));
     if (i < I) {
