@@ -551,6 +551,17 @@ def test_layer_refuses_buffers_of_another_block_size():
         moe.moe_forward_w8(X.to(dev()), ids, w, g, d, B=256, buffers=moe.alloc_buffers_w8(T, k, E, H, I, 16, dev()))
 
 
+def test_weight_gradient_product_ends_in_small_tiles():
+    # 320 tiles of 256 x 256: the last rows in a launch of their own; integers, so that sums are exact
+    M, N, K = 4096, 5120, 72
+    g = torch.Generator().manual_seed(24)
+    a, b = (torch.randint(-2, 3, (r, K), generator=g).to(torch.bfloat16).to(dev()) for r in (M, N))
+    say("w4_bf16_gemm_nt in two launches")
+    assert torch.equal(w4.w4_bf16_gemm_nt(a, b).float(), a.float() @ b.float().t())
+    got = w4.w4_bf16_gemm_nt(a[:M - 100].contiguous(), b)
+    assert torch.equal(got.float(), a[:M - 100].float() @ b.float().t())
+
+
 # ------------------------------------------------------ offsets past 32 bits --
 # One nonzero product per output: exact in any order.
 
