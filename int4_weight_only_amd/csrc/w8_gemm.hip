@@ -194,7 +194,7 @@ __global__ __launch_bounds__(NW * 64) void k_w8_split(const uint8_t* __restrict_
 // Rates: 4096 x 14336 x 4096 209 us (2.3 PFLOP/s), 8192^3 398 us (2.76), grouped
 // 16384 rows of 32 experts x [4096, 4096] 290 us with SwiGLU (the
 // layer 596 us with the two apart, 556 together); bound by the feed of operands (above).
-// 2048 rows of 128 experts x [4096, 4096] in 64 x 128 tiles read W at 5.1 TB/s.
+// 2048 rows of 128 experts x [4096, 4096] in 64 x 256 tiles read W at 5.3 TB/s.
 //
 // SWIGLU (256 x 256, grouped): W's 2 I rows are gate, then up; a tile takes 128
 // of each, in the waves wn = 0 and 1, which exchange half of their bf16
@@ -805,7 +805,15 @@ hipError_t launch_w8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_
   switch (moe_tile_rows(T * k / x_row_div, K, B)) {
     case 16: return split<1, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 16, gr, st);
     case 32: return split<2, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 32, gr, st);
-    case 64: return tile<2, 4, 1, 4, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
+    case 64: {
+      // 256 columns read weights in longer runs, if there are tiles for all CUs (at
+      // most one expert a pair): 256 x 8 pairs over 128 of [4096, 4096] take 402
+      // us, 418 in 128 columns; 64 x 2 over 8 of [4096, 4096] 33 and 26.
+      const int64_t blocks = std::max(std::min((int64_t)E, T * k), T * k / 64);
+      if (blocks * ((N + 255) / 256) >= cu_count())
+        return tile<2, 8, 1, 3, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
+      return tile<2, 4, 1, 4, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
+    }
     case 128: return tile<4, 8, 1, 3, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
     default: return tile<8, 8, 1, 2, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
   }

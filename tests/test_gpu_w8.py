@@ -253,7 +253,7 @@ def experts(E, N, K, seed):
 
 GROUPS = [(1, 4, 2, 64, 128, 16, "k"), (5, 3, 2, 100, 272, 16, "k"), (40, 5, 3, 130, 528, 32, "1"), (64, 4, 4, 260, 144, 64, "k"),
           (96, 2, 2, 257, 400, 128, "1"), (300, 3, 2, 512, 272, 256, "k"), (90, 4, 1, 96, 1040, 48, "k"), (700, 2, 1, 384, 256, 512, "1"),
-          (33, 7, 7, 48, 640, 1024, "1")]
+          (33, 7, 7, 48, 640, 1024, "1"), (90, 32, 4, 2060, 272, 64, "k"), (200, 36, 2, 2048, 1040, 192, "1"), (70, 64, 3, 1025, 128, 64, "k")]
 
 
 @pytest.mark.parametrize("T,E,k,N,K,B,rows", GROUPS)
