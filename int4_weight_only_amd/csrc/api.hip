@@ -694,11 +694,11 @@ int w8a8_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const uin
 }
 
 // Blocks that hold most experts' rows whole, so that an expert's weights are
-// read once: 2048 x 8 pairs over 32 experts of [4096, 4096] take 308 us in
-// blocks of 256, 521 of 128 and 689 of 64; 512 x 8 over 128 of [2048, 4096]
-// (32 rows each) 230 us in 64 and 449 in 16.  Up to 8 rows the 16-row tiles
-// read the weights fastest (64 x 8 pairs over 128 of [4096, 4096]: 351 us,
-// 393 in blocks of 64).
+// read once: 2048 x 8 pairs over 32 experts of [4096, 4096] take 332 us in
+// blocks of 256, 410 of 128 and 581 of 64; 1024 x 8 over 128 of them (64 rows
+// each) 442 us in 128 and 513 in 64; 512 x 8 over 128 of [2048, 4096] 230 us in
+// 64 and 450 in 16.  Up to 8 rows the 16-row tiles read the weights fastest (64 x
+// 8 pairs over 128 of [4096, 4096]: 341 us, 370 in blocks of 64).
 int32_t w8_pick_block_size(int64_t T, int32_t k, int32_t E) {
   if (T < 0 || k < 1 || E < 1) return 0;
   if (T > ((int64_t)1 << 40)) return 256;
