@@ -677,6 +677,7 @@ constexpr Kind kKinds[] = {
     {64, 128, 1, 0.40f, 6.0f},
     {128, 128, 1, 0.60f, 6.0f},
     {128, 256, 1, 1.05f, 10.0f},
+    {192, 256, 1, 1.10f, 11.0f},
     {256, 256, 1, 1.35f, 12.0f},
 };
 
@@ -695,10 +696,12 @@ float estimate(int kind, int64_t M, int64_t N, int64_t K) {
 // The kernel that the estimate says is done first.  Few large tiles move the
 // least data, but leave CUs idle where they are too few: 4096 x 14336 x 4096
 // takes 209 us in 896 tiles of 256 x 256, 278 in 1792 of 128 x 256 and 356 in
-// 3584 of 128 x 128; 1024 x 4096 x 4096 takes 51, 36 and 26 us.
+// 3584 of 128 x 128; 1024 x 4096 x 4096 takes 51, 36 and 26 us.  192 rows fit
+// where 256 leave a third of the CUs idle and 128 need a second round: 2304 x
+// 4096 x 4096 takes 40.5 us, 47.5 without them.
 int pick(int64_t M, int64_t N, int64_t K, float& us) {
   int best = -1;
-  for (int i = M <= 64 ? 0 : 1; i < (M <= 16 ? 1 : 6); ++i) {
+  for (int i = M <= 64 ? 0 : 1; i < (M <= 16 ? 1 : 7); ++i) {
     const float e = estimate(i, M, N, K);
     if (best < 0 || e < us) {
       best = i;
@@ -730,6 +733,7 @@ hipError_t run_kind(int kind, const uint8_t* X8, const uint8_t* SX, const uint8_
     case 2: return tile<2, 4, 1, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
     case 3: return tile<4, 4, 1, 4, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
     case 4: return tile<4, 8, 1, 3, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
+    case 5: return tile<6, 8, 1, 2, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
     default: return tile<8, 8, 1, 2, false>(X8, SX, W8, SW, Y, M, N, K, none, st);
   }
 }

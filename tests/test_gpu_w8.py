@@ -165,7 +165,7 @@ def operands(M, N, K, seed=4, wide=False):
 
 SHAPES = [(1, 1, 16), (1, 8300, 272), (5, 12301, 144), (16, 12288, 400), (1, 512, 4096), (3, 130, 144), (8, 257, 528), (16, 64, 1040), (17, 100, 128), (32, 1000, 2064),
           (33, 48, 400), (64, 64, 64), (65, 129, 1296), (100, 272, 512), (128, 256, 256), (129, 384, 1152),
-          (200, 515, 272), (256, 512, 128), (300, 640, 784), (513, 257, 640), (1030, 1028, 336), (2304, 768, 272), (1500, 3000, 1008),
+          (200, 515, 272), (256, 512, 128), (300, 640, 784), (513, 257, 640), (1030, 1028, 336), (2304, 768, 272), (2300, 4096, 272), (1140, 8187, 400), (1500, 3000, 1008),
           (3000, 5000, 1296), (140, 3001, 272)]
 
 
