@@ -826,20 +826,23 @@ def _out(t, name, shape, dtype, like):
     """``t`` checked, or a new tensor."""
     if t is None:
         return like.new_empty(shape, dtype=dtype)
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.is_contiguous()
+            and t.get_device() == like.get_device() and t.numel() == math.prod(shape)):
+        return t
     _need(t, name, dtype)
-    if t.numel() != math.prod(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on another GPU than the inputs")
-    return t
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _ints(t, name, size, device):
+    if (isinstance(t, _Tensor) and t.dtype is _I32 and t.is_contiguous() and t.get_device() == device
+            and t.numel() >= size):
+        return
     _need(t, name, _I32)
-    if t.numel() < size:
-        raise ValueError(f"{name} needs {size} entries")
     if t.get_device() != device:
         raise ValueError(f"{name} is on another GPU than the other operands")
+    raise ValueError(f"{name} needs {size} entries")
 
 
 def w8_scale_cols(K):
