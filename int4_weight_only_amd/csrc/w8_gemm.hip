@@ -349,9 +349,13 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
       load_lds16(br, sb + I * 1024, 16 * piece(I) < left ? boff[i - XA] : kOOB, k0);
     }
   };
+  // quads past K repeat the row's last one: what lies behind it is another
+  // row's, and a NaN scale there would reach this row through 0 * NaN
+  const int last_quad = (steps - 1) >> 2;
   auto load_scales = [&](int quad) __attribute__((always_inline)) {
-    load_lds4(sar, rx[quad & 1] + 64 * wave, sxoff, (uint32_t)quad * 4u);
-    load_lds4(sbr, rw[quad & 1], swoff, (uint32_t)quad * 4u);   // by every wave, the same bytes
+    const uint32_t at = (uint32_t)min(quad, last_quad) * 4u;
+    load_lds4(sar, rx[quad & 1] + 64 * wave, sxoff, at);
+    load_lds4(sbr, rw[quad & 1], swoff, at);                    // by every wave, the same bytes
   };
   // operand tile i of a wave's rows (16 rows keep the swizzle of the first)
   auto read = [&](const uint8_t* s, int at, int i) __attribute__((always_inline)) {
@@ -377,16 +381,15 @@ __global__ __launch_bounds__(256 * KG, 1) void k_w8_tile(const uint8_t* __restri
   constexpr int HI = WHOLE ? MI : MI / 2, HJ = WHOLE ? NI : NI / 2;
   i32x8 x[2][HI], w[2][HJ];
   uint32_t sx[MI], sw;
-  // the dword that holds a step's scale (the added step repeats the last
-  // one's), and its place in it
-  auto scale_at = [&](int step) { return min(step, steps - 1); };
+  // the dword that holds a step's scale, and its place in it (steps past K take
+  // the last step's)
   auto read_sx = [&](int step, int i) __attribute__((always_inline)) {
-    return rx[(scale_at(step) >> 2) & 1][xrow + 16 * i];
+    return rx[(step >> 2) & 1][xrow + 16 * i];
   };
   auto read_sw = [&](int step) __attribute__((always_inline)) {
-    return rw[(scale_at(step) >> 2) & 1][(wn * 16 * NI) >> 7];
+    return rw[(step >> 2) & 1][(wn * 16 * NI) >> 7];
   };
-  auto shift = [&](int step) { return 8 * (scale_at(step) & 3); };
+  auto shift = [&](int step) { return 8 * (min(step, steps - 1) & 3); };
   auto fence = [] __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);

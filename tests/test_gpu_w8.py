@@ -201,6 +201,23 @@ def test_gemm_nan_weight_block_stays_in_its_columns(M):
     assert nan[:, 128:256].all() and not nan[:, :128].any() and not nan[:, 256:].any()
 
 
+@pytest.mark.parametrize("M,N,K", [(80, 260, 16), (80, 260, 384), (80, 260, 512), (80, 260, 1536), (65, 130, 2560), (512, 1024, 1536),
+                                   (300, 256, 1168), (3, 130, 144), (300, 640, 784), (1140, 8187, 400), (2304, 768, 272)])
+def test_gemm_nan_rows_stay_in_their_rows(M, N, K):
+    # tiles whose K groups end in steps past K, and the others; whatever stands
+    # in the padding of the scales
+    x = synth.bits(synth.activations(M, K, 25)).copy()
+    x[2, K - 1] = 0x7FC1
+    if M > 40:
+        x[7, 0], x[8, K // 2], x[40] = 0xFF80, 0x7F80, 0x7FC1
+    x8, sx = ow8.quantize_rows(x)
+    w8_, sw = ow8.quantize_blocks(synth.bits(synth.weights(N, K, 25)))
+    sx[:, -(-K // 128):], sw[:, -(-K // 128):] = 255, 255
+    say(f"w8a8_gemm nan rows M={M} N={N} K={K}")
+    y = w4.w8a8_gemm(codes(x8), scales(sx), codes(w8_), scales(sw))
+    assert_product(y, x8, sx, w8_, sw)
+
+
 @pytest.mark.parametrize("M", [2, 48, 300])
 def test_gemm_every_code(M):
     # all 254 numbers on both sides, integers only by scale
