@@ -395,6 +395,7 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
   load_row<NPER>(row, bias, E, in_lanes ? NPER * lane : lane, in_lanes ? 1 : 64, x, add);
   int my_id = 0;
   bool my_live = false, sure;
+  float top = -INFINITY;                       // softmax: the row's largest logit
   {
     float c[NPER];
     if (rule.sigmoid) {
@@ -402,7 +403,6 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
       for (int i = 0; i < NPER; ++i)
         c[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
     } else {
-      float top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NPER; ++i) {
         c[i] = masked(x[i]) ? -INFINITY : fminf(x[i], FLT_MAX);
@@ -433,13 +433,17 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
   }
   RowSum rs = {0.0, 1.0};
   if (!rule.sigmoid) {
-    if (!sure || !rule.renorm) {
+    // renormalised: the picks' own largest logit will do, unless it is so far
+    // below the row's that the scores are near zero in 64 bits too
+    bool far = true;
+    if (sure && rule.renorm) {
+      const float best = wave_max_of(lane < k ? fminf(row[my_id], FLT_MAX) : -INFINITY);
+      rs.top = (double)best;
+      far = top - best >= 600.0f;
+    }
+    if (far) {
       load_row<NPER>(row, bias, E, lane, 64, x, add);
       rs = row_sum<NPER>(x, E, lane);
-    } else {
-      // renormalised: the picks' own largest logit will do
-      const float y = lane < k && my_live ? fminf(row[my_id], FLT_MAX) : -INFINITY;
-      rs.top = (double)wave_max_of(y);
     }
   }
   if (!sure) {

@@ -76,6 +76,33 @@ def test_masks_infinities_and_ties(rule):
     assert all(len(set(r)) == k for r in ids)
 
 
+@pytest.mark.parametrize("tied", [False, True])
+@pytest.mark.parametrize("groups,topk_groups", [(1, 1), (4, 2)])
+@pytest.mark.parametrize("E", [16, 256])
+def test_scores_that_vanish_in_64_bits(E, groups, topk_groups, tied):
+    # the bias picks experts whose softmax is zero, or nearly, beside one logit:
+    # the same weights whether their choice values are apart or equal
+    lg = np.zeros((7, E), np.float32)
+    lg[:, 9] = [1000, 800, 700, 650, 590, 300, np.inf]
+    lg[:6, 3] = [0, 0, -5, 1, 2, -400]
+    bias = np.zeros(E, np.float32)
+    bias[[1, 3]] = [3.0, 3.0 if tied else 2.5]
+    rule = dict(groups=groups, topk_groups=topk_groups)
+    say(f"route_scored vanishing scores E={E} groups={groups} tied={tied}")
+    ids, w = w4.w4_moe_route_scored(up(lg), 2, bias=up(bias), **rule)
+    ids_ref, p = ow8.route_scored(lg, 2, bias=bias, **rule)
+    np.testing.assert_array_equal(down(ids), ids_ref)
+    assert np.all(ids_ref == [1, 3]) and not p[[0, 1, 6]].any() and p[2:6].any(1).all()
+    np.testing.assert_allclose(down(w), p, rtol=2.0 ** -23, atol=1e-45)
+    # the gradient by its formula: the oracle's divides by the square of a sum
+    # that is zero in 64 bits
+    dw = np.random.default_rng(8).normal(size=p.shape).astype(np.float32)
+    ref = np.zeros(lg.shape)
+    np.put_along_axis(ref, ids_ref.astype(np.int64), p * (dw - (p * dw).sum(1, keepdims=True)), 1)
+    got = down(w4.w4_moe_route_scored_bwd(up(lg), ids, w, up(dw))).astype(np.float64)
+    assert np.all(np.abs(got - ref) <= 2.0 ** -23 * np.abs(ref) + 2.0 ** -45 * np.abs(dw).max())
+
+
 @pytest.mark.parametrize("E,k,groups,topk_groups", [(64, 4, 8, 3), (128, 8, 8, 4), (256, 8, 32, 3), (384, 6, 64, 2), (512, 16, 2, 1),
                                                     (1024, 5, 16, 5), (24, 4, 3, 2), (384, 8, 6, 3), (64, 2, 64, 5), (90, 6, 10, 4)])
 @pytest.mark.parametrize("sigmoid,group_top", [(True, 2), (False, 1)])
