@@ -72,16 +72,19 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
 // last place for every g (beyond the limits it is zero or infinite);
 // v_exp_f32 and v_rcp_f32 give one unit each.  (The rounding to e4m3 that
 // follows is 2^19 times coarser; with the exactly rounded division and expf the
-// quantizer took 78 us at 32775 x 2000, 59 now.)  The quarters keep the
-// reciprocal of 1 + e^-g a normal number, which v_rcp_f32 would flush to zero
-// from e^-g = 2^126 on.
+// quantizer took 78 us at 32775 x 2000, 59 now.)  From t = 120 on the quotient
+// and u are taken with 2^136 moved from one to the other: silu(g) itself is then
+// below fp32's range, or near its end, while a large u brings the product back
+// (t = 262, g = -181, is where the largest u no longer does).
 __device__ __forceinline__ float silu_mul_fast(float g, float u) {
   constexpr float kLog2e = 1.44269502f, kRest = 1.92596299e-8f, kLn2 = 0.693147182f;
   const float c = __builtin_amdgcn_fmed3f(g, -1024.0f, 1024.0f);
   const float t = -c * kLog2e;
   const float r = __builtin_fmaf(-c, kLog2e, -t) - c * kRest;
-  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(r, kLn2, 1.0f);
-  return 0.25f * g * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.25f, 0.25f)) * u;
+  const bool far = t > 120.0f;
+  const float one = far ? 0x1p-136f : 1.0f;
+  const float e = __builtin_amdgcn_exp2f(far ? t - 136.0f : t) * __builtin_fmaf(r, kLn2, 1.0f);
+  return g * __builtin_amdgcn_rcpf(e + one) * (u * one);
 }
 
 hipError_t launch_w8_quantize_rows(const uint16_t* X, int64_t M, int64_t K, uint8_t* X8,

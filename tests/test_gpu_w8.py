@@ -156,6 +156,29 @@ def test_silu_far_negative_gates():
             assert np.all(np.abs(y - v) <= np.maximum(np.abs(v) * 2.0 ** -4, step * 2.0 ** -10) + 2.0 ** -18 * np.abs(v))
 
 
+def test_silu_gates_past_the_range_of_their_exponential():
+    # silu(g) down to 2^-254, which u brings back into fp32's range: half a step
+    # of e4m3, the slack of test_silu_mul_quantize, and 2^-126 for what may flush
+    gates = np.concatenate([np.linspace(-95.0, -83.0, 384), np.linspace(-200.0, -95.0, 384), [-300, -1e4, -3e38, -1e-3] * 32])
+    h = np.zeros((6, 2 * len(gates)), np.float32)
+    h[:, :len(gates)] = gates
+    h[:, len(gates):] = np.array([1e-3, 1.0, -2.0 ** 40, 2.0 ** 90, 2.0 ** 127, 3e38])[:, None]
+    b = synth.bits(torch.from_numpy(h).to(torch.bfloat16))
+    say("silu_mul_quantize gates past the range of e^-g")
+    q, s = (bytes_of(t) for t in w4.w8_silu_mul_quantize(up_bits(b)))
+    a = ow8.silu_mul(b)
+    for r in range(a.shape[0]):
+        for c in range(0, a.shape[1], 128):
+            v, step = a[r, c:c + 128], 2.0 ** (int(s[r, c // 128]) - 127.0)
+            y = ow8.e4m3_values(q[r, c:c + 128]) * step
+            top = np.abs(v).max()
+            assert top <= 449 * step + 2.0 ** -126
+            if top > 2.0 ** -110:
+                assert top >= 223 * step
+            assert np.all(np.abs(y - v) <= np.maximum(np.abs(v) * 2.0 ** -4, step * 2.0 ** -10)
+                          + 2.0 ** -18 * np.abs(v) + 2.0 ** -126), f"row {r} block {c}"
+
+
 # ---------------------------------------------------------------- product --
 
 def operands(M, N, K, seed=4, wide=False):
