@@ -284,7 +284,8 @@ int w4_dequant_t(const int32_t* Wq, const uint16_t* S, const uint8_t* Z,
  *   C[m, n] = bf16_rne( sum_k A[m, k] * B[n, k] )    (order fixed)
  * A bf16 [M, K], B bf16 [N, K], both 16-byte aligned; C bf16 [M, N],
  * 2-byte aligned.  K % 8 == 0 (W4_ERR_SHAPE otherwise); K == 0 writes
- * zeros; A and B each below 2 GiB (W4_ERR_UNSUPPORTED otherwise).
+ * zeros; any 256 rows of A or B below 2 GiB, that is K < 2^22 where there are
+ * that many (W4_ERR_UNSUPPORTED otherwise).
  */
 int w4_bf16_gemm_nt(const uint16_t* A, const uint16_t* B, uint16_t* C, int64_t M,
                     int64_t N, int64_t K, void* stream);

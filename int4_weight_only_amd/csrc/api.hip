@@ -300,10 +300,13 @@ int w4_bf16_gemm_nt(const uint16_t* A, const uint16_t* B, uint16_t* C, int64_t M
   if (M == 0 || N == 0) return W4_OK;
   if (!C) return W4_ERR_NULL;
   if (!aligned(C, 2)) return W4_ERR_MISALIGNED;
-  if (!fits_buffer(M * K * 2) || !fits_buffer(N * K * 2) ||
-      ((M + 127) / 128) * ((N + 127) / 128) >= kMaxI32 || M * N > ((int64_t)1 << 40))
+  if (((M + 127) / 128) * ((N + 127) / 128) >= kMaxI32 || M * N > ((int64_t)1 << 40))
     return W4_ERR_UNSUPPORTED;
   if (K == 0) return hip_status(w4::launch_zero_bf16(C, M * N, as_stream(stream)));
+  // 256 rows of an operand are one buffer
+  if (M > kMaxI32 - 256 || N > kMaxI32 - 256 || K > kMaxI32 - 256 ||
+      !fits_buffer((M < 256 ? M : 256) * K * 2) || !fits_buffer((N < 256 ? N : 256) * K * 2))
+    return W4_ERR_UNSUPPORTED;
   if (!A || !B) return W4_ERR_NULL;
   if (!aligned(A, 16) || !aligned(B, 16)) return W4_ERR_MISALIGNED;
   return hip_status(w4::launch_bf16_gemm_nt(A, B, C, M, N, K, as_stream(stream)));

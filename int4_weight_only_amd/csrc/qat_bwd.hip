@@ -225,24 +225,26 @@ __global__ __launch_bounds__(NWV * 64, 1) void k_bf16_gemm_nt(const uint16_t* __
   const int m0 = (group * 8 + in_group % gm) * BM;
   const int n0 = (in_group / gm) * BN;
 
-  const __amdgpu_buffer_rsrc_t ar = rsrc(A, (uint32_t)M * (uint32_t)K * 2u);
-  const __amdgpu_buffer_rsrc_t br = rsrc(B, (uint32_t)N * (uint32_t)K * 2u);
+  // a buffer per tile: its rows are within 32-bit offsets of each other, also
+  // where A or B is larger
+  const int rows_a = min(BM, M - m0), rows_b = min(BN, N - n0);
+  const __amdgpu_buffer_rsrc_t ar = rsrc(A + (int64_t)m0 * K, (uint32_t)rows_a * (uint32_t)K * 2u);
+  const __amdgpu_buffer_rsrc_t br = rsrc(B + (int64_t)n0 * K, (uint32_t)rows_b * (uint32_t)K * 2u);
   // Load I of a stage fills stage rows 8 I .. 8 I + 7: lane l writes the 16
   // bytes at slot l, row r = 8 I + l / 8, stored piece l % 8, which holds
   // the row's piece (l % 8) ^ ((r / 2) % 8).  Byte offset of the lane's
   // piece at step 0 (OOB for rows past the end) and its k within a step.
-  auto row_off = [&](int first, int lim, int I) {
+  auto row_off = [&](int rows, int I) {
     const int r = 8 * I + (lane >> 3);
     const int pg = (lane & 7) ^ ((r >> 1) & 7);
-    const int row = first + r;
-    return row < lim ? ((uint32_t)row * (uint32_t)K + 8u * (uint32_t)pg) * 2u : kOOB;
+    return r < rows ? ((uint32_t)r * (uint32_t)K + 8u * (uint32_t)pg) * 2u : kOOB;
   };
   auto piece_k = [&](int I) { return 8 * ((lane & 7) ^ (((8 * I + (lane >> 3)) >> 1) & 7)); };
   uint32_t aoff[XA], boff[XB];
 #pragma unroll
-  for (int i = 0; i < XA; ++i) aoff[i] = row_off(m0, M, wave * XA + i);
+  for (int i = 0; i < XA; ++i) aoff[i] = row_off(rows_a, wave * XA + i);
 #pragma unroll
-  for (int i = 0; i < XB; ++i) boff[i] = row_off(n0, N, wave * XB + i);
+  for (int i = 0; i < XB; ++i) boff[i] = row_off(rows_b, wave * XB + i);
   auto load_stage = [&](int step, uint16_t* sa, uint16_t* sb) __attribute__((always_inline)) {
     const int k0 = step * KS;
 #pragma unroll

@@ -12,7 +12,8 @@ identity, so
                                     the same call
   dW = dY^T * X                     bf16, unquantized operands
                                     (``w4_bf16_transpose``, ``w4_bf16_gemm_nt``)
-The master weight stays bf16.  The backward is not differentiable again.  To
+which covers fewer than 2^22 tokens: more of them are refused in the forward
+where W needs a gradient.  The master weight stays bf16.  The backward is not differentiable again.  To
 capture a backward into a graph, take gradients with ``torch.autograd.grad``, or
 let no eager graph of the same leaves be alive.
 """
@@ -23,6 +24,13 @@ from torch.autograd.function import once_differentiable
 from . import (w4_bf16_gemm_nt, w4_bf16_transpose, w8_quantize_blocks, w8_quantize_rows, w8a8_gemm)
 
 __all__ = ["W8Linear", "w8_linear"]
+
+
+def _padded(rows):
+    """Columns of the weight gradient's transposed operands: whole 128-byte
+    lines, their ends zero (the product of [4096, 2056] and [5120, 2056] takes
+    109 us, 97 in 2112)."""
+    return (rows + 63) // 64 * 64
 
 
 class W8Linear(torch.autograd.Function):
@@ -38,6 +46,8 @@ class W8Linear(torch.autograd.Function):
         need_dx, need_dw = ctx.needs_input_grad
         if need_dx and N % 16:
             raise ValueError(f"the W8A8 input gradient needs N % 16 == 0 (N = {N})")
+        if need_dw and min(256, max(N, K)) * _padded(X2.shape[0]) * 2 >= 1 << 31:
+            raise ValueError(f"the W8A8 weight gradient covers fewer than 2^22 tokens, got {X2.shape[0]}")
         W8, SW, WT8, ST = w8_quantize_blocks(W, transposed=need_dx)
         Y = w8a8_gemm(*w8_quantize_rows(X2), W8, SW)
         ctx.save_for_backward(X2 if need_dw else None, WT8, ST)
@@ -53,9 +63,7 @@ class W8Linear(torch.autograd.Function):
         if ctx.needs_input_grad[0]:
             dX = w8a8_gemm(*w8_quantize_rows(dY), WT8, ST).reshape(ctx.x_shape)
         if ctx.needs_input_grad[1]:
-            # transposed rows of whole 128-byte lines, their ends zero: the
-            # product of [4096, 2056] and [5120, 2056] takes 109 us, 97 in 2112
-            rows = (dY.shape[0] + 63) // 64 * 64
+            rows = _padded(dY.shape[0])
             dW = w4_bf16_gemm_nt(w4_bf16_transpose(dY, rows), w4_bf16_transpose(X2, rows))
         return dX, dW
 

@@ -146,3 +146,16 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
                  lambda: w4.w4_moe_route_scored(x, 2)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_weight_gradient_limits(lib):
+    f = lib.w4_bf16_gemm_nt
+    K = 1 << 22
+    assert f(None, None, A2, 16384, 8192, 70016, None) == NULL      # operands past 2 GiB: covered
+    assert f(None, None, A2, 1 << 20, 256, K - 8, None) == NULL
+    assert f(None, None, A2, 255, 100, K, None) == NULL
+    assert f(None, None, A2, 256, 100, K, None) == f(None, None, A2, 100, 256, K, None) == UNSUPPORTED
+    assert f(None, None, A2, 1, 1, 1 << 30, None) == UNSUPPORTED
+    x, w = torch.zeros(1, 16, dtype=torch.bfloat16).expand(K, 16), torch.zeros(256, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="tokens"):
+        w8.w8_linear(x, w.requires_grad_())

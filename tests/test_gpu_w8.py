@@ -669,3 +669,34 @@ def test_wide_quantization():
     assert torch.equal(s.view(torch.uint8)[-1:], s1.view(torch.uint8))
     assert torch.equal(qt.view(torch.uint8)[K - 16:].t(), q.view(torch.uint8)[:, K - 16:])
     assert torch.equal(st.view(torch.uint8)[:313, 546], s.view(torch.uint8)[546, :313])
+
+
+@pytest.mark.parametrize("M,N,K", [(600, 520, 2097160), (4096, 4096, 262152), (4352, 4096, 262152)])
+def test_wide_bf16_product(M, N, K):
+    # operands past 2 GiB in small tiles, large ones, and both
+    say(f"w4_bf16_gemm_nt M={M} N={N} K={K}")
+    a, b = torch.zeros(M, K, dtype=torch.bfloat16, device=dev()), torch.zeros(N, K, dtype=torch.bfloat16, device=dev())
+    m, n = torch.arange(M, device=dev()), torch.arange(N, device=dev())
+    at = torch.arange(9, device=dev()) * ((K - 1) // 8)      # nine columns that are not zero, from the first to the last eight
+    va = ((m[:, None] * 7 + torch.arange(9, device=dev())) % 5 - 2).float()
+    vb = ((n[:, None] * 3 + torch.arange(9, device=dev())) % 7 - 3).float()
+    a[:, at], b[:, at] = va.bfloat16(), vb.bfloat16()
+    assert torch.equal(w4.w4_bf16_gemm_nt(a, b).float(), va @ vb.t())   # integers below 2^8: exact
+
+
+def test_wide_linear_gradients():
+    M, N, K = 70000, 16384, 64                   # dY and its transpose 2.3 GB
+    say("w8_linear with 2.3 GB of dY")
+    rows = torch.tensor([0, 1, 40000, 65535, 65536, M - 1], device=dev())
+    X = torch.zeros(M, K, dtype=torch.bfloat16, device=dev())
+    X[rows] = ((torch.arange(6 * K, device=dev()).view(6, K) % 7) - 3).bfloat16()
+    W = torch.zeros(N, K, dtype=torch.bfloat16, device=dev())
+    W[:, 5] = (torch.arange(N, device=dev()) % 3 - 1).bfloat16()
+    dY = torch.zeros(M, N, dtype=torch.bfloat16, device=dev())
+    dY[rows] = ((torch.arange(6 * N, device=dev()).view(6, N) % 5) - 2).bfloat16()
+    X.requires_grad_(), W.requires_grad_()
+    dx, dw = torch.autograd.grad(w8.w8_linear(X, W), (X, W), dY)
+    d, x = dY[rows].double(), X.detach()[rows].double()
+    assert torch.equal(dw.double(), (d.t() @ x))             # integers below 2^8: exact
+    want = (d @ W.detach().double()).bfloat16()
+    assert torch.equal(dx[rows], want) and not dx[2:40000].any()
