@@ -356,9 +356,11 @@ hipError_t launch_nt(const uint16_t* A, const uint16_t* B, uint16_t* C, int64_t 
 // [4096, 14336]; smaller products keep the 128 x 256 tile of 4 waves
 // (three stages), which spreads them over more CUs and takes 0.6 of the time
 // a round.  Where the large tiles would end in a round of few, the rows of that
-// round take small tiles in a launch of their own (4096 x 5120 x 2112: 108 ->
-// 97 us; 14336 x 4096 x 4096: 415 -> 408).  All sum each output in the same order, so the choice does not
-// change a bit.
+// round take small tiles in a launch of their own, if K is long enough that a
+// round is more than its stores (4096 x 5120: K = 64 18.6 us in one launch and
+// 20.9 in two, 512 36.4 and 37.4, 1024 59.5 and 55.4, 2112 109 and 96; 14336 x
+// 4096 x 4096 426 and 410).  All sum each output in the same order, so the
+// choice does not change a bit.
 hipError_t launch_bf16_gemm_nt(const uint16_t* A, const uint16_t* B, uint16_t* C, int64_t M,
                                int64_t N, int64_t K, hipStream_t st) {
   const int64_t cus = cu_count(), rows = (M + 255) / 256, cols = (N + 255) / 256;
@@ -366,7 +368,8 @@ hipError_t launch_bf16_gemm_nt(const uint16_t* A, const uint16_t* B, uint16_t* C
   if (rounds == 0) return launch_nt<128, 4, 3>(A, B, C, M, N, K, st);
   const int64_t main = std::min(M, rounds * cus / cols * 256), rest = M - main;
   const int64_t small = ((rest + 127) / 128 * cols + cus - 1) / cus;
-  if (main == 0 || rest == 0 || rows * cols == rounds * cus || 0.6 * (double)small >= 0.9)
+  if (K <= 512 || main == 0 || rest == 0 || rows * cols == rounds * cus ||
+      0.6 * (double)small >= 0.9)
     return launch_nt<256, 8, 2>(A, B, C, M, N, K, st);
   const hipError_t e = launch_nt<256, 8, 2>(A, B, C, main, N, K, st);
   if (e != hipSuccess) return e;

@@ -602,6 +602,17 @@ def test_weight_gradient_product_ends_in_small_tiles():
     assert torch.equal(got.float(), a[:M - 100].float() @ b.float().t())
 
 
+@pytest.mark.parametrize("K", [64, 512, 520, 1032])
+def test_bf16_product_in_one_launch_and_in_two(K):
+    # 272 tiles of 256 x 256: from K = 520 on the last rows have a launch of their own; integers, so that sums are exact
+    M, N = 4096 + 200, 4096
+    g = torch.Generator().manual_seed(26)
+    a, b = (torch.randint(-2, 3, (r, K), generator=g).to(torch.bfloat16).to(dev()) for r in (M, N))
+    say(f"w4_bf16_gemm_nt one launch or two K={K}")
+    want = (a.float() @ b.float().t()).bfloat16()
+    assert torch.equal(w4.w4_bf16_gemm_nt(a, b), want)
+
+
 # ------------------------------------------------------ offsets past 32 bits --
 # One nonzero product per output: exact in any order.
 
