@@ -616,7 +616,7 @@ int w8_moe_validate(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, con
       T * k + (int64_t)E * B >= kMaxI32 || T * k * N > kMaxElems || N * K > kMaxElems ||
       E * (N * K) > kMaxElems)
     return W4_ERR_UNSUPPORTED;
-  if (w4::w8_moe_threads(T, k, E, N, K, B) >= kMaxGrid) return W4_ERR_UNSUPPORTED;
+  if (w4::w8_moe_threads(T, k, E, N, K, B, x_row_div) >= kMaxGrid) return W4_ERR_UNSUPPORTED;
   if (T == 0) return -1;
   if (!X8 || !SX || !W8 || !SW || !sorted_token_ids || !expert_ids || !num_tokens_post_padded || !Y)
     return W4_ERR_NULL;

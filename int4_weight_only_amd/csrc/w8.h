@@ -93,12 +93,13 @@ hipError_t launch_w8_quantize_blocks(const uint16_t* W, int64_t N, int64_t K, ui
                                      uint8_t* SW, uint8_t* WT8, uint8_t* ST, hipStream_t st);
 hipError_t launch_w8_silu_mul_quantize(const uint16_t* H1, int64_t R, int64_t I, uint8_t* A8,
                                        uint8_t* SA, hipStream_t st);
-// threads the products would start at most (for the launch limit)
+// threads the products' largest launch starts (for the launch limit)
 int64_t w8_gemm_threads(int64_t M, int64_t N, int64_t K);
 hipError_t launch_w8_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
                           const uint8_t* SW, uint16_t* Y, int64_t M, int64_t N, int64_t K,
                           hipStream_t st);
-int64_t w8_moe_threads(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B);
+int64_t w8_moe_threads(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B,
+                       int32_t x_row_div);
 hipError_t launch_w8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
                               const uint8_t* SW, const int32_t* sorted_ids,
                               const int32_t* expert_ids, const int32_t* ntpp, uint16_t* Y,

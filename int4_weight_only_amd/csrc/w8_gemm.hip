@@ -714,21 +714,31 @@ int pick(int64_t M, int64_t N, int64_t K, float& us) {
   return best;
 }
 
+// The split kernel's rows of W and waves per workgroup.  64 rows of W per
+// workgroup share their rows of X, which counts once there are some and N fills
+// the CUs (16 x 12288 x 4096: 12.5 us, 15.9 in 16 rows); else 16, on 16 waves
+// where there are few workgroups and 8 where there are many (4096 x 7168: 7.6 and
+// 9.2 us; 12288 x 4096: 10.7 and 10.0, one row).
+struct Split {
+  int bn, waves;
+};
+Split split_of(int64_t M, int64_t N) {
+  const int64_t cus = cu_count();
+  if (M > 2 && M <= 16 && N >= 48 * cus) return {64, 8};
+  return {16, N <= 32 * cus ? 16 : 8};
+}
+
 hipError_t run_kind(int kind, const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
                     const uint8_t* SW, uint16_t* Y, int64_t M, int64_t N, int64_t K,
                     hipStream_t st) {
   const Grouped none = {};
   switch (kind) {
     case 0: {
-      const int64_t slots = (M + 15) / 16, cus = cu_count();
-      // 64 rows of W per workgroup share their rows of X, which counts once
-      // there are some and N fills the CUs (16 x 12288 x 4096: 12.5 us, 15.9 in
-      // 16 rows); else 16, on 16 waves where there are few workgroups and 8
-      // where there are many (4096 x 7168: 7.6 and 9.2 us; 12288 x 4096: 10.7
-      // and 10.0, one row).
-      if (M > 2 && M <= 16 && N >= 48 * cus)
+      const int64_t slots = (M + 15) / 16;
+      const Split p = split_of(M, N);
+      if (p.bn == 64)
         return split<1, 4, 8, false>(X8, SX, W8, SW, Y, M, N, K, slots, none, st);
-      if (N <= 32 * cus)
+      if (p.waves == 16)
         return split<1, 1, 16, false>(X8, SX, W8, SW, Y, M, N, K, slots, none, st);
       return split<1, 1, 8, false>(X8, SX, W8, SW, Y, M, N, K, slots, none, st);
     }
@@ -763,7 +773,8 @@ int64_t w8_gemm_threads(int64_t M, int64_t N, int64_t K) {
     if (rows == 0) continue;
     float us;
     const Kind& t = kKinds[pick(rows, N, K, us)];
-    most = std::max(most, t.kg == 0 ? tiles_of(t, rows, N) * 1024
+    const Split p = split_of(rows, N);
+    most = std::max(most, t.kg == 0 ? (rows + 15) / 16 * ((N + p.bn - 1) / p.bn) * 64 * p.waves
                                     : (tiles_of(t, rows, N) + 7) * 256 * t.kg);
   }
   return most;
@@ -796,10 +807,23 @@ int moe_tile_rows(int64_t rows_x, int64_t K, int32_t B) {
   return B % 32 == 0 ? 32 : 16;
 }
 
+// Columns of the grouped product's tiles.  64 rows: 256 columns read weights in
+// longer runs, if there are tiles for all CUs (at most one expert a pair): 256 x 8
+// pairs over 128 of [4096, 4096] take 402 us, 418 in 128 columns; 64 x 2 over 8 of
+// [4096, 4096] 33 and 26.
+int moe_tile_cols(int rows, int64_t T, int32_t k, int32_t E, int64_t N) {
+  if (rows <= 32) return 32;
+  if (rows > 64) return 256;
+  const int64_t blocks = std::max(std::min((int64_t)E, T * k), T * k / 64);
+  return blocks * ((N + 255) / 256) >= cu_count() ? 256 : 128;
+}
+
 }  // namespace
 
-int64_t w8_moe_threads(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B) {
-  return moe_rows(T, k, E, B) / 16 * ((N + 31) / 32) * 256;
+int64_t w8_moe_threads(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B,
+                       int32_t x_row_div) {
+  const int rows = moe_tile_rows(T * k / x_row_div, K, B), cols = moe_tile_cols(rows, T, k, E, N);
+  return (moe_rows(T, k, E, B) / rows * ((N + cols - 1) / cols) + 7) * 256;
 }
 
 hipError_t launch_w8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8,
@@ -809,18 +833,14 @@ hipError_t launch_w8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_
                               int32_t x_row_div, hipStream_t st) {
   const Grouped gr = {sorted_ids, expert_ids, ntpp, (int)(T * k), E, B, x_row_div};
   const int64_t cap = moe_rows(T, k, E, B);
-  switch (moe_tile_rows(T * k / x_row_div, K, B)) {
+  const int rows = moe_tile_rows(T * k / x_row_div, K, B);
+  switch (rows) {
     case 16: return split<1, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 16, gr, st);
     case 32: return split<2, 2, 4, true>(X8, SX, W8, SW, Y, 0, N, K, cap / 32, gr, st);
-    case 64: {
-      // 256 columns read weights in longer runs, if there are tiles for all CUs (at
-      // most one expert a pair): 256 x 8 pairs over 128 of [4096, 4096] take 402
-      // us, 418 in 128 columns; 64 x 2 over 8 of [4096, 4096] 33 and 26.
-      const int64_t blocks = std::max(std::min((int64_t)E, T * k), T * k / 64);
-      if (blocks * ((N + 255) / 256) >= cu_count())
+    case 64:
+      if (moe_tile_cols(rows, T, k, E, N) == 256)
         return tile<2, 8, 1, 3, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
       return tile<2, 4, 1, 4, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
-    }
     case 128: return tile<4, 8, 1, 3, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
     default: return tile<8, 8, 1, 2, true>(X8, SX, W8, SW, Y, cap, N, K, gr, st);
   }

@@ -159,3 +159,16 @@ def test_weight_gradient_limits(lib):
     x, w = torch.zeros(1, 16, dtype=torch.bfloat16).expand(K, 16), torch.zeros(256, 16, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="tokens"):
         w8.w8_linear(x, w.requires_grad_())
+
+
+def test_launch_limit_counts_the_launch(lib):
+    def moe(B, T=1 << 17, k=8, N=8192, E=16, K=64):
+        return lib.w8a8_moe_gemm(None, A4, A16, A4, A4, A4, A4, A2, T, k, E, N, K, B, k, None)
+    # 2^20 pairs x 8192: tiles of 64 rows and more start far fewer than 2^32 threads, those of 16 do not
+    assert moe(256) == moe(128) == moe(64) == NULL
+    assert moe(16) == UNSUPPORTED
+    assert moe(32) == NULL and moe(32, N=16384) == UNSUPPORTED
+    f = lib.w8a8_moe_gemm_swiglu
+    assert f(None, A4, A16, A4, A4, A4, A4, A16, A4, 1 << 17, 8, 16, 8192, 64, 256, 8, None) == NULL
+    assert lib.w8a8_gemm(None, A4, A16, A4, A2, 1, 100000000, 16, None) == NULL
+    assert lib.w8a8_gemm(None, A4, A16, A4, A2, 1, 1 << 27, 16, None) == UNSUPPORTED

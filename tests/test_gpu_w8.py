@@ -711,3 +711,26 @@ def test_wide_linear_gradients():
     assert torch.equal(dw.double(), (d.t() @ x))             # integers below 2^8: exact
     want = (d @ W.detach().double()).bfloat16()
     assert torch.equal(dx[rows], want) and not dx[2:40000].any()
+
+
+def test_wide_grouped_product():
+    T, E, k, N, K, B = 1 << 17, 16, 8, 8192, 64, 256         # 2^20 pairs, Y 17 GB
+    say("w8a8_moe_gemm of 2^20 pairs x 8192")
+    x = torch.zeros(T, K, dtype=torch.uint8, device=dev())
+    x[:, 3] = ONE + (torch.arange(T, device=dev()) % 8).to(torch.uint8)
+    w = torch.zeros(E, N, K, dtype=torch.uint8, device=dev())
+    w[:, :, 3] = ONE + 8 * ((torch.arange(N, device=dev())[None] + torch.arange(E, device=dev())[:, None]) % 5).to(torch.uint8)
+    sx = torch.full((T, 4), 127, dtype=torch.uint8, device=dev()).view(E8M0)
+    sw = torch.full((E, N // 128, 4), 127, dtype=torch.uint8, device=dev()).view(E8M0)
+    ids = ((torch.arange(T, device=dev())[:, None] * 5 + torch.arange(k, device=dev()) * 3) % E).to(torch.int32)
+    plan = w4.moe_align_block_size(ids, E, B)
+    y = w4.w8a8_moe_gemm(x.view(E4M3), sx, w.view(E4M3), sw, *plan, T, k, B, k)
+    wx, ww = x[:, 3].view(E4M3).float(), w[:, :, 3].contiguous().view(E4M3).float()
+    for f in (0, 1, 262143, 262144, 524288, T * k - 1):
+        assert torch.equal(y[f].float(), wx[f // k] * ww[int(ids.view(-1)[f])]), f"row {f}"
+    del y
+    a8, sa = w4.w8a8_moe_gemm_swiglu(x.view(E4M3), sx, w.view(E4M3), sw, *plan, T, k, B, k)
+    for f in (0, 1, 262143, 524288, T * k - 1):
+        h1 = (wx[f // k] * ww[int(ids.view(-1)[f])]).bfloat16()[None].contiguous()
+        q, s = w4.w8_silu_mul_quantize(h1)
+        assert torch.equal(a8.view(torch.uint8)[f], q.view(torch.uint8)[0]) and torch.equal(sa.view(torch.uint8)[f], s.view(torch.uint8)[0])
