@@ -335,13 +335,23 @@ def alloc_buffers_w8(T, k, E, H, I, B, device):
                         new((T * k, H), bf), new((T, H), bf))
 
 
+def _refuse_gradients(*inputs):
+    """The expert layer has no backward: an input that wants a gradient would
+    get none, without a word."""
+    if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
+        raise ValueError("the W8A8 expert layer has no backward: detach its inputs, or call it under "
+                         "torch.no_grad()")
+
+
 def moe_forward_w8(X, topk_ids, topk_weights, gate_up, down, B=None, buffers=None):
     """Expert part of the layer for routed tokens on 8-bit experts.
 
     X bf16 [T, H]; topk_ids int32 [T, k], all in [0, E); topk_weights fp32 [T,
     k]; gate_up: E experts of [2I, H]; down: E experts of [H, I]
-    (``ExpertWeightsW8``).  B defaults to ``w8_pick_block_size``.  Returns (Out bf16 [T, H], buffers).
+    (``ExpertWeightsW8``).  B defaults to ``w8_pick_block_size``.  Inputs that
+    want a gradient are refused.  Returns (Out bf16 [T, H], buffers).
     """
+    _refuse_gradients(X, topk_weights)
     T, H = X.shape
     k = topk_ids.shape[1]
     E = gate_up.E
@@ -368,7 +378,8 @@ def moe_forward_w8(X, topk_ids, topk_weights, gate_up, down, B=None, buffers=Non
 def moe_layer_w8(X, logits, k, gate_up, down, sigmoid=False, bias=None, groups=1, topk_groups=1,
                  group_top=1, renorm=True, scale=1.0, B=None, buffers=None):
     """The scored router plus ``moe_forward_w8``: logits fp32 [T, E] -> (Out
-    bf16 [T, H], ids, weights, buffers)."""
+    bf16 [T, H], ids, weights, buffers).  Inputs that want a gradient are refused."""
+    _refuse_gradients(X, logits)
     ids, w = w4_moe_route_scored(logits, k, sigmoid, bias, groups, topk_groups, group_top, renorm,
                                  scale, *((buffers.ids, buffers.weights) if buffers else ()))
     out, b = moe_forward_w8(X, ids, w, gate_up, down, B, buffers)

@@ -172,3 +172,17 @@ def test_launch_limit_counts_the_launch(lib):
     assert f(None, A4, A16, A4, A4, A4, A4, A16, A4, 1 << 17, 8, 16, 8192, 64, 256, 8, None) == NULL
     assert lib.w8a8_gemm(None, A4, A16, A4, A2, 1, 100000000, 16, None) == NULL
     assert lib.w8a8_gemm(None, A4, A16, A4, A2, 1, 1 << 27, 16, None) == UNSUPPORTED
+
+
+def test_expert_layer_refuses_inputs_that_want_gradients():
+    x, lg, w = torch.zeros(2, 32, dtype=torch.bfloat16), torch.zeros(2, 4), torch.zeros(2, 1)
+    ids = torch.zeros(2, 1, dtype=torch.int32)
+    e = moe.ExpertWeightsW8(torch.zeros(4, 32, 32, dtype=torch.bfloat16).to(torch.float8_e4m3fn), torch.zeros(4, 1, 4))
+    for call in (lambda: moe.moe_layer_w8(x.clone().requires_grad_(), lg, 1, e, e),
+                 lambda: moe.moe_layer_w8(x, lg.clone().requires_grad_(), 1, e, e),
+                 lambda: moe.moe_forward_w8(x.clone().requires_grad_(), ids, w, e, e),
+                 lambda: moe.moe_forward_w8(x, ids, w.clone().requires_grad_(), e, e)):
+        with pytest.raises(ValueError, match="no backward"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="on a GPU|do not match"):
+            call()
