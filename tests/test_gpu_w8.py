@@ -455,6 +455,37 @@ def test_linear_gradient_against_differences():
             assert abs(mine - diff) <= 2 * 2.0 ** -4 * (d.norm() * dY.norm() * max(W.norm(), X.norm())).item()
 
 
+def test_linear_gradient_along_its_own_directions():
+    """Differences of the unquantized loss sum(X W^T dY), which is linear in X
+    and in W, along the gradient itself, whole and in parts, where a wrong
+    gradient shows in full.  dX: each e4m3 operand has errors of at most 2^-4
+    of a value, of random sign: a relative norm of sqrt(2 / 3) 2^-4 = 0.051 for
+    both over thousands of elements; 2 x 2^-4 is allowed.  dW: bf16 operands,
+    one rounding by at most 2^-8 of a value, and fp32 sums."""
+    M, N, K = 96, 256, 384
+    X, W, dY = synth.activations(M, K, 27), synth.weights(N, K, 27), synth.normal_bf16((M, N), 1.0, 27, 77)
+    x, w = X.to(dev()).requires_grad_(), W.to(dev()).requires_grad_()
+    say("w8_linear along its gradient")
+    w8.w8_linear(x, w).backward(dY.to(dev()))
+    X, W, dY = X.double(), W.double(), dY.double()
+
+    def off(got, grad, at, loss):
+        worst = 0.0
+        for rows in (slice(None), slice(0, at.shape[0] // 2), slice(at.shape[0] // 2, None)):
+            for cols in (slice(None), slice(0, 128), slice(128, None)):
+                d = torch.zeros_like(at)
+                d[rows, cols] = grad[rows, cols]
+                diff = (loss(at + 0.5 * d) - loss(at - 0.5 * d)).item()
+                worst = max(worst, abs((got * d).sum().item() - diff) / diff)
+        return worst
+    for got, grad, at, loss, bound in ((x.grad, dY @ W, X, lambda v: (v @ W.T * dY).sum(), 2 * 2.0 ** -4),
+                                       (w.grad, dY.T @ X, W, lambda v: (X @ v.T * dY).sum(), 2.0 ** -8 + 2.0 ** -13)):
+        got = got.double().cpu()
+        assert off(got, grad, at, loss) <= bound
+        for wrong in (0 * got, -got, 2 * got, 0.75 * got, got.roll(1, 0)):
+            assert off(wrong, grad, at, loss) > bound        # the bound tells them apart
+
+
 def test_linear_partial_gradients_and_refusals():
     X, W = synth.activations(6, 64, 15).to(dev()), synth.weights(24, 64, 15).to(dev())
     y = w8.w8_linear(X, W.clone().requires_grad_())           # N % 16 only matters to X's gradient
