@@ -37,13 +37,14 @@ class W8Linear(torch.autograd.Function):
     """y = Q(x) * Q(W)^T with a straight-through backward."""
 
     @staticmethod
-    def forward(ctx, X, W):
+    def forward(ctx, X, W, grad=True):
         N, K = W.shape
         if X.shape[-1] != K:
             raise ValueError(f"X has {X.shape[-1]} features, W expects {K}")
         W = W.contiguous()
         X2 = X.reshape(-1, K).contiguous()
-        need_dx, need_dw = ctx.needs_input_grad
+        # needs_input_grad goes by the inputs alone, also under torch.no_grad()
+        need_dx, need_dw = (n and grad for n in ctx.needs_input_grad[:2])
         if need_dx and N % 16:
             raise ValueError(f"the W8A8 input gradient needs N % 16 == 0 (N = {N})")
         if need_dw and min(256, max(N, K)) * _padded(X2.shape[0]) * 2 >= 1 << 31:
@@ -65,11 +66,11 @@ class W8Linear(torch.autograd.Function):
         if ctx.needs_input_grad[1]:
             rows = _padded(dY.shape[0])
             dW = w4_bf16_gemm_nt(w4_bf16_transpose(dY, rows), w4_bf16_transpose(X2, rows))
-        return dX, dW
+        return dX, dW, None
 
 
 def w8_linear(X, W):
     """Linear layer without bias on e4m3 operands: X bf16 [..., K], W bf16
     [N, K] (K % 16 == 0, and N % 16 == 0 where X needs a gradient) -> bf16
     [..., N]."""
-    return W8Linear.apply(X, W)
+    return W8Linear.apply(X, W, torch.is_grad_enabled())

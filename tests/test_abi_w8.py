@@ -186,3 +186,15 @@ def test_expert_layer_refuses_inputs_that_want_gradients():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="on a GPU|do not match"):
             call()
+
+
+def test_linear_without_gradients_has_no_limits_of_theirs():
+    x = torch.zeros(2, 16, dtype=torch.bfloat16, requires_grad=True)
+    w = torch.zeros(24, 16, dtype=torch.bfloat16, requires_grad=True)
+    many = torch.zeros(1, 16, dtype=torch.bfloat16).expand(1 << 22, 16)
+    with pytest.raises(ValueError, match="N % 16"):
+        w8.w8_linear(x, w)
+    with torch.no_grad():
+        for a, b in ((x, w), (many, torch.zeros(256, 16, dtype=torch.bfloat16, requires_grad=True))):
+            with pytest.raises(ValueError, match="on a GPU"):
+                w8.w8_linear(a, b)

@@ -501,6 +501,14 @@ def test_linear_partial_gradients_and_refusals():
     assert y3.shape == (2, 3, 16) and x3.grad.shape == (2, 3, 64) and w.grad.shape == (16, 64)
 
 
+def test_linear_without_gradients():
+    X, W = synth.activations(6, 64, 28).to(dev()).requires_grad_(), synth.weights(24, 64, 28).to(dev()).requires_grad_()
+    say("w8_linear under no_grad")
+    with torch.no_grad():                        # N % 16 only matters to X's gradient
+        y = w8.w8_linear(X, W)
+    assert not y.requires_grad and torch.equal(y, w8.w8_linear(X.detach(), W.detach()))
+
+
 # -------------------------------------------------- streams, graphs, repeats --
 
 def test_deterministic_and_on_a_side_stream():
