@@ -31,6 +31,7 @@ of the pages' rollout comparison) behind the scored router:
     H2, weights --w4_moe_sum--> Out [T, H]
 """
 
+import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -343,6 +344,13 @@ def _refuse_gradients(*inputs):
                          "torch.no_grad()")
 
 
+def _on_device_of(X):
+    """X's GPU as the current one, which the INT4 layer's calls take."""
+    if X.get_device() == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(X.device)
+
+
 def moe_forward_w8(X, topk_ids, topk_weights, gate_up, down, B=None, buffers=None):
     """Expert part of the layer for routed tokens on 8-bit experts.
 
@@ -362,16 +370,17 @@ def moe_forward_w8(X, topk_ids, topk_weights, gate_up, down, B=None, buffers=Non
         B = w8_pick_block_size(T, k, E)
     b = buffers or alloc_buffers_w8(T, k, E, H, I, B, X.device)
     w8_quantize_rows(X, b.X8, b.SX)
-    plan = moe_align_block_size(topk_ids, E, B, b.sorted_token_ids, b.expert_ids, b.ntpp)
-    if _fuses_swiglu_w8(T, H, I, B):
-        w8a8_moe_gemm_swiglu(b.X8, b.SX, gate_up.W8, gate_up.SW, *plan, T, k, B, k, b.A8, b.SA)
-    else:
-        if b.H1 is None:
-            raise ValueError("these sizes need buffers with H1 (allocated for the same B)")
-        w8a8_moe_gemm(b.X8, b.SX, gate_up.W8, gate_up.SW, *plan, T, k, B, k, out=b.H1)
-        w8_silu_mul_quantize(b.H1, b.A8, b.SA)
-    w8a8_moe_gemm(b.A8, b.SA, down.W8, down.SW, *plan, T, k, B, 1, out=b.H2)
-    w4_moe_sum(b.H2, topk_weights, T, k, out=b.out)
+    with _on_device_of(X):
+        plan = moe_align_block_size(topk_ids, E, B, b.sorted_token_ids, b.expert_ids, b.ntpp)
+        if _fuses_swiglu_w8(T, H, I, B):
+            w8a8_moe_gemm_swiglu(b.X8, b.SX, gate_up.W8, gate_up.SW, *plan, T, k, B, k, b.A8, b.SA)
+        else:
+            if b.H1 is None:
+                raise ValueError("these sizes need buffers with H1 (allocated for the same B)")
+            w8a8_moe_gemm(b.X8, b.SX, gate_up.W8, gate_up.SW, *plan, T, k, B, k, out=b.H1)
+            w8_silu_mul_quantize(b.H1, b.A8, b.SA)
+        w8a8_moe_gemm(b.A8, b.SA, down.W8, down.SW, *plan, T, k, B, 1, out=b.H2)
+        w4_moe_sum(b.H2, topk_weights, T, k, out=b.out)
     return b.out, b
 
 

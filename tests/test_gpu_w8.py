@@ -417,6 +417,36 @@ def test_layer_row_without_experts_and_buffers():
         moe.moe_forward_w8(X.to(dev()), ids, w, d, g)
 
 
+def test_layer_off_the_current_device(monkeypatch):
+    # on one GPU: the current device said to be another, calls that run on the
+    # current one seen to be inside a switch to X's
+    T, E, k, H, I = 24, 8, 2, 128, 64
+    X, lg, _, _, g, d = layer_case(T, E, k, H, I, 29)
+    X, lg = X.to(dev()), lg.to(dev())
+    want, (ids, w) = moe.moe_layer_w8(X, lg, k, g, d)[0].clone(), w4.w4_moe_route_scored(lg, k)
+    inside, seen, switch = [], [], torch.cuda.device
+
+    class Switch(switch):
+        def __enter__(self):
+            inside.append(self.idx)
+            return super().__enter__()
+
+        def __exit__(self, *a):
+            inside.pop()
+            return super().__exit__(*a)
+    monkeypatch.setattr(torch.cuda, "device", Switch)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for name in ("moe_align_block_size", "w4_moe_sum"):
+        def spy(*a, f=getattr(moe, name), **kw):
+            seen.append(list(inside))
+            return f(*a, **kw)
+        monkeypatch.setattr(moe, name, spy)
+    say("moe_forward_w8 off the current device")
+    out, _ = moe.moe_forward_w8(X, ids, w, g, d)
+    assert seen == [[0], [0]] and not inside
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 16, 16), (5, 144, 272), (70, 256, 400), (300, 528, 256)])
 def test_linear_gradients(M, N, K):
     say(f"w8_linear M={M} N={N} K={K}")
