@@ -339,7 +339,7 @@ def alloc_buffers_w8(T, k, E, H, I, B, device):
 def _refuse_gradients(*inputs):
     """The expert layer has no backward: an input that wants a gradient would
     get none, without a word."""
-    if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
         raise ValueError("the W8A8 expert layer has no backward: detach its inputs, or call it under "
                          "torch.no_grad()")
 

@@ -447,6 +447,17 @@ def test_layer_off_the_current_device(monkeypatch):
     assert torch.equal(out, want)
 
 
+def test_layer_with_other_forms_of_weights():
+    T, E, k, H, I = 24, 8, 2, 128, 64
+    X, lg, _, _, g, d = layer_case(T, E, k, H, I, 30)
+    X = X.to(dev())
+    ids, w = w4.w4_moe_route_scored(lg.to(dev()), k)
+    say("moe_forward_w8 flat weights and none")
+    out = moe.moe_forward_w8(X, ids, w, g, d)[0]
+    assert torch.equal(out, moe.moe_forward_w8(X, ids, w.view(-1), g, d)[0])
+    assert torch.equal(moe.moe_forward_w8(X, ids, torch.ones_like(w), g, d)[0], moe.moe_forward_w8(X, ids, None, g, d)[0])
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 16, 16), (5, 144, 272), (70, 256, 400), (300, 528, 256)])
 def test_linear_gradients(M, N, K):
     say(f"w8_linear M={M} N={N} K={K}")
