@@ -37,7 +37,7 @@ from dataclasses import dataclass
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (moe_align_block_size, w4_moe_align_capacity, w4_moe_combine_workspace_words,
+from . import (_shape, moe_align_block_size, w4_moe_align_capacity, w4_moe_combine_workspace_words,
                w4_moe_route, w4_moe_sum, w4a16_moe_gemm_combine,
                w4_pick_block_size, w4_quantize_pack, w4_quantize_pack_asym, w4_repack,
                w4_repack_groups, w4_silu_mul, w4a16_moe_gemm, w4a16_moe_gemm_asym, w4a16_moe_gemm_swiglu,
@@ -370,6 +370,10 @@ def moe_forward_w8(X, topk_ids, topk_weights, gate_up, down, B=None, buffers=Non
         B = w8_pick_block_size(T, k, E)
     b = buffers or alloc_buffers_w8(T, k, E, H, I, B, X.device)
     w8_quantize_rows(X, b.X8, b.SX)
+    device = X.get_device()
+    _shape(topk_ids, "topk_ids", torch.int32, (T, k), device)
+    if topk_weights is not None and topk_weights.get_device() != device:
+        raise ValueError("topk_weights is on another device than X")
     with _on_device_of(X):
         plan = moe_align_block_size(topk_ids, E, B, b.sorted_token_ids, b.expert_ids, b.ntpp)
         if _fuses_swiglu_w8(T, H, I, B):

@@ -458,6 +458,17 @@ def test_layer_with_other_forms_of_weights():
     assert torch.equal(moe.moe_forward_w8(X, ids, torch.ones_like(w), g, d)[0], moe.moe_forward_w8(X, ids, None, g, d)[0])
 
 
+def test_layer_refuses_routes_of_other_tokens():
+    T, E, k, H, I = 24, 8, 2, 128, 64
+    X, lg, _, _, g, d = layer_case(T, E, k, H, I, 30)
+    X = X.to(dev())
+    ids, w = w4.w4_moe_route_scored(lg.to(dev()), k)
+    say("moe_forward_w8 routes of other tokens")
+    for i, v in ((ids[:20], w), (ids, w[:20]), (ids.cpu(), w), (ids, w.cpu()), (torch.cat([ids, ids]), w)):
+        with pytest.raises(ValueError):
+            moe.moe_forward_w8(X, i, v, g, d)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 16, 16), (5, 144, 272), (70, 256, 400), (300, 528, 256)])
 def test_linear_gradients(M, N, K):
     say(f"w8_linear M={M} N={N} K={K}")
