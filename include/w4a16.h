@@ -564,7 +564,7 @@ int w8_silu_mul_quantize(const uint16_t* H1, int64_t R, int64_t I, uint8_t* A8, 
                          void* stream);
 
 /*
- * w8a8_gemm -- Y = (X8, SX) * (W8, SW)^T, fp32 accumulation:
+ * w8a8_gemm -- Y = (X8, SX) * (W8, SW)^T, fp32 sums of products cut as below:
  *   Y[m, n] = bf16_rne( sum_k X8[m, k] 2^(SX[m, k/128] - 127)
  *                             W8[n, k] 2^(SW[n/128, k/128] - 127) )
  * (order unspecified but fixed).  The matrix unit adds products in groups of
@@ -595,7 +595,9 @@ int32_t w8_pick_block_size(int64_t T, int32_t k, int32_t E);
  * [E, ceil(N/128), C]; Y bf16 [T*k, N].  Rows of Y that no slot names are not
  * written.  Alignment arrays as moe_align_block_size fills them (same T, k, E,
  * B); B a multiple of 16 up to 1024 (W4_ERR_SHAPE, W4_ERR_UNSUPPORTED),
- * x_row_div in {1, k}, E <= 1024, N, K >= 1.  Alignment as w8a8_gemm.
+ * x_row_div in {1, k}, E <= 1024, N, K >= 1.  Alignment as w8a8_gemm.  X8 of
+ * 2 GiB and more goes through a kernel with 64-bit addresses, about ten times as
+ * slow at large B.
  */
 int w8a8_moe_gemm(const uint8_t* X8, const uint8_t* SX, const uint8_t* W8, const uint8_t* SW,
                   const int32_t* sorted_token_ids, const int32_t* expert_ids,

@@ -7,9 +7,11 @@
 // tell apart (sixteen thousand rows of 384 hold several such pairs), and a
 // swapped expert is another result, not a rounding.  Rows whose values 32 bits
 // do tell apart, nearly all, are chosen by those.  One wave per token.
-// 16384 x 384, sigmoid, bias: 18.7 us, 25.3 with 8 groups; bound by vector
-// instructions (430 and 565 a row; the row's 1.5 KB would take 5 us).  72 us when
-// every row is chosen in 64 bits.
+// 16384 x 384, sigmoid, bias: 18.7 us, 25.3 with 8 groups (the row's 1.5 KB would
+// take 5 us): 430 and 565 vector instructions a row, many of them in chains of
+// lane exchanges.  With groups the vector units issue in half to three fifths of
+// the time; a wave spends half its cycles ready and not issuing, and a quarter in
+// waits for memory and LDS.  72 us when every row is chosen in 64 bits.
 #include <cfloat>
 
 #include "w8.h"
@@ -480,9 +482,10 @@ __global__ __launch_bounds__(256) void k_route_scored(const float* __restrict__ 
 // -------------------------------------------------------------- gradient --
 // p over the picks (slots whose weight is zero took no part); the row is put
 // together in LDS and written once.  Slots that name one expert twice add up in
-// slot order.  Bound by the bytes written, but for softmax without
-// renormalisation, where every score takes a 64-bit exponential: 16384 x 384 9.4
-// and 25 us.
+// slot order.  16384 x 384: 9.4 us for 25 MB written and 6 read; the waves spend
+// 77% of their cycles in waits, for the picks' logits, which come one by one, and
+// for the wave that weighs them.  Softmax without renormalisation takes 25 us, a
+// 64-bit exponential for every score.
 template <int NPER>
 __global__ __launch_bounds__(256) void k_route_scored_bwd(const float* __restrict__ logits,
                                                           const int32_t* __restrict__ ids,

@@ -191,9 +191,10 @@ __global__ __launch_bounds__(NW * 64) void k_w8_split(const uint8_t* __restrict_
 // GROUPED: the rows of a tile are sorted pairs of one expert, gathered by the
 // loads.
 //
-// Rates: 4096 x 14336 x 4096 209 us (2.3 PFLOP/s), 8192^3 398 us (2.76), grouped
-// 16384 rows of 32 experts x [4096, 4096] 290 us with SwiGLU (the
-// layer 596 us with the two apart, 556 together); bound by the feed of operands (above).
+// Rates: 4096 x 14336 x 4096 203 to 217 us by card (2.2 to 2.4 PFLOP/s), 8192^3
+// 398 us (2.76), grouped 16384 rows of 32 experts x [4096, 4096] 292 to 298 us
+// with SwiGLU (fusing it took 40 us off the layer); bound by the feed of operands
+// (above).
 // 2048 rows of 128 experts x [4096, 4096] in 64 x 256 tiles read W at 5.3 TB/s.
 //
 // SWIGLU (256 x 256, grouped): W's 2 I rows are gate, then up; a tile takes 128
@@ -716,9 +717,10 @@ int pick(int64_t M, int64_t N, int64_t K, float& us) {
 
 // The split kernel's rows of W and waves per workgroup.  64 rows of W per
 // workgroup share their rows of X, which counts once there are some and N fills
-// the CUs (16 x 12288 x 4096: 12.5 us, 15.9 in 16 rows); else 16, on 16 waves
-// where there are few workgroups and 8 where there are many (4096 x 7168: 7.6 and
-// 9.2 us; 12288 x 4096: 10.7 and 10.0, one row).
+// the CUs (12288 x 4096, 16 rows of X: 12.5 us, 15.9 in 16 rows of W; 8192 x 4096:
+// 12.7 and 11.7; from 9728 on 64 would do for 8 rows and more, 13.3 and 16.4 us
+// at 16); else 16, on 16 waves where there are few workgroups and 8 where there
+// are many (4096 x 7168: 7.6 and 9.2 us; 12288 x 4096: 10.7 and 10.0, one row).
 struct Split {
   int bn, waves;
 };
@@ -799,7 +801,8 @@ int64_t moe_rows(int64_t T, int32_t k, int32_t E, int32_t B) {
 
 // Rows of the grouped product's tiles: a divisor of B.  The tiles gather with
 // 32-bit offsets into X; where X is larger, the split kernel (64-bit
-// addresses) takes the blocks 16 rows at a time.
+// addresses) takes the blocks 16 rows at a time, ten times as long (2^20 rows of
+// 2048 x 32 experts of [4096, 2048]: 93 ms, 9.7 with eight rows less).
 int moe_tile_rows(int64_t rows_x, int64_t K, int32_t B) {
   if (rows_x * K >= (int64_t)kOOB) return 16;
   for (int bm = 256; bm >= 64; bm /= 2)

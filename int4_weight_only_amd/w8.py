@@ -13,9 +13,9 @@ identity, so
   dW = dY^T * X                     bf16, unquantized operands
                                     (``w4_bf16_transpose``, ``w4_bf16_gemm_nt``)
 which covers fewer than 2^22 tokens: more of them are refused in the forward
-where W needs a gradient.  The master weight stays bf16.  The backward is not differentiable again.  To
-capture a backward into a graph, take gradients with ``torch.autograd.grad``, or
-let no eager graph of the same leaves be alive.
+where W needs a gradient.  The master weight stays bf16.  The backward is not
+differentiable again.  To capture a backward into a graph, take gradients with
+``torch.autograd.grad``, or let no eager graph of the same leaves be alive.
 """
 
 import torch
