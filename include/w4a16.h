@@ -668,6 +668,94 @@ int w4_moe_route_scored_bwd(const float* logits, const int32_t* topk_ids,
                             int32_t E, int32_t k, int32_t sigmoid, int32_t renorm, float scale,
                             float* grad_logits, void* stream);
 
+/*
+ * ------------------------------------- training the routed experts (bf16) ----
+ * The experts' products in bf16, in the three directions that a training step
+ * needs, over the aligned pairs of moe_align_block_size; the SwiGLU's gradient;
+ * and the same from activation checkpoints in 8 bits ([RL] §2.1: the training
+ * side keeps bf16 master weights and computes in bf16, the straight-through
+ * estimator passes the gradient through the fake quantization).
+ *  - Alignment arrays as moe_align_block_size fills them (same T, k, E, B); B a
+ *    multiple of 64 up to 1024 (W4_ERR_SHAPE, W4_ERR_UNSUPPORTED): see
+ *    w4_bf16_pick_block_size.
+ *  - A checkpoint is what w8_quantize_rows writes: e4m3 codes [R, K], K % 16 == 0,
+ *    with SX [R, w8_scale_cols(K)]; it stands for bf16_rne(code * 2^(SX - 127)),
+ *    which is exact unless it lies below bf16's normal range.
+ *  - A pair whose expert lies outside [0, E) takes no part in any product; rows
+ *    of outputs that no slot names are not written.
+ *  - Limits: E <= 1024, N and K <= 2^22, T*k + E*B < 2^31, 2^40 elements per
+ *    matrix, 2^32 threads per launch (W4_ERR_UNSUPPORTED).
+ *
+ * w4_bf16_pick_block_size -- alignment block size of these products: the
+ * smallest of 64, 128 and 256 that holds one and a half times the average number
+ * of pairs per expert (256 beyond).  0 if T < 0, k < 1 or E < 1.
+ */
+int32_t w4_bf16_pick_block_size(int64_t T, int32_t k, int32_t E);
+
+/*
+ * w4_bf16_moe_gemm -- for every slot holding a pair f < T*k of a block with
+ * expert e in [0, E):
+ *   Y[f, n] = bf16_rne( sum_k X[f / x_row_div, k] * W[e, n, k] )     transposed == 0
+ *   Y[f, n] = bf16_rne( sum_k X[f / x_row_div, k] * W[e, k, n] )     transposed != 0
+ * with fp32 accumulation (order unspecified but fixed).  The second is the
+ * input gradient of the first: X the gradient of its Y, W the same weights.
+ * X bf16 [(T*k) / x_row_div, K], W bf16 [E, N, K] or [E, K, N], both 16-byte
+ * aligned; Y bf16 [T*k, N], 2-byte aligned.  K % 8 == 0, and N % 8 == 0 where
+ * transposed; N, K >= 1; x_row_div in {1, k} (W4_ERR_SHAPE).  T == 0 is a no-op.
+ */
+int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted_token_ids,
+                     const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
+                     uint16_t* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K,
+                     int32_t B, int32_t x_row_div, int32_t transposed, void* stream);
+
+/*
+ * w4_bf16_moe_wgrad -- the weight gradient of w4_bf16_moe_gemm (transposed == 0):
+ *   dW[e, n, k] = bf16_rne( sum over the pairs f of expert e of
+ *                           dY[f / dy_row_div, n] * X[f / x_row_div, k] )
+ * with fp32 accumulation (order unspecified but fixed), and zeros for an expert
+ * without pairs.  dY bf16 [(T*k) / dy_row_div, N]; X bf16 [(T*k) / x_row_div, K],
+ * or with SX a checkpoint of such rows; dW bf16 [E, N, K], written whole; all
+ * 16-byte aligned, SX 4-byte.  N % 8 == 0, K % 8 == 0 (16 with SX), both >= 1;
+ * dy_row_div and x_row_div in {1, k} (W4_ERR_SHAPE).  T == 0 writes zeros.
+ */
+int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,
+                      const int32_t* sorted_token_ids, const int32_t* expert_ids,
+                      const int32_t* num_tokens_post_padded, uint16_t* dW, int64_t T, int32_t k,
+                      int32_t E, int64_t N, int64_t K, int32_t B, int32_t dy_row_div,
+                      int32_t x_row_div, void* stream);
+
+/*
+ * w4_bf16_gemm_tn -- C = A^T B, summed over the rows that both have (a linear
+ * layer's weight gradient dW = dY^T X from the operands as they are):
+ *   C[n, k] = bf16_rne( sum_m A[m, n] * B[m, k] )
+ * with fp32 accumulation (order unspecified but fixed).  A bf16 [M, N]; B bf16
+ * [M, K], or with SB a checkpoint of such rows; C bf16 [N, K]; all 16-byte
+ * aligned, SB 4-byte.  N % 8 == 0, K % 8 == 0 (16 with SB) (W4_ERR_SHAPE).
+ * N*K == 0 is a no-op; M == 0 writes zeros.
+ */
+int w4_bf16_gemm_tn(const uint16_t* A, const void* B, const uint8_t* SB, uint16_t* C, int64_t M,
+                    int64_t N, int64_t K, void* stream);
+
+/*
+ * w4_silu_mul_bwd -- gradient of the SwiGLU between the expert projections and
+ * of the top-k weight that follows them, with the activation computed again.
+ * For row r, with g = H1[r, i], u = H1[r, I + i], s = 1 / (1 + e^-g), w =
+ * weights[r] (NULL: 1) and dA the gradient of the down product's input before
+ * the weight is applied (out = sum_j w_j W a_j, dA = W^T dout):
+ *   dH1[r, i]     = bf16_rne( w * dA * u * s * (1 + g * (1 - s)) )
+ *   dH1[r, I + i] = bf16_rne( w * dA * g * s )
+ *   A[r, i]       = bf16_rne( w * g * s * u )         (unless A is NULL)
+ *   dw[r]         = sum_i dA[r, i] * g * s * u        (unless dw is NULL; fp32)
+ * so that dW_down = w4_bf16_moe_wgrad(dout, A), and neither the activation nor
+ * the down product's output need be kept.  fp32 arithmetic, good to a few units
+ * in the last place (dw: of the largest terms).  H1 bf16 [R, 2I], or with SH a
+ * checkpoint of such rows (I % 8 == 0 is enough for it here); dA, A bf16 [R, I],
+ * dH1 bf16 [R, 2I], all 16-byte aligned; weights, dw fp32 [R].  I % 8 == 0.
+ * R or I == 0 is a no-op, but for dw, which is written as zeros where I == 0.
+ */
+int w4_silu_mul_bwd(const void* H1, const uint8_t* SH, const uint16_t* dA, const float* weights,
+                    int64_t R, int64_t I, uint16_t* dH1, uint16_t* A, float* dw, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,7 +20,9 @@ Layouts (all row-major, contiguous, on one GPU):
           the *_tiled products read Wt, St and Zt and take N explicitly
   X8, W8  float8_e4m3fn [M, K], [N, K] or [E, N, K]   codes of the W8A8 products
   SX, SW  float8_e8m0fnu [M, C], [ceil(N/128), C] or [E, ceil(N/128), C]   one
-          scale per 128 k of a row / per 128 x 128 block; C = w8_scale_cols(K)
+          scale per 128 k of a row / per 128 x 128 block; C = w8_scale_cols(K).
+          X8 with SX is also an activation checkpoint: what the bf16 products of
+          training take in place of the bf16 rows
 """
 
 import math
@@ -43,6 +45,8 @@ __all__ = [
     "w8_scale_cols", "w8_quantize_rows", "w8_quantize_blocks", "w8_silu_mul_quantize", "w8a8_gemm",
     "w8_pick_block_size", "w8a8_moe_gemm", "w8a8_moe_gemm_swiglu", "w4_moe_route_scored",
     "w4_moe_route_scored_bwd",
+    "w4_bf16_pick_block_size", "w4_bf16_moe_gemm", "w4_bf16_moe_wgrad", "w4_bf16_gemm_tn",
+    "w4_silu_mul_bwd",
 ]
 
 
@@ -1015,3 +1019,119 @@ def w4_moe_route_scored_bwd(logits, topk_ids, topk_weights, grad_weights, sigmoi
           topk_weights.data_ptr(), grad_weights.data_ptr(), T, E, shape[1], int(sigmoid), int(renorm),
           scale, grad_logits.data_ptr())
     return grad_logits
+
+
+# ------------------------------------------------- training the routed experts --
+
+def w4_bf16_pick_block_size(T, k, E):
+    return int(_lib.load().w4_bf16_pick_block_size(T, k, E))
+
+
+def _bf16_plan(sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, E, B, device):
+    """The alignment arrays' pointers, checked."""
+    if T < 0 or k < 1 or B < 1:
+        raise ValueError("invalid T, k or B")
+    cap = (T * k + E * (B - 1) + B - 1) // B * B
+    _ints(sorted_token_ids, "sorted_token_ids", cap, device)
+    _ints(expert_ids, "expert_ids", cap // B, device)
+    _ints(num_tokens_post_padded, "num_tokens_post_padded", 1, device)
+    return sorted_token_ids.data_ptr(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr()
+
+
+def _pair_rows(t, name, dtype, T, k, div, device=None):
+    """(device, columns) of an operand with a row per ``div`` pairs."""
+    if div != 1 and div != k:
+        raise ValueError(f"{name}'s row divisor must be 1 or k")
+    device = _in(t, name, dtype, 2, device)
+    if t.shape[0] != T * k // div:
+        raise ValueError(f"{name} must have {T * k // div} rows, got {t.shape[0]}")
+    return device, t.shape[1]
+
+
+def _rows_or_codes(scales):
+    return _BF16 if scales is None else _E4M3
+
+
+def w4_bf16_moe_gemm(X, W, sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, B, x_row_div,
+                     transposed=False, out=None):
+    """Grouped bf16 expert product over aligned blocks of B (a multiple of 64).
+
+    Row f of ``out`` bf16 [T*k, N] = row f // x_row_div of X bf16 times W[e]^T
+    (W bf16 [E, N, K]), or times W[e] (``transposed``, W [E, K, N]: the input
+    gradient), for every valid slot f of every block with e = expert_ids[b].
+    Other rows are not written.
+    """
+    device, K = _pair_rows(X, "X", _BF16, T, k, x_row_div)
+    _in(W, "W", _BF16, 3, device)
+    E, N, KW = W.shape
+    if transposed:
+        N, KW = KW, N
+    if KW != K:
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)} W {tuple(W.shape)}")
+    plan = _bf16_plan(sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, E, B, device)
+    out = _out(out, "out", (T * k, N), _BF16, X)
+    _call("w4_bf16_moe_gemm", device, X.data_ptr(), W.data_ptr(), *plan, out.data_ptr(), T, k, E, N, K,
+          B, x_row_div, int(transposed))
+    return out
+
+
+def w4_bf16_moe_wgrad(dY, X, sorted_token_ids, expert_ids, num_tokens_post_padded, E, T, k, B,
+                      dy_row_div, x_row_div, SX=None, out=None):
+    """Weight gradient of ``w4_bf16_moe_gemm``: bf16 [E, N, K], expert e's the sum
+    over its pairs f of dY[f // dy_row_div]^T X[f // x_row_div], zeros where it has
+    none.  dY bf16; X bf16, or with SX a checkpoint (``w8_quantize_rows``)."""
+    device, N = _pair_rows(dY, "dY", _BF16, T, k, dy_row_div)
+    _, K = _pair_rows(X, "X", _rows_or_codes(SX), T, k, x_row_div, device)
+    if SX is not None:
+        _shape(SX, "SX", _E8M0, (X.shape[0], w8_scale_cols(K)), device)
+    if E < 1:
+        raise ValueError("E must be at least 1")
+    plan = _bf16_plan(sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, E, B, device)
+    out = _out(out, "out", (E, N, K), _BF16, dY)
+    _call("w4_bf16_moe_wgrad", device, dY.data_ptr(), X.data_ptr(), _ptr(SX), *plan, out.data_ptr(), T, k,
+          E, N, K, B, dy_row_div, x_row_div)
+    return out
+
+
+def w4_bf16_gemm_tn(A, B, SB=None, out=None):
+    """bf16 A [M, N], B [M, K] -> bf16 [N, K] = A^T B; B bf16, or with SB a
+    checkpoint (``w8_quantize_rows``)."""
+    device = _in(A, "A", _BF16, 2)
+    _in(B, "B", _rows_or_codes(SB), 2, device)
+    M, N = A.shape
+    K = B.shape[1]
+    if B.shape[0] != M:
+        raise ValueError(f"shape mismatch: A {tuple(A.shape)} B {tuple(B.shape)}")
+    if SB is not None:
+        _shape(SB, "SB", _E8M0, (M, w8_scale_cols(K)), device)
+    out = _out(out, "out", (N, K), _BF16, A)
+    _call("w4_bf16_gemm_tn", device, A.data_ptr(), B.data_ptr(), _ptr(SB), out.data_ptr(), M, N, K)
+    return out
+
+
+def w4_silu_mul_bwd(H1, dA, weights=None, SH=None, dH1=None, A=None, dw=None):
+    """Gradient of the SwiGLU and of the top-k weight behind it: (dH1 bf16 [R,
+    2I], A bf16 [R, I], dw fp32 [R]).
+
+    H1 bf16 [R, 2I] (gate, up), or with SH a checkpoint of it; dA bf16 [R, I] the
+    gradient of the down product's input before the weight; ``weights`` fp32, R
+    of them (None: ones).  A is the activation again, times the weight; dw the
+    weight's gradient.
+    """
+    device = _in(H1, "H1", _rows_or_codes(SH), 2)
+    R, I2 = H1.shape
+    if I2 % 2:
+        raise ValueError("H1 must have an even number of columns")
+    I = I2 // 2
+    _shape(dA, "dA", _BF16, (R, I), device)
+    if SH is not None:
+        _shape(SH, "SH", _E8M0, (R, w8_scale_cols(I2)), device)
+    if weights is not None:
+        if _in(weights, "weights", _F32, weights.dim(), device) != device or weights.numel() != R:
+            raise ValueError(f"weights must have {R} entries")
+    dH1 = _out(dH1, "dH1", (R, I2), _BF16, dA)
+    A = _out(A, "A", (R, I), _BF16, dA)
+    dw = _out(dw, "dw", (R,), _F32, dA)
+    _call("w4_silu_mul_bwd", device, H1.data_ptr(), _ptr(SH), dA.data_ptr(), _ptr(weights), R, I,
+          dH1.data_ptr(), A.data_ptr(), dw.data_ptr())
+    return dH1, A, dw

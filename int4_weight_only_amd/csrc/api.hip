@@ -5,6 +5,7 @@
 // allocates, synchronizes or reads device memory.
 #include "w4a16.h"
 
+#include "bf16.h"
 #include "common.h"
 #include "w8.h"
 
@@ -777,6 +778,113 @@ int w4_moe_route_scored_bwd(const float* logits, const int32_t* topk_ids,
   const w4::RouteRule r = {sigmoid != 0, 1, 1, 1, renorm != 0, scale};
   return hip_status(w4::launch_route_scored_bwd(logits, topk_ids, topk_weights, grad_weights, T, E,
                                                 k, r, grad_logits, as_stream(stream)));
+}
+
+}  // extern "C"
+
+// ------------------------------------------- training the routed experts --
+
+namespace {
+
+constexpr int64_t kBf16MaxCols = (int64_t)1 << 22;
+
+// Sizes and alignment arrays shared by the grouped bf16 products; W4_OK or an
+// error status.
+int bf16_moe_validate(const int32_t* sorted_token_ids, const int32_t* expert_ids,
+                      const int32_t* num_tokens_post_padded, int64_t T, int32_t k, int32_t E,
+                      int64_t N, int64_t K, int32_t B) {
+  if (T < 0 || k < 1 || E < 1 || N < 1 || K < 1 || K % 8 != 0 || B < 64 || B % 64 != 0)
+    return W4_ERR_SHAPE;
+  if (B > 1024 || E > 1024 || T > kMaxI32 || N > kBf16MaxCols || K > kBf16MaxCols ||
+      T * k + (int64_t)E * B >= kMaxI32 || T * k * N > kMaxElems || T * k * K > kMaxElems ||
+      E * (N * K) > kMaxElems)
+    return W4_ERR_UNSUPPORTED;
+  if (!sorted_token_ids || !expert_ids || !num_tokens_post_padded) return W4_ERR_NULL;
+  if (!aligned(sorted_token_ids, 4) || !aligned(expert_ids, 4) ||
+      !aligned(num_tokens_post_padded, 4))
+    return W4_ERR_MISALIGNED;
+  return W4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t w4_bf16_pick_block_size(int64_t T, int32_t k, int32_t E) {
+  if (T < 0 || k < 1 || E < 1) return 0;
+  if (T > ((int64_t)1 << 40) / k) return 256;
+  int32_t B = 64;
+  while (B < 256 && 2 * (int64_t)B * E < 3 * T * k) B *= 2;
+  return B;
+}
+
+int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted_token_ids,
+                     const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
+                     uint16_t* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K,
+                     int32_t B, int32_t x_row_div, int32_t transposed, void* stream) {
+  const int v = bf16_moe_validate(sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, E, N,
+                                  K, B);
+  if (v == W4_ERR_SHAPE) return v;
+  if ((x_row_div != 1 && x_row_div != k) || (transposed && N % 8 != 0)) return W4_ERR_SHAPE;
+  if (v == W4_ERR_UNSUPPORTED || w4::bf16_moe_threads(T * k, E, N, K, B) >= kMaxGrid)
+    return W4_ERR_UNSUPPORTED;
+  if (T == 0) return W4_OK;
+  if (v != W4_OK) return v;
+  if (!X || !W || !Y) return W4_ERR_NULL;
+  if (!aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 2)) return W4_ERR_MISALIGNED;
+  const w4::Bf16Plan plan = {sorted_token_ids, expert_ids, num_tokens_post_padded, T * k, E, B};
+  return hip_status(w4::launch_bf16_moe_gemm(X, W, Y, plan, N, K, x_row_div, transposed != 0,
+                                             as_stream(stream)));
+}
+
+int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,
+                      const int32_t* sorted_token_ids, const int32_t* expert_ids,
+                      const int32_t* num_tokens_post_padded, uint16_t* dW, int64_t T, int32_t k,
+                      int32_t E, int64_t N, int64_t K, int32_t B, int32_t dy_row_div,
+                      int32_t x_row_div, void* stream) {
+  const int v = bf16_moe_validate(sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, E, N,
+                                  K, B);
+  if (v == W4_ERR_SHAPE) return v;
+  if ((dy_row_div != 1 && dy_row_div != k) || (x_row_div != 1 && x_row_div != k) || N % 8 != 0 ||
+      (SX && K % 16 != 0))
+    return W4_ERR_SHAPE;
+  if (v == W4_ERR_UNSUPPORTED || w4::bf16_wgrad_threads(E, N, K) >= kMaxGrid)
+    return W4_ERR_UNSUPPORTED;
+  if (v != W4_OK) return v;
+  if (!dW || (T > 0 && (!dY || !X))) return W4_ERR_NULL;
+  if (!aligned(dY, 16) || !aligned(X, 16) || !aligned(SX, 4) || !aligned(dW, 16))
+    return W4_ERR_MISALIGNED;
+  const w4::Bf16Plan plan = {sorted_token_ids, expert_ids, num_tokens_post_padded, T * k, E, B};
+  return hip_status(w4::launch_bf16_moe_wgrad(dY, {X, SX}, dW, plan, N, K, dy_row_div, x_row_div,
+                                              as_stream(stream)));
+}
+
+int w4_bf16_gemm_tn(const uint16_t* A, const void* B, const uint8_t* SB, uint16_t* C, int64_t M,
+                    int64_t N, int64_t K, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || N % 8 != 0 || K % 8 != 0 || (SB && K % 16 != 0))
+    return W4_ERR_SHAPE;
+  if (M > kMaxI32 || N > kBf16MaxCols || K > kBf16MaxCols || M * N > kMaxElems ||
+      M * K > kMaxElems || N * K > kMaxElems || w4::bf16_wgrad_threads(1, N, K) >= kMaxGrid)
+    return W4_ERR_UNSUPPORTED;
+  if (N == 0 || K == 0) return W4_OK;
+  if (!C || (M > 0 && (!A || !B))) return W4_ERR_NULL;
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(SB, 4) || !aligned(C, 16))
+    return W4_ERR_MISALIGNED;
+  if (M == 0) return hip_status(w4::launch_zero_bf16(C, N * K, as_stream(stream)));
+  return hip_status(w4::launch_bf16_gemm_tn(A, {B, SB}, C, M, N, K, as_stream(stream)));
+}
+
+int w4_silu_mul_bwd(const void* H1, const uint8_t* SH, const uint16_t* dA, const float* weights,
+                    int64_t R, int64_t I, uint16_t* dH1, uint16_t* A, float* dw, void* stream) {
+  if (R < 0 || I < 0 || I % 8 != 0) return W4_ERR_SHAPE;
+  if (R > kMaxI32 || I > kBf16MaxCols || R * I > kMaxElems) return W4_ERR_UNSUPPORTED;
+  if (R == 0 || (I == 0 && !dw)) return W4_OK;
+  if (I > 0 && (!H1 || !dA || !dH1)) return W4_ERR_NULL;
+  if (!aligned(H1, 16) || !aligned(SH, 4) || !aligned(dA, 16) || !aligned(weights, 4) ||
+      !aligned(dH1, 16) || !aligned(A, 16) || !aligned(dw, 4))
+    return W4_ERR_MISALIGNED;
+  return hip_status(w4::launch_silu_mul_bwd({H1, SH}, dA, weights, R, I, dH1, A, dw,
+                                            as_stream(stream)));
 }
 
 }  // extern "C"

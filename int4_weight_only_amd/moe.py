@@ -29,6 +29,17 @@ of the pages' rollout comparison) behind the scored router:
        then w8_silu_mul_quantize --> A8, SA: the same bits)
     A8 --w8a8_moe_gemm (down, x_row_div = 1)--> H2 [T*k, H]
     H2, weights --w4_moe_sum--> Out [T, H]
+
+``moe_train`` is the layer with gradients, on bf16 master weights: the forward
+runs on their INT4 codes (the straight-through estimator of §2.1) or on the
+weights themselves, the backward in bf16 products grouped by expert, with the
+activations between kept in bf16 or as 8-bit checkpoints:
+
+    dOut --w4_bf16_moe_gemm (down, transposed, x_row_div = k)--> G [T*k, I]
+    H1, G, weights --w4_silu_mul_bwd--> dH1 [T*k, 2I], A [T*k, I], dweights
+    dOut, A --w4_bf16_moe_wgrad--> ddown [E, H, I]
+    dH1, X --w4_bf16_moe_wgrad--> dgate_up [E, 2I, H]
+    dH1 --w4_bf16_moe_gemm (gate_up, transposed)--> [T*k, H] --w4_moe_sum--> dX
 """
 
 import contextlib
@@ -37,10 +48,11 @@ from dataclasses import dataclass
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (_shape, moe_align_block_size, w4_moe_align_capacity, w4_moe_combine_workspace_words,
+from . import (_in, _shape, moe_align_block_size, w4_bf16_moe_gemm, w4_bf16_moe_wgrad,
+               w4_bf16_pick_block_size, w4_dequant, w4_moe_align_capacity, w4_moe_combine_workspace_words,
                w4_moe_route, w4_moe_sum, w4a16_moe_gemm_combine,
                w4_pick_block_size, w4_quantize_pack, w4_quantize_pack_asym, w4_repack,
-               w4_repack_groups, w4_silu_mul, w4a16_moe_gemm, w4a16_moe_gemm_asym, w4a16_moe_gemm_swiglu,
+               w4_repack_groups, w4_silu_mul, w4_silu_mul_bwd, w4a16_moe_gemm, w4a16_moe_gemm_asym, w4a16_moe_gemm_swiglu,
                w4a16_moe_gemm_swiglu_asym, w4a16_moe_gemm_swiglu_tiled, w4a16_moe_gemm_tiled,
                w4_moe_route_scored, w4_moe_route_scored_bwd, w8_pick_block_size,
                w8_quantize_blocks, w8_quantize_rows, w8_scale_cols, w8_silu_mul_quantize,
@@ -397,3 +409,107 @@ def moe_layer_w8(X, logits, k, gate_up, down, sigmoid=False, bias=None, groups=1
                                  scale, *((buffers.ids, buffers.weights) if buffers else ()))
     out, b = moe_forward_w8(X, ids, w, gate_up, down, B, buffers)
     return out, ids, w, b
+
+
+# ------------------------------------------------------ training the experts --
+
+class RoutedExperts(torch.autograd.Function):
+    """The routed layer behind ``moe_train``: out [T, H], with gradients to X,
+    the top-k weights and both stacks of experts."""
+
+    @staticmethod
+    def forward(ctx, X, weights, gate_up, down, topk_ids, int4, checkpoint, B, grad):
+        with _on_device_of(X):
+            T, H = X.shape
+            k = topk_ids.shape[1]
+            E, I = gate_up.shape[0], down.shape[2]
+            plan = moe_align_block_size(topk_ids, E, B)
+
+            def product(x, w, div):
+                if int4:
+                    return w4a16_moe_gemm(x, *w, *plan, T, k, B, div), w
+                return w4_bf16_moe_gemm(x, w, *plan, T, k, B, div), (w, None)
+            H1, up = product(X, _int4_codes(gate_up) if int4 else gate_up, k)
+            H2, dn = product(w4_silu_mul(H1), _int4_codes(down) if int4 else down, 1)
+            out = w4_moe_sum(H2, weights, T, k)
+            need_x, need_w, need_up, need_dn = (n and grad for n in ctx.needs_input_grad[:4])
+            inner = need_x or need_up
+            XS = HS = None
+            if checkpoint:
+                if need_up:
+                    X, XS = w8_quantize_rows(X)
+                if inner or need_w or need_dn:
+                    H1, HS = w8_quantize_rows(H1)
+            ctx.save_for_backward(X if need_up else None, XS, H1 if inner or need_w or need_dn else None,
+                                  HS, weights, *(up if need_x else (None, None)),
+                                  *(dn if inner or need_w else (None, None)), *plan)
+            ctx.sizes = T, k, E, H, I, B
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        X, XS, H1, HS, weights, up, up_s, dn, dn_s, *plan = ctx.saved_tensors
+        T, k, E, H, I, B = ctx.sizes
+        need_x, need_w, need_up, need_dn = ctx.needs_input_grad[:4]
+        dX = dw = d_up = d_dn = None
+        with _on_device_of(grad_out):
+            dO = grad_out.to(torch.bfloat16).contiguous()
+            if need_x or need_up or need_w:
+                Wd = dn if dn_s is None else w4_dequant(dn.view(E * H, I // 8), dn_s.view(E * H, I // 32))
+                G = w4_bf16_moe_gemm(dO, Wd.view(E, H, I), *plan, T, k, B, k, transposed=True)
+            else:                                  # only the activation is needed
+                G = H1.new_zeros((T * k, I), dtype=torch.bfloat16)
+            dH1, A, dw = w4_silu_mul_bwd(H1, G, weights, HS)
+            if need_dn:
+                d_dn = w4_bf16_moe_wgrad(dO, A, *plan, E, T, k, B, k, 1)
+            if need_up:
+                d_up = w4_bf16_moe_wgrad(dH1, X, *plan, E, T, k, B, 1, k, XS)
+            if need_x:
+                Wu = up if up_s is None else w4_dequant(up.view(E * 2 * I, H // 8), up_s.view(E * 2 * I, H // 32))
+                dXp = w4_bf16_moe_gemm(dH1, Wu.view(E, 2 * I, H), *plan, T, k, B, 1, transposed=True)
+                dX = w4_moe_sum(dXp, None, T, k)
+        return (dX, dw.view(T, k) if need_w else None, d_up, d_dn, *(None,) * 5)
+
+
+def _int4_codes(W):
+    """Packed codes and scales of stacked experts bf16 [E, N, K]."""
+    E, N, K = W.shape
+    Wq, S = w4_quantize_pack(W.view(E * N, K))
+    return Wq.view(E, N, K // 8), S.view(E, N, K // 32)
+
+
+def moe_train(X, topk_ids, topk_weights, gate_up, down, int4=False, checkpoint=False, B=None):
+    """Expert part of the layer for routed tokens, differentiable.
+
+    X bf16 [T, H]; topk_ids int32 [T, k], all in [0, E); topk_weights fp32 [T,
+    k] (``route_scored`` gives them a gradient to the logits); gate_up bf16 [E,
+    2I, H] and down bf16 [E, H, I], master weights.  ``int4``: the products run on
+    the weights' INT4 codes, so that the output is ``moe_forward``'s bit for bit, and
+    the straight-through estimator passes the gradient to the weights (H, I
+    multiples of 32).  ``checkpoint``: X and the gate_up product are kept for the
+    backward as e4m3 codes (``w8_quantize_rows``), half the bytes; the output does
+    not change, the gradients of the weights, of X and of the top-k weights are
+    those at the kept values (H, 2I multiples of 16).  Otherwise H, I multiples of
+    8.  B defaults to ``w4_bf16_pick_block_size``.  Returns out bf16 [T, H].  The
+    backward is not differentiable again.
+    """
+    device = _in(X, "X", torch.bfloat16, 2)
+    T, H = X.shape
+    _in(topk_ids, "topk_ids", torch.int32, 2, device)
+    k = topk_ids.shape[1]
+    _shape(topk_ids, "topk_ids", torch.int32, (T, k), device)
+    _shape(topk_weights, "topk_weights", torch.float32, (T, k), device)
+    _in(gate_up, "gate_up", torch.bfloat16, 3, device)
+    _in(down, "down", torch.bfloat16, 3, device)
+    E, I = gate_up.shape[0], down.shape[2]
+    if gate_up.shape != (E, 2 * I, H) or down.shape != (E, H, I):
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)} gate_up {tuple(gate_up.shape)} "
+                         f"down {tuple(down.shape)}")
+    step = 32 if int4 else 16 if checkpoint else 8
+    if H % step or I % (8 if step == 16 else step) or k < 1 or I < 1 or H < 1:
+        raise ValueError(f"H and I must be multiples of {step}, and k at least 1")
+    if B is None:
+        B = w4_bf16_pick_block_size(T, k, E)
+    return RoutedExperts.apply(X, topk_weights, gate_up, down, topk_ids, int4, checkpoint, B,
+                               torch.is_grad_enabled())

@@ -27,12 +27,17 @@ from the packed codes the forward made (bit-exact with fake quant) and
 dW = dY^T * X runs in the library too: ``w4_bf16_transpose`` writes dY^T and
 X^T with the token dimension padded to a multiple of 8 (zeros), and
 ``w4_bf16_gemm_nt`` contracts over it.
+
+With ``checkpoint`` the layer keeps its input for the weight gradient as e4m3
+codes with a power-of-two scale per 128 (``w8_quantize_rows``), half the bytes,
+and dW = dY^T * Q(X) is taken from them (``w4_bf16_gemm_tn``).  Output and input
+gradient do not change.
 """
 
 import torch
 
-from . import (w4_bf16_gemm_nt, w4_bf16_transpose, w4_dequant_t, w4_fake_quant, w4_quantize_pack,
-               w4a16_gemm)
+from . import (w4_bf16_gemm_nt, w4_bf16_gemm_tn, w4_bf16_transpose, w4_dequant_t, w4_fake_quant,
+               w4_quantize_pack, w4a16_gemm, w8_quantize_rows)
 
 __all__ = ["FakeInt4STE", "fake_quant_ste", "Int4QATLinear", "qat_linear"]
 
@@ -60,7 +65,7 @@ class Int4QATLinear(torch.autograd.Function):
     backward to the bf16 master weight."""
 
     @staticmethod
-    def forward(ctx, X, W):
+    def forward(ctx, X, W, checkpoint=False, grad=True):
         N, K = W.shape
         if X.shape[-1] != K:
             raise ValueError(f"X has {X.shape[-1]} features, W expects {K}")
@@ -68,13 +73,18 @@ class Int4QATLinear(torch.autograd.Function):
         X2 = X.reshape(-1, K).contiguous()
         Wq, S = w4_quantize_pack(W)
         Y = w4a16_gemm(X2, Wq, S)
-        ctx.save_for_backward(X2, Wq, S)
+        SX = None
+        if checkpoint and grad and ctx.needs_input_grad[1]:
+            if N % 8:
+                raise ValueError(f"the weight gradient from a checkpoint needs N % 8 == 0 (N = {N})")
+            X2, SX = w8_quantize_rows(X2)
+        ctx.save_for_backward(X2, SX, Wq, S)
         ctx.x_shape = X.shape
         return Y.reshape(*X.shape[:-1], N)
 
     @staticmethod
     def backward(ctx, grad_out):
-        X2, Wq, S = ctx.saved_tensors
+        X2, SX, Wq, S = ctx.saved_tensors
         N = Wq.shape[0]
         dY = grad_out.reshape(-1, N).to(torch.bfloat16).contiguous()
         dX = dW = None
@@ -82,13 +92,16 @@ class Int4QATLinear(torch.autograd.Function):
             if N % 8:
                 raise ValueError(f"the QAT input gradient needs N % 8 == 0 (N = {N})")
             dX = w4_bf16_gemm_nt(dY, w4_dequant_t(Wq, S)).reshape(ctx.x_shape)
-        if ctx.needs_input_grad[1]:
+        if ctx.needs_input_grad[1] and SX is not None:
+            dW = w4_bf16_gemm_tn(dY, X2, SX)
+        elif ctx.needs_input_grad[1]:
             Mp = (dY.shape[0] + 7) // 8 * 8
             dW = w4_bf16_gemm_nt(w4_bf16_transpose(dY, Mp), w4_bf16_transpose(X2, Mp))
-        return dX, dW
+        return dX, dW, None, None
 
 
-def qat_linear(X, W):
+def qat_linear(X, W, checkpoint=False):
     """QAT linear layer without bias: X bf16 [..., K], W bf16 [N, K]
-    (K % 32 == 0) -> bf16 [..., N] = X * fake_quant(W)^T."""
-    return Int4QATLinear.apply(X, W)
+    (K % 32 == 0) -> bf16 [..., N] = X * fake_quant(W)^T.  ``checkpoint``: the
+    backward keeps X as 8-bit codes (N % 8 == 0 where W needs a gradient)."""
+    return Int4QATLinear.apply(X, W, checkpoint, torch.is_grad_enabled())
