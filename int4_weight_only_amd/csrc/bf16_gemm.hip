@@ -7,6 +7,9 @@
 //
 // Bf16 operands, fp32 accumulation in a fixed order, one rounding to bf16.  The
 // second operand of a sum may be a checkpoint of e4m3 codes.
+#include <algorithm>
+#include <type_traits>
+
 #include "bf16.h"
 
 namespace w4 {
@@ -176,50 +179,627 @@ __global__ __launch_bounds__(256) void k_bf16_simple(Job j) {
   }
 }
 
+// --------------------------------------------------------------- LDS tile --
+// A workgroup of four waves computes BM = 32 MI rows of C times BN = 32 NI
+// columns, wave (wm, wn) of the 2 x 2 waves 16 MI x 16 NI of them as MI x NI tiles
+// of v_mfma_f32_16x16x32_bf16.  Both operands go from memory straight into LDS
+// (16-byte buffer_load ... lds), 64 of the summed dimension per step.  An operand
+// whose rows run along the sum is stored [row][64], its eight 16-byte pieces
+// XOR-swizzled by (row / 2) % 8.  One whose rows run across it (TA, TB: weights in
+// the input gradient, both operands of a weight gradient) is stored as it lies in
+// memory, [64][BM or BN], in units of 32 bytes XOR-swizzled by its row, and read
+// through ds_read_b64_tr_b16, which hands four rows of 16 columns to 16 lanes
+// column-wise: the transposition costs no instruction, and the swizzle spreads the
+// eight rows that 32 lanes read over all banks.
+namespace {
+
+constexpr uint32_t kOOB = 0x80000000u;   // byte offset past any buffer: reads 0
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+
+// p and bytes are the same in every lane; said so, or each load would loop
+// over the resources of the lanes
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  const uint64_t u = (uint64_t)uniform((uint32_t)(a >> 32)) << 32 | uniform((uint32_t)a);
+  return __builtin_amdgcn_make_buffer_rsrc((void*)u, (short)0, (int)uniform((uint32_t)bytes),
+                                           0x00020000);
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off,
+                                           uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 16, off, soff, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 4, off, 0, 0, 0);
+}
+
+// Four rows of 16 columns, column-wise: lane c of each 16 gets column c.
+__device__ __forceinline__ u32x2 read_tr(const uint8_t* s) {
+  return __builtin_bit_cast(
+      u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                 (__attribute__((address_space(3))) i16x4*)(__attribute__((address_space(3))) void*)s));
+}
+
+// Four consecutive outputs n .. n + 3 of a row; vec: whole and aligned.
+__device__ __forceinline__ void store4(uint16_t* row, int64_t n, int64_t N, f32x4 s, bool vec) {
+  if (n >= N) return;
+  const u32x2 o = {pk_bf16(s.x, s.y), pk_bf16(s.z, s.w)};
+  uint16_t* y = row + n;
+  if (vec) {
+    *(u32x2*)y = o;
+    return;
+  }
+  y[0] = (uint16_t)o.x;
+  if (n + 1 < N) y[1] = (uint16_t)(o.x >> 16);
+  if (n + 2 < N) y[2] = (uint16_t)o.y;
+  if (n + 3 < N) y[3] = (uint16_t)(o.y >> 16);
+}
+
+// f / d for f < 2^31, with m = floor(2^32 / d) + 1 (d > 1): the high product is the
+// quotient or one more.
+struct Div {
+  uint32_t d, m;
+};
+__device__ __forceinline__ uint32_t div_by(uint32_t f, Div v) {
+  if (v.d == 1) return f;
+  const uint32_t q = __umulhi(f, v.m);
+  return q * v.d > f ? q - 1 : q;
+}
+
+// Swizzle of a row (of the summed dimension) in units of 32 bytes: the eight
+// rows {0..3, 8..11} (or {4..7, 12..15}) that 32 lanes read together get eight
+// different places in 256 bytes.
+template <int RB>
+__device__ __forceinline__ int tr_swizzle(int row) {
+  return RB >= 256 ? (row & 3) | ((row >> 3) & 1) << 2 : ((row >> 1) & 1) | ((row >> 3) & 1) << 1;
+}
+
+struct Operand {           // 16 rows x 64 of the sum: two MFMA operands
+  u32x4 lo, hi;
+};
+
+}  // namespace
+
+// Large tiles (NST 2 or 3 stages) multiply a step in four quarters, (A low, B low),
+// (A low, B high), (A high, B high), (A high, B low), so that a wave holds its
+// operands once and reads them during the quarters before: the high halves in the
+// first, then, when the next stage has landed, its low halves in the third and
+// fourth, into registers whose half is done (B's two sets swap roles every step).
+// After the first quarter a stage has been read and its buffer takes the loads of
+// NST steps ahead, spread over the other three quarters.  An odd number of steps is
+// made even by one of zeros.  Small tiles (four stages) hold two steps' operands:
+// one multiplies while the next is read, one barrier a step.
+//
+// KG > 1: KG such groups of four waves share the tile and split the steps between
+// them, each with stages of its own; their sums are joined through LDS in group
+// order.
+//
+// kRows: the rows of a tile are sorted pairs of one expert, gathered by the loads.
+// kSums: the summed rows of both operands are the pairs of one expert; their ids
+// pass through a small LDS ring, four steps at a time, ahead of the loads.
+template <int MI, int NI, int KG, int NST, Group G, bool TA, bool TB>
+__global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db) {
+  constexpr int BM = 32 * MI, BN = 32 * NI;
+  constexpr int XA = BM / 32, XB = BN / 32;        // 1 KB loads per wave and stage
+  static_assert(MI % 2 == 0 && NI % 2 == 0 && MI <= 8 && NI <= 8, "halves");
+  static_assert(!TA || (MI & (MI - 1)) == 0, "lanes of a row");
+  static_assert(!TB || (NI & (NI - 1)) == 0, "lanes of a row");
+  static_assert(NST >= 2 && NST <= 4, "stages");
+  static_assert(G == kSums ? TA && TB : true, "pairs run across both operands");
+  constexpr int SA = BM * 128, SB = BN * 128;
+  constexpr bool S3 = NST > 2, S4 = NST > 3;
+  // each stage an object of its own: the compiler then knows which loads an
+  // operand read has to wait for
+  __shared__ __attribute__((aligned(16))) uint8_t as0_[KG][SA], as1_[KG][SA];
+  __shared__ __attribute__((aligned(16))) uint8_t bs0_[KG][SB], bs1_[KG][SB];
+  __shared__ __attribute__((aligned(16))) uint8_t as2_[KG][S3 ? SA : 16], as3_[KG][S4 ? SA : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t bs2_[KG][S3 ? SB : 16], bs3_[KG][S4 ? SB : 16];
+  __shared__ __attribute__((aligned(16))) int32_t ring_[KG][2][G == kSums ? 256 : 4];
+
+  const int lane = threadIdx.x & 63;
+  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int r16 = lane & 15, h = lane >> 4;
+  uint8_t* const as0 = as0_[kg];
+  uint8_t* const as1 = as1_[kg];
+  uint8_t* const as2 = as2_[kg];
+  uint8_t* const as3 = as3_[kg];
+  uint8_t* const bs0 = bs0_[kg];
+  uint8_t* const bs1 = bs1_[kg];
+  uint8_t* const bs2 = bs2_[kg];
+  uint8_t* const bs3 = bs3_[kg];
+  auto& ring = ring_[kg];
+
+  // tile order: XCD x (workgroups round-robin over 8) walks a contiguous range
+  // of tiles in groups of 8 row blocks, which share operands in its L2; an
+  // expert's tiles of a weight gradient are spread over all XCDs, since hot
+  // experts would keep one busy
+  int64_t cap = 0, M = j.M;
+  if constexpr (G != kDense) cap = (j.g.P + (int64_t)j.g.E * (j.g.B - 1) + j.g.B - 1) / j.g.B * j.g.B;
+  if constexpr (G == kRows) M = min(M, min(cap, (int64_t)j.g.ntpp[0]));
+  const int64_t mt = (M + BM - 1) / BM, nt = (j.N + BN - 1) / BN, tiles = mt * nt;
+  const int64_t per = (tiles + 7) / 8;
+  int64_t at = blockIdx.x / 8, e = 0, chunk = blockIdx.x % 8;
+  if constexpr (G == kSums) {
+    e = at / per;
+    at -= e * per;
+    chunk = (chunk + 8 - e * tiles % 8) % 8;       // few tiles: another XCD for the next expert
+  }
+  const int64_t t = chunk * per + at;
+  if (t >= tiles || at >= per) return;
+  const int64_t band = t / (8 * nt), in_band = t - band * 8 * nt;
+  const int gm = (int)min((int64_t)8, mt - band * 8);
+  const int64_t m0 = (band * 8 + in_band % gm) * BM, n0 = in_band / gm * BN;
+
+  int sum = (int)j.K;                              // length of the sum
+  const int32_t* ids = j.g.sorted_ids;
+  const uint16_t* A = j.A;
+  const uint16_t* B = (const uint16_t*)j.B.p;
+  uint16_t* C = j.C;
+  if constexpr (G == kRows) {
+    e = j.g.expert_ids[m0 / j.g.B];
+    if (e < 0 || e >= j.g.E || (uint32_t)ids[m0] >= (uint32_t)j.g.P) return;
+    B += e * j.N * j.K;
+  }
+  if constexpr (G == kSums) {
+    const Segment seg = segment(j.g, cap, (int)e);
+    ids += seg.first;
+    sum = seg.count;
+    C += e * M * j.N;
+  }
+  const int steps = (sum + 63) / 64;
+  // this group's steps, a multiple of the stages for every group (those past
+  // its own part of the sum are zeros)
+  constexpr int ROUND = NST == 3 ? 2 : NST;
+  const int share = ((steps + KG - 1) / KG + ROUND - 1) / ROUND * ROUND;
+  const int first = kg * share, last = first + share;
+  const int k_end = min(sum, last * 64);
+
+  const int64_t lda = TA ? M : j.K, ldb = TB ? j.N : j.K;     // elements of a row in memory
+  const int64_t rows_a = TA ? (G == kSums ? j.g.P / (int)da.d : sum)
+                            : (G == kRows ? j.g.P / (int)da.d : min((int64_t)BM, M - m0));
+  const int64_t rows_b = TB ? (G == kSums ? j.g.P / (int)db.d : sum) : min((int64_t)BN, j.N - n0);
+  // from the tile's first column (TA, TB) or row on
+  const __amdgpu_buffer_rsrc_t ar =
+      rsrc(A + (TA ? m0 : (G == kRows ? 0 : m0 * lda)), (rows_a * lda - (TA ? m0 : 0)) * 2);
+  const __amdgpu_buffer_rsrc_t br = rsrc(B + (TB ? n0 : n0 * ldb), (rows_b * ldb - (TB ? n0 : 0)) * 2);
+  const __amdgpu_buffer_rsrc_t ir = rsrc(ids, G == kSums ? (int64_t)sum * 4 : 0);
+
+  // Load I of a stage.  Rows along the sum: it fills rows 8 I .. 8 I + 7, lane l
+  // slot l % 8 of row l / 8, which holds piece (l % 8) ^ ((row / 2) % 8).
+  // Across: rows of RB bytes, lane l slot l % LR of row l / LR.
+  constexpr int LRA = BM / 8, LRB = BN / 8;
+  auto piece = [&](int I) { return (lane & 7) ^ ((4 * I + (lane >> 4)) & 7); };
+  auto trow = [&](int I, int LR) { return I * (64 / LR) + lane / LR; };
+  auto tcol = [&](int slot, int swz) { return 8 * (((slot >> 1) ^ swz) << 1 | (slot & 1)); };
+  // byte offset of the lane's 16 bytes at step 0; of its column alone (kSums); past the end: kOOB
+  uint32_t aoff[XA], boff[XB];
+#pragma unroll
+  for (int i = 0; i < XA; ++i) {
+    const int I = wave * XA + i;
+    if constexpr (TA) {
+      const int row = trow(I, LRA), col = tcol(lane % LRA, tr_swizzle<2 * BM>(row));
+      aoff[i] = m0 + col < M ? (uint32_t)((G == kSums ? 0 : row * lda) + col) * 2u : kOOB;
+    } else {
+      const int r = 8 * I + (lane >> 3);
+      int64_t row = r < rows_a ? r : -1;
+      if constexpr (G == kRows) {
+        const uint32_t f = (uint32_t)ids[m0 + r];
+        row = f < (uint32_t)j.g.P ? (int64_t)div_by(f, da) : -1;
+      }
+      aoff[i] = row >= 0 ? (uint32_t)(row * lda + 8 * piece(I)) * 2u : kOOB;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < XB; ++i) {
+    const int I = wave * XB + i;
+    if constexpr (TB) {
+      const int row = trow(I, LRB), col = tcol(lane % LRB, tr_swizzle<2 * BN>(row));
+      boff[i] = n0 + col < j.N ? (uint32_t)((G == kSums ? 0 : row * ldb) + col) * 2u : kOOB;
+    } else {
+      const int r = 8 * I + (lane >> 3);
+      boff[i] = r < rows_b ? (uint32_t)(r * ldb + 8 * piece(I)) * 2u : kOOB;
+    }
+  }
+  // kSums: byte offsets of the rows that the next loads take
+  uint32_t arow[G == kSums ? XA : 1], brow[G == kSums ? XB : 1];
+  auto next_rows = [&](int step) __attribute__((always_inline)) {
+    if constexpr (G == kSums) {
+      const int32_t* q = ring[(step >> 2) & 1] + (step & 3) * 64;
+      const int left = k_end - step * 64;
+#pragma unroll
+      for (int i = 0; i < XA; ++i) {
+        const int r = trow(wave * XA + i, LRA);
+        const uint32_t f = (uint32_t)q[r];
+        const bool ok = r < left && f < (uint32_t)j.g.P;
+        arow[i] = ok ? div_by(f, da) * (uint32_t)lda * 2u : kOOB;
+        if constexpr (XA == XB) brow[i] = ok ? div_by(f, db) * (uint32_t)ldb * 2u : kOOB;
+      }
+      if constexpr (XA != XB) {
+#pragma unroll
+        for (int i = 0; i < XB; ++i) {
+          const int r = trow(wave * XB + i, LRB);
+          const uint32_t f = (uint32_t)q[r];
+          brow[i] = r < left && f < (uint32_t)j.g.P ? div_by(f, db) * (uint32_t)ldb * 2u : kOOB;
+        }
+      }
+    }
+  };
+  // load i of a wave's XA + XB of a stage
+  auto load_one = [&](int i, int step, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
+    const int k0 = step * 64, left = k_end - k0;   // what lies past the end reads zero
+    if (i < XA) {
+      const int I = wave * XA + i;
+      if constexpr (G == kSums) {
+        load_lds16(ar, sa + I * 1024, aoff[i] != kOOB ? arow[i] + aoff[i] : kOOB, 0);
+      } else if constexpr (TA) {
+        load_lds16(ar, sa + I * 1024, trow(I, LRA) < left ? aoff[i] : kOOB, (uint32_t)k0 * (uint32_t)lda * 2u);
+      } else {
+        load_lds16(ar, sa + I * 1024, 8 * piece(I) < left ? aoff[i] : kOOB, (uint32_t)k0 * 2u);
+      }
+    } else {
+      const int b = i - XA, I = wave * XB + b;
+      if constexpr (G == kSums) {
+        load_lds16(br, sb + I * 1024, boff[b] != kOOB ? brow[b] + boff[b] : kOOB, 0);
+      } else if constexpr (TB) {
+        load_lds16(br, sb + I * 1024, trow(I, LRB) < left ? boff[b] : kOOB, (uint32_t)k0 * (uint32_t)ldb * 2u);
+      } else {
+        load_lds16(br, sb + I * 1024, 8 * piece(I) < left ? boff[b] : kOOB, (uint32_t)k0 * 2u);
+      }
+    }
+  };
+  // the pairs of four steps into the ring, a quarter by each wave; ids past the
+  // segment read 0 and are not used
+  constexpr int EX = G == kSums ? 1 : 0;
+  auto load_ids = [&](int quad) __attribute__((always_inline)) {
+    if constexpr (G == kSums)
+      load_lds4(ir, ring[quad & 1] + 64 * wave, (uint32_t)(quad * 256 + 64 * wave + lane) * 4u);
+  };
+  // operand tile i of a wave's rows
+  const int arow0 = wm * 16 * MI, brow0 = wn * 16 * NI;
+  const int swz = 16 * (h ^ (r16 >> 1));
+  const int at_a = TA ? (8 * h + (r16 >> 2)) * 2 * BM + (r16 & 3) * 8 : (arow0 + r16) * 128 + swz;
+  const int at_b = TB ? (8 * h + (r16 >> 2)) * 2 * BN + (r16 & 3) * 8 : (brow0 + r16) * 128 + swz;
+  const int swz_a = 32 * tr_swizzle<2 * BM>(8 * h + (r16 >> 2)), swz_b = 32 * tr_swizzle<2 * BN>(8 * h + (r16 >> 2));
+  auto read_across = [&](const uint8_t* s, int RB) __attribute__((always_inline)) {
+    const u32x2 a = read_tr(s), b = read_tr(s + 4 * RB), c = read_tr(s + 32 * RB), d = read_tr(s + 36 * RB);
+    return Operand{u32x4{a.x, a.y, b.x, b.y}, u32x4{c.x, c.y, d.x, d.y}};
+  };
+  auto read_a = [&](const uint8_t* s, int i) __attribute__((always_inline)) {
+    if constexpr (TA) return read_across(s + at_a + ((arow0 * 2 + 32 * i) ^ swz_a), 2 * BM);
+    return Operand{*(const u32x4*)(s + at_a + 2048 * i), *(const u32x4*)(s + (at_a ^ 64) + 2048 * i)};
+  };
+  auto read_b = [&](const uint8_t* s, int i) __attribute__((always_inline)) {
+    if constexpr (TB) return read_across(s + at_b + ((brow0 * 2 + 32 * i) ^ swz_b), 2 * BN);
+    return Operand{*(const u32x4*)(s + at_b + 2048 * i), *(const u32x4*)(s + (at_b ^ 64) + 2048 * i)};
+  };
+  constexpr int RA = TA ? 4 : 2, RBN = TB ? 4 : 2;   // LDS reads of an operand tile
+
+  // a zero that the compiler does not see as constant: it would split loop
+  // variables that start at one into single registers
+  f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  asm("" : "+v"(zero));
+  f32x4 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int n = 0; n < NI; ++n) acc[i][n] = zero;
+  // small tiles hold two steps' operands (WHOLE), large ones halves
+  constexpr bool WHOLE = MI + NI <= 8;
+  static_assert(WHOLE == (NST == 4), "stages of the two schedules");
+  static_assert(NST != 3 || KG == 1, "three stages: any even number of steps");
+  constexpr int HI = WHOLE ? MI : MI / 2, HJ = WHOLE ? NI : NI / 2;
+  Operand x[2][HI], w[2][HJ];
+  auto fence = [] __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto multiply = [&](f32x4& d, const Operand& b, const Operand& a) __attribute__((always_inline)) {
+    d = mfma16(b.lo, a.lo, d);
+    d = mfma16(b.hi, a.hi, d);
+  };
+
+  // one quarter: rows hx of A, hw of B (in register set set); read_one(i) reads
+  // operand tile i for a later quarter (nr LDS reads in all), load(i) is load i
+  auto quarter = [&](auto HX, auto HW, int set, auto read_one, int reads, int nr, auto load, int loads)
+      __attribute__((always_inline)) {
+    constexpr int hx = decltype(HX)::value, hw = decltype(HW)::value;
+#pragma unroll
+    for (int i = 0; i < reads; ++i) read_one(i);
+#pragma unroll
+    for (int i = 0; i < loads; ++i) load(i);
+#pragma unroll
+    for (int q = 0; q < HI * HJ; ++q) {
+      // the operand that arrives last goes slowest
+      const int i = hx == 0 ? q % HI : q / HJ, n = hx == 0 ? q / HI : q % HJ;
+      multiply(acc[hx * HI + i][hw * HJ + n], w[set][n], x[hx][i]);
+    }
+#pragma unroll
+    for (int q = 0; q < 2 * HI * HJ; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // one MFMA
+      if (q < nr) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);        // one LDS read
+      if (q % 2 == 0 && q / 2 < loads) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // one load
+    }
+    fence();
+  };
+  using std::integral_constant;
+  constexpr integral_constant<int, 0> lo{};
+  constexpr integral_constant<int, 1> hi{};
+  auto none = [](int) {};
+
+  // small tiles, one step: its operands are in set S; the next one's are read
+  // into the other while they multiply
+  auto body_whole = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
+      __attribute__((always_inline)) {
+    constexpr int s = decltype(S)::value;
+    // the loads of the two steps after the next may be in flight
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NST - 2) * (XA + XB + EX)) : "memory");
+    __builtin_amdgcn_s_barrier();
+    fence();
+    load_ids((step + NST) / 4 + 1);
+#pragma unroll
+    for (int n = 0; n < NI; ++n) w[1 - s][n] = read_b(nb, n);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) x[1 - s][i] = read_a(na, i);
+    next_rows(step + NST);
+    fence();
+#pragma unroll
+    for (int i = 0; i < XA + XB; ++i) load_one(i, step + NST, sa, sb);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int n = 0; n < NI; ++n) multiply(acc[i][n], w[s][n], x[s][i]);
+#pragma unroll
+    for (int q = 0; q < 2 * MI * NI; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                    // one MFMA
+      if (q < XA + XB) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // one load
+    }
+    fence();
+  };
+
+  // one step on stage (sa, sb); (na, nb) is the next one's; the step's low
+  // half of B is in set S
+  auto body_halves = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
+      __attribute__((always_inline)) {
+    constexpr int s = decltype(S)::value;
+    constexpr int L2 = (XA + XB) * 3 / 8, L3 = (XA + XB) * 3 / 8;   // loads per quarter
+    // read the rest of this stage; when everyone has, its buffer is free
+    quarter(lo, lo, s,
+            [&](int i) {
+              if (i < HJ)
+                w[1 - s][i] = read_b(sb, HJ + i);
+              else
+                x[1][i - HJ] = read_a(sa, HI + i - HJ);
+            },
+            HJ + HI, HJ * RBN + HI * RA, none, 0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    fence();
+    load_ids((step + NST) / 4 + 1);
+    quarter(lo, hi, 1 - s, none, 0, 0, [&](int i) { load_one(i, step + NST, sa, sb); }, L2);
+    // the next stage has landed; the loads just issued, and with three stages
+    // those of the step before, may be in flight
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * (XA + XB + EX) + EX + L2) : "memory");
+    __builtin_amdgcn_s_barrier();
+    fence();
+    quarter(hi, hi, 1 - s, [&](int i) { x[0][i] = read_a(na, i); }, HI, HI * RA,
+            [&](int i) { load_one(L2 + i, step + NST, sa, sb); }, L3);
+    quarter(hi, lo, s, [&](int i) { w[1 - s][i] = read_b(nb, i); }, HJ, HJ * RBN,
+            [&](int i) { load_one(L2 + L3 + i, step + NST, sa, sb); }, XA + XB - L2 - L3);
+    next_rows(step + 1 + NST);
+    fence();
+  };
+
+  if (G != kSums || sum > 0) {
+    // the ids of the first two quads, then the first stages
+    if constexpr (G == kSums) {
+      load_ids(first / 4);
+      load_ids(first / 4 + 1);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      fence();
+    }
+    // (as many loads a stage as a step issues: the waits below count them)
+    auto load_stage = [&](int step, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
+      load_ids(first / 4 + 1);
+      next_rows(step);
+#pragma unroll
+      for (int i = 0; i < XA + XB; ++i) load_one(i, step, sa, sb);
+    };
+    load_stage(first, as0, bs0);
+    load_stage(first + 1, as1, bs1);
+    if constexpr (S3) load_stage(first + 2, as2, bs2);
+    if constexpr (S4) load_stage(first + 3, as3, bs3);
+    next_rows(first + NST);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 1) * (XA + XB + EX)) : "memory");
+    __builtin_amdgcn_s_barrier();
+    fence();
+#pragma unroll
+    for (int i = 0; i < HI; ++i) x[0][i] = read_a(as0, i);
+#pragma unroll
+    for (int n = 0; n < HJ; ++n) w[0][n] = read_b(bs0, n);
+    fence();
+    for (int step = first; step < last; step += NST == 3 ? 6 : NST) {
+      if constexpr (NST == 3) {
+        body_halves(lo, step, as0, bs0, as1, bs1);
+        body_halves(hi, step + 1, as1, bs1, as2, bs2);
+        if (step + 2 >= last) break;
+        body_halves(lo, step + 2, as2, bs2, as0, bs0);
+        body_halves(hi, step + 3, as0, bs0, as1, bs1);
+        if (step + 4 >= last) break;
+        body_halves(lo, step + 4, as1, bs1, as2, bs2);
+        body_halves(hi, step + 5, as2, bs2, as0, bs0);
+      } else if constexpr (WHOLE) {
+        body_whole(lo, step, as0, bs0, as1, bs1);
+        body_whole(hi, step + 1, as1, bs1, as2, bs2);
+        body_whole(lo, step + 2, as2, bs2, as3, bs3);
+        body_whole(hi, step + 3, as3, bs3, as0, bs0);
+      } else {
+        body_halves(lo, step, as0, bs0, as1, bs1);
+        body_halves(hi, step + 1, as1, bs1, as0, bs0);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // loads past the end drained
+  }
+
+  if constexpr (KG > 1) {
+    // one column of tiles per round through the stages that are done with
+    f32x4(*part)[4][MI][64] = (f32x4(*)[4][MI][64])as0_;
+#pragma unroll
+    for (int n = 0; n < NI; ++n) {
+      __syncthreads();
+      if (kg > 0) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) part[kg][wave][i][lane] = acc[i][n];
+      }
+      __syncthreads();
+      if (kg == 0) {
+#pragma unroll
+        for (int g = 1; g < KG; ++g)
+#pragma unroll
+          for (int i = 0; i < MI; ++i) acc[i][n] += part[g][wave][i][lane];
+      }
+    }
+    if (kg > 0) return;
+  }
+  const bool vec = (j.N & 3) == 0 && ((uintptr_t)C & 7) == 0;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    int64_t row = m0 + arow0 + r16 + 16 * i;
+    if constexpr (G == kRows) {
+      row = ids[row];
+      if ((uint32_t)row >= (uint32_t)j.g.P) continue;
+    } else if (row >= M) {
+      continue;
+    }
+#pragma unroll
+    for (int n = 0; n < NI; ++n)
+      store4(C + row * j.N, n0 + brow0 + 16 * n + 4 * h, j.N, acc[i][n], vec);
+  }
+}
+
 namespace {
 
 int64_t moe_cap(int64_t P, int32_t E, int32_t B) {
   return (P + (int64_t)E * (B - 1) + B - 1) / B * B;
 }
 
+Div divisor(int32_t d) { return {(uint32_t)d, (uint32_t)(((uint64_t)1 << 32) / (uint64_t)d + 1)}; }
+
+int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
+
 template <Group G, bool TA, bool TB, bool C8>
-hipError_t run_simple(const Job& j, int64_t tiles, hipStream_t st) {
+hipError_t run_simple(const Job& j, hipStream_t st) {
+  const int64_t tiles = tiles_of(j.M, j.N, 64, 64) * (G == kSums ? j.g.E : 1);
   hipLaunchKernelGGL((k_bf16_simple<G, TA, TB, C8>), dim3((unsigned)tiles), dim3(256), 0, st, j);
   return hipGetLastError();
 }
 
-int64_t simple_tiles(int64_t M, int64_t N) { return ((M + 63) / 64) * ((N + 63) / 64); }
+template <int MI, int NI, int KG, int NST, Group G, bool TA, bool TB>
+hipError_t run_tile(const Job& j, hipStream_t st) {
+  const int64_t per = (tiles_of(j.M, j.N, 32 * MI, 32 * NI) + 7) / 8;
+  hipLaunchKernelGGL((k_bf16_tile<MI, NI, KG, NST, G, TA, TB>),
+                     dim3((unsigned)(8 * per * (G == kSums ? j.g.E : 1))), dim3(256 * KG), 0, st, j,
+                     divisor(j.a_div), divisor(j.b_div));
+  return hipGetLastError();
+}
+
+// The tiles and what they cost: a round of one workgroup per CU takes step_us per
+// 64 of the sum and fixed_us besides (launch, first loads, stores).
+struct Kind {
+  int bm, bn, kg;
+  float step_us, fixed_us;
+};
+constexpr Kind kKinds[] = {
+    {64, 64, 2, 0.32f, 6.0f},   {64, 128, 1, 0.40f, 6.0f},  {64, 256, 1, 0.70f, 8.0f},
+    {128, 128, 1, 0.60f, 6.0f}, {128, 256, 1, 1.05f, 10.0f}, {256, 256, 1, 1.35f, 12.0f},
+};
+constexpr int kKindCount = 6;
+
+// The kind that is done first for `tiles` groups of rows and columns, among those
+// with bm rows (0: any).
+int pick(int64_t M, int64_t N, int64_t groups, int64_t sum, int bm) {
+  int best = -1;
+  float least = 0.0f;
+  const int64_t steps = std::max((sum + 63) / 64, (int64_t)1), cus = cu_count();
+  for (int i = 0; i < kKindCount; ++i) {
+    const Kind& t = kKinds[i];
+    if (bm != 0 && t.bm != bm) continue;
+    const int64_t rounds = (groups * tiles_of(M, N, t.bm, t.bn) + cus - 1) / cus;
+    const float us = (float)rounds * ((float)((steps + t.kg - 1) / t.kg) * t.step_us + t.fixed_us);
+    if (best < 0 || us < least) {
+      best = i;
+      least = us;
+    }
+  }
+  return best;
+}
+
+template <Group G, bool TA, bool TB>
+hipError_t run_kind(int kind, const Job& j, hipStream_t st) {
+  switch (kind) {
+    case 0: return run_tile<2, 2, 2, 4, G, TA, TB>(j, st);
+    case 1: return run_tile<2, 4, 1, 4, G, TA, TB>(j, st);
+    case 2: return run_tile<2, 8, 1, 3, G, TA, TB>(j, st);
+    case 3: return run_tile<4, 4, 1, 4, G, TA, TB>(j, st);
+    case 4: return run_tile<4, 8, 1, 3, G, TA, TB>(j, st);
+    default: return run_tile<8, 8, 1, 2, G, TA, TB>(j, st);
+  }
+}
+
+// The tiles address an operand's rows with 32-bit offsets; what they do not cover
+// goes through the simple kernel.
+bool fits(int64_t elems) { return elems * 2 < (int64_t)kOOB; }
 
 }  // namespace
 
+// (the simple tile is the smallest of all: most workgroups, of 256 threads; KG = 2
+// makes as many of 512)
 int64_t bf16_moe_threads(int64_t P, int32_t E, int64_t N, int64_t K, int32_t B) {
-  return simple_tiles(moe_cap(P, E, B), N) * 256;
+  return (tiles_of(moe_cap(P, E, B), N, 64, 64) + 8) * 512;
 }
-int64_t bf16_wgrad_threads(int32_t E, int64_t N, int64_t K) { return E * simple_tiles(N, K) * 256; }
+int64_t bf16_wgrad_threads(int32_t E, int64_t N, int64_t K) {
+  return E * (tiles_of(N, K, 64, 64) + 8) * 512;
+}
 
 hipError_t launch_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, uint16_t* Y,
                                 const Bf16Plan& plan, int64_t N, int64_t K, int32_t div,
                                 bool transposed, hipStream_t st) {
-  const int64_t cap = moe_cap(plan.P, plan.E, plan.B);
-  const Job j = {X, {W, nullptr}, Y, cap, N, K, plan, div, 1};
-  if (transposed) return run_simple<kRows, false, true, false>(j, simple_tiles(cap, N), st);
-  return run_simple<kRows, false, false, false>(j, simple_tiles(cap, N), st);
+  const Job j = {X, {W, nullptr}, Y, moe_cap(plan.P, plan.E, plan.B), N, K, plan, div, 1};
+  if (!fits(plan.P / div * K) || !fits(transposed ? N * K : std::min(N, (int64_t)256) * K))
+    return transposed ? run_simple<kRows, false, true, false>(j, st)
+                      : run_simple<kRows, false, false, false>(j, st);
+  const int bm = plan.B % 256 == 0 ? 256 : plan.B % 128 == 0 ? 128 : 64;
+  // rows that are not padding, an expert's last block half full
+  const int64_t rows = plan.P + std::min(plan.P, (int64_t)plan.E) * (bm / 2);
+  const int kind = pick(rows, N, 1, K, bm);
+  return transposed ? run_kind<kRows, false, true>(kind, j, st)
+                    : run_kind<kRows, false, false>(kind, j, st);
 }
 
 hipError_t launch_bf16_moe_wgrad(const uint16_t* dY, const Bf16Rows& X, uint16_t* dW,
                                  const Bf16Plan& plan, int64_t N, int64_t K, int32_t dy_div,
                                  int32_t x_div, hipStream_t st) {
   const Job j = {dY, X, dW, N, K, 0, plan, dy_div, x_div};
-  const int64_t tiles = plan.E * simple_tiles(N, K);
-  if (X.scales) return run_simple<kSums, true, true, true>(j, tiles, st);
-  return run_simple<kSums, true, true, false>(j, tiles, st);
+  if (X.scales) return run_simple<kSums, true, true, true>(j, st);
+  if (!fits(plan.P / dy_div * N) || !fits(plan.P / x_div * K))
+    return run_simple<kSums, true, true, false>(j, st);
+  return run_kind<kSums, true, true>(pick(N, K, plan.E, plan.P / plan.E, 0), j, st);
 }
 
 hipError_t launch_bf16_gemm_tn(const uint16_t* A, const Bf16Rows& B, uint16_t* C, int64_t M,
                                int64_t N, int64_t K, hipStream_t st) {
   const Job j = {A, B, C, N, K, M, {}, 1, 1};
-  if (B.scales) return run_simple<kDense, true, true, true>(j, simple_tiles(N, K), st);
-  return run_simple<kDense, true, true, false>(j, simple_tiles(N, K), st);
+  if (B.scales) return run_simple<kDense, true, true, true>(j, st);
+  if (!fits(M * N) || !fits(M * K)) return run_simple<kDense, true, true, false>(j, st);
+  return run_kind<kDense, true, true>(pick(N, K, 1, M, 0), j, st);
 }
 
 }  // namespace w4
