@@ -226,30 +226,42 @@ __device__ __forceinline__ u32x2 read_tr(const uint8_t* s) {
                  (__attribute__((address_space(3))) i16x4*)(__attribute__((address_space(3))) void*)s));
 }
 
-// Four consecutive outputs n .. n + 3 of a row; vec: whole and aligned.
-__device__ __forceinline__ void store4(uint16_t* row, int64_t n, int64_t N, f32x4 s, bool vec) {
-  if (n >= N) return;
-  const u32x2 o = {pk_bf16(s.x, s.y), pk_bf16(s.z, s.w)};
-  uint16_t* y = row + n;
-  if (vec) {
-    *(u32x2*)y = o;
-    return;
-  }
-  y[0] = (uint16_t)o.x;
-  if (n + 1 < N) y[1] = (uint16_t)(o.x >> 16);
-  if (n + 2 < N) y[2] = (uint16_t)o.y;
-  if (n + 3 < N) y[3] = (uint16_t)(o.y >> 16);
+// Outputs of two neighbouring tiles of 16 columns: lane (r16, h) gives columns
+// 4 h .. 4 h + 3 of row r16 of each and gets eight consecutive ones, of the first
+// tile in h = 0, 1 and of the second in h = 2, 3, so that a store covers 64 bytes of
+// a row instead of 32.
+__device__ __forceinline__ u32x4 join_tiles(f32x4 a, f32x4 b) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+  u2 x = {pk_bf16(a.x, a.y), pk_bf16(b.x, b.y)}, y = {pk_bf16(a.z, a.w), pk_bf16(b.z, b.w)};
+  x = __builtin_amdgcn_permlane32_swap(x.x, x.y, false, false);
+  y = __builtin_amdgcn_permlane32_swap(y.x, y.y, false, false);
+  x = __builtin_amdgcn_permlane16_swap(x.x, x.y, false, false);
+  y = __builtin_amdgcn_permlane16_swap(y.x, y.y, false, false);
+  return u32x4{x.x, y.x, x.y, y.y};
 }
 
-// f / d for f < 2^31, with m = floor(2^32 / d) + 1 (d > 1): the high product is the
-// quotient or one more.
+// Eight consecutive outputs n .. n + 7 of a row; vec: N is a multiple of 8, and the
+// address of 16 bytes.
+__device__ __forceinline__ void store8(uint16_t* row, int64_t n, int64_t N, u32x4 v, bool vec) {
+  if (n >= N) return;
+  if (vec) {
+    *(u32x4*)(row + n) = v;
+    return;
+  }
+  const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (n + i < N) row[n + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
+}
+
+// f / d for f < 2^31, with m = floor((2^32 - 1) / d): the high product is the
+// quotient or one less.
 struct Div {
   uint32_t d, m;
 };
 __device__ __forceinline__ uint32_t div_by(uint32_t f, Div v) {
-  if (v.d == 1) return f;
   const uint32_t q = __umulhi(f, v.m);
-  return q * v.d > f ? q - 1 : q;
+  return f - q * v.d >= v.d ? q + 1 : q;
 }
 
 // Swizzle of a row (of the summed dimension) in units of 32 bytes: the eight
@@ -300,7 +312,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   __shared__ __attribute__((aligned(16))) uint8_t bs0_[KG][SB], bs1_[KG][SB];
   __shared__ __attribute__((aligned(16))) uint8_t as2_[KG][S3 ? SA : 16], as3_[KG][S4 ? SA : 16];
   __shared__ __attribute__((aligned(16))) uint8_t bs2_[KG][S3 ? SB : 16], bs3_[KG][S4 ? SB : 16];
-  __shared__ __attribute__((aligned(16))) int32_t ring_[KG][2][G == kSums ? 256 : 4];
+  __shared__ __attribute__((aligned(16))) u32x2 rows_[KG][4][2][G == kSums ? 64 : 1];
 
   const int lane = threadIdx.x & 63;
   const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
@@ -315,7 +327,6 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   uint8_t* const bs1 = bs1_[kg];
   uint8_t* const bs2 = bs2_[kg];
   uint8_t* const bs3 = bs3_[kg];
-  auto& ring = ring_[kg];
 
   // tile order: XCD x (workgroups round-robin over 8) walks a contiguous range
   // of tiles in groups of 8 row blocks, which share operands in its L2; an
@@ -408,27 +419,28 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
       boff[i] = r < rows_b ? (uint32_t)(r * ldb + 8 * piece(I)) * 2u : kOOB;
     }
   }
-  // kSums: byte offsets of the rows that the next loads take
+  // kSums: lane l holds the pair of row l of a coming step (loaded a step before it
+  // is needed), turns it into the byte offsets of that row in A and B (kOOB: none),
+  // and the loads' lanes take theirs out of a corner of LDS that is the wave's own
   uint32_t arow[G == kSums ? XA : 1], brow[G == kSums ? XB : 1];
-  auto next_rows = [&](int step) __attribute__((always_inline)) {
+  auto load_id = [&](int step) __attribute__((always_inline)) {
+    return G == kSums ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ir, (step * 64 + lane) * 4, 0, 0) : 0u;
+  };
+  auto next_rows = [&](int step, uint32_t f) __attribute__((always_inline)) {
     if constexpr (G == kSums) {
-      const int32_t* q = ring[(step >> 2) & 1] + (step & 3) * 64;
-      const int left = k_end - step * 64;
+      u32x2* q = rows_[kg][wave][step & 1];
+      const bool ok = step * 64 + lane < k_end && f < (uint32_t)j.g.P;
+      q[lane] = ok ? u32x2{div_by(f, da) * (uint32_t)lda * 2u, div_by(f, db) * (uint32_t)ldb * 2u}
+                   : u32x2{kOOB, kOOB};
 #pragma unroll
       for (int i = 0; i < XA; ++i) {
-        const int r = trow(wave * XA + i, LRA);
-        const uint32_t f = (uint32_t)q[r];
-        const bool ok = r < left && f < (uint32_t)j.g.P;
-        arow[i] = ok ? div_by(f, da) * (uint32_t)lda * 2u : kOOB;
-        if constexpr (XA == XB) brow[i] = ok ? div_by(f, db) * (uint32_t)ldb * 2u : kOOB;
+        const u32x2 o = q[trow(wave * XA + i, LRA)];
+        arow[i] = o.x;
+        if constexpr (XA == XB) brow[i] = o.y;
       }
       if constexpr (XA != XB) {
 #pragma unroll
-        for (int i = 0; i < XB; ++i) {
-          const int r = trow(wave * XB + i, LRB);
-          const uint32_t f = (uint32_t)q[r];
-          brow[i] = r < left && f < (uint32_t)j.g.P ? div_by(f, db) * (uint32_t)ldb * 2u : kOOB;
-        }
+        for (int i = 0; i < XB; ++i) brow[i] = q[trow(wave * XB + i, LRB)].y;
       }
     }
   };
@@ -455,13 +467,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
       }
     }
   };
-  // the pairs of four steps into the ring, a quarter by each wave; ids past the
-  // segment read 0 and are not used
-  constexpr int EX = G == kSums ? 1 : 0;
-  auto load_ids = [&](int quad) __attribute__((always_inline)) {
-    if constexpr (G == kSums)
-      load_lds4(ir, ring[quad & 1] + 64 * wave, (uint32_t)(quad * 256 + 64 * wave + lane) * 4u);
-  };
+  constexpr int EX = G == kSums ? 1 : 0;           // a step's load of pairs
   // operand tile i of a wave's rows
   const int arow0 = wm * 16 * MI, brow0 = wn * 16 * NI;
   const int swz = 16 * (h ^ (r16 >> 1));
@@ -497,6 +503,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   static_assert(NST != 3 || KG == 1, "three stages: any even number of steps");
   constexpr int HI = WHOLE ? MI : MI / 2, HJ = WHOLE ? NI : NI / 2;
   Operand x[2][HI], w[2][HJ];
+  uint32_t id = 0;                                 // kSums: the pair that next_rows turns next
   auto fence = [] __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -508,13 +515,14 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
 
   // one quarter: rows hx of A, hw of B (in register set set); read_one(i) reads
   // operand tile i for a later quarter (nr LDS reads in all), load(i) is load i
-  auto quarter = [&](auto HX, auto HW, int set, auto read_one, int reads, int nr, auto load, int loads)
-      __attribute__((always_inline)) {
+  auto quarter = [&](auto HX, auto HW, int set, auto read_one, int reads, int nr, auto load, int loads,
+                     auto also) __attribute__((always_inline)) {
     constexpr int hx = decltype(HX)::value, hw = decltype(HW)::value;
 #pragma unroll
     for (int i = 0; i < reads; ++i) read_one(i);
 #pragma unroll
     for (int i = 0; i < loads; ++i) load(i);
+    also();
 #pragma unroll
     for (int q = 0; q < HI * HJ; ++q) {
       // the operand that arrives last goes slowest
@@ -533,6 +541,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   constexpr integral_constant<int, 0> lo{};
   constexpr integral_constant<int, 1> hi{};
   auto none = [](int) {};
+  auto nothing = [] {};
 
   // small tiles, one step: its operands are in set S; the next one's are read
   // into the other while they multiply
@@ -540,15 +549,16 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
       __attribute__((always_inline)) {
     constexpr int s = decltype(S)::value;
     // the loads of the two steps after the next may be in flight
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NST - 2) * (XA + XB + EX)) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NST - 2) * (XA + XB)) : "memory");
     __builtin_amdgcn_s_barrier();
     fence();
-    load_ids((step + NST) / 4 + 1);
+    const uint32_t coming = load_id(step + 1 + NST);
 #pragma unroll
     for (int n = 0; n < NI; ++n) w[1 - s][n] = read_b(nb, n);
 #pragma unroll
     for (int i = 0; i < MI; ++i) x[1 - s][i] = read_a(na, i);
-    next_rows(step + NST);
+    next_rows(step + NST, id);
+    id = coming;
     fence();
 #pragma unroll
     for (int i = 0; i < XA + XB; ++i) load_one(i, step + NST, sa, sb);
@@ -578,47 +588,42 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
               else
                 x[1][i - HJ] = read_a(sa, HI + i - HJ);
             },
-            HJ + HI, HJ * RBN + HI * RA, none, 0);
+            HJ + HI, HJ * RBN + HI * RA, none, 0, nothing);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     fence();
-    load_ids((step + NST) / 4 + 1);
-    quarter(lo, hi, 1 - s, none, 0, 0, [&](int i) { load_one(i, step + NST, sa, sb); }, L2);
+    const uint32_t coming = load_id(step + 2 + NST);
+    quarter(lo, hi, 1 - s, none, 0, 0, [&](int i) { load_one(i, step + NST, sa, sb); }, L2, nothing);
     // the next stage has landed; the loads just issued, and with three stages
     // those of the step before, may be in flight
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * (XA + XB + EX) + EX + L2) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * (XA + XB) + EX + L2) : "memory");
     __builtin_amdgcn_s_barrier();
     fence();
     quarter(hi, hi, 1 - s, [&](int i) { x[0][i] = read_a(na, i); }, HI, HI * RA,
-            [&](int i) { load_one(L2 + i, step + NST, sa, sb); }, L3);
+            [&](int i) { load_one(L2 + i, step + NST, sa, sb); }, L3, nothing);
     quarter(hi, lo, s, [&](int i) { w[1 - s][i] = read_b(nb, i); }, HJ, HJ * RBN,
-            [&](int i) { load_one(L2 + L3 + i, step + NST, sa, sb); }, XA + XB - L2 - L3);
-    next_rows(step + 1 + NST);
-    fence();
+            [&](int i) { load_one(L2 + L3 + i, step + NST, sa, sb); }, XA + XB - L2 - L3,
+            [&] { next_rows(step + 1 + NST, id); });
+    id = coming;
   };
 
   if (G != kSums || sum > 0) {
-    // the ids of the first two quads, then the first stages
-    if constexpr (G == kSums) {
-      load_ids(first / 4);
-      load_ids(first / 4 + 1);
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      fence();
-    }
-    // (as many loads a stage as a step issues: the waits below count them)
-    auto load_stage = [&](int step, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
-      load_ids(first / 4 + 1);
-      next_rows(step);
+    // the pairs of the first stages together, then the stages
+    uint32_t f[NST + 2];
 #pragma unroll
-      for (int i = 0; i < XA + XB; ++i) load_one(i, step, sa, sb);
+    for (int i = 0; i < NST + 2; ++i) f[i] = load_id(first + i);
+    auto load_stage = [&](int i, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
+      next_rows(first + i, f[i]);
+#pragma unroll
+      for (int n = 0; n < XA + XB; ++n) load_one(n, first + i, sa, sb);
     };
-    load_stage(first, as0, bs0);
-    load_stage(first + 1, as1, bs1);
-    if constexpr (S3) load_stage(first + 2, as2, bs2);
-    if constexpr (S4) load_stage(first + 3, as3, bs3);
-    next_rows(first + NST);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 1) * (XA + XB + EX)) : "memory");
+    load_stage(0, as0, bs0);
+    load_stage(1, as1, bs1);
+    if constexpr (S3) load_stage(2, as2, bs2);
+    if constexpr (S4) load_stage(3, as3, bs3);
+    if constexpr (!WHOLE) next_rows(first + NST, f[NST]);
+    id = f[WHOLE ? NST : NST + 1];
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 1) * (XA + XB)) : "memory");
     __builtin_amdgcn_s_barrier();
     fence();
 #pragma unroll
@@ -669,19 +674,20 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     }
     if (kg > 0) return;
   }
-  const bool vec = (j.N & 3) == 0 && ((uintptr_t)C & 7) == 0;
+  const bool vec = (j.N & 7) == 0 && ((uintptr_t)C & 15) == 0;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     int64_t row = m0 + arow0 + r16 + 16 * i;
+    bool ok = row < M;
     if constexpr (G == kRows) {
       row = ids[row];
-      if ((uint32_t)row >= (uint32_t)j.g.P) continue;
-    } else if (row >= M) {
-      continue;
+      ok = (uint32_t)row < (uint32_t)j.g.P;
     }
 #pragma unroll
-    for (int n = 0; n < NI; ++n)
-      store4(C + row * j.N, n0 + brow0 + 16 * n + 4 * h, j.N, acc[i][n], vec);
+    for (int n = 0; n < NI; n += 2) {
+      const u32x4 v = join_tiles(acc[i][n], acc[i][n + 1]);
+      if (ok) store8(C + row * j.N, n0 + brow0 + 16 * n + 8 * h, j.N, v, vec);
+    }
   }
 }
 
@@ -691,7 +697,7 @@ int64_t moe_cap(int64_t P, int32_t E, int32_t B) {
   return (P + (int64_t)E * (B - 1) + B - 1) / B * B;
 }
 
-Div divisor(int32_t d) { return {(uint32_t)d, (uint32_t)(((uint64_t)1 << 32) / (uint64_t)d + 1)}; }
+Div divisor(int32_t d) { return {(uint32_t)d, 0xFFFFFFFFu / (uint32_t)d}; }
 
 int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
