@@ -61,6 +61,14 @@ __device__ __forceinline__ Segment segment(const Bf16Plan& g, int64_t cap, int e
   return {lo * g.B, last - lo * g.B + tail};
 }
 
+// The lower and the upper two of four e4m3 codes times a power of two, as bf16.
+__device__ __forceinline__ uint32_t cvt2(uint32_t codes, float s) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, false));
+}
+__device__ __forceinline__ uint32_t cvt2h(uint32_t codes, float s) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, true));
+}
+
 // Eight consecutive values of a row as bf16.
 template <bool C8>
 __device__ __forceinline__ u32x4 eight(const Bf16Rows& o, int64_t row, int64_t cols, int64_t c) {
@@ -69,12 +77,7 @@ __device__ __forceinline__ u32x4 eight(const Bf16Rows& o, int64_t row, int64_t c
   } else {
     const u32x2 q = *(const u32x2*)((const uint8_t*)o.p + row * cols + c);
     const float s = __uint_as_float((uint32_t)o.scales[row * w8_cols(cols) + (c >> 7)] << 23);
-    u32x4 r;
-    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.x, s, false));
-    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.x, s, true));
-    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.y, s, false));
-    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.y, s, true));
-    return r;
+    return u32x4{cvt2(q.x, s), cvt2h(q.x, s), cvt2(q.y, s), cvt2h(q.y, s)};
   }
 }
 
@@ -293,12 +296,19 @@ struct Operand {           // 16 rows x 64 of the sum: two MFMA operands
 // order.
 //
 // kRows: the rows of a tile are sorted pairs of one expert, gathered by the loads.
-// kSums: the summed rows of both operands are the pairs of one expert; their ids
-// pass through a small LDS ring, four steps at a time, ahead of the loads.
-template <int MI, int NI, int KG, int NST, Group G, bool TA, bool TB>
+// kSums: the summed rows of both operands are the pairs of one expert, which
+// are turned into byte offsets a step ahead of the loads.
+//
+// C8: B is a checkpoint.  Its codes come into registers, 16 of a row with their
+// scale a lane, become bf16 by v_cvt_scalef32_pk_bf16_fp8 (which applies the power of
+// two) and go into the stage as bf16 rows would, so that each element is converted
+// once a workgroup and memory sees half the bytes.
+template <int MI, int NI, int KG, int NST, Group G, bool TA, bool TB, bool C8 = false>
 __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db) {
   constexpr int BM = 32 * MI, BN = 32 * NI;
-  constexpr int XA = BM / 32, XB = BN / 32;        // 1 KB loads per wave and stage
+  constexpr int XA = BM / 32, XB = C8 ? 0 : BN / 32;   // 1 KB loads per wave and stage
+  constexpr int XC = C8 ? BN / 64 : 0;             // 16 codes each, and their scales
+  static_assert(!C8 || (TA && TB), "rows across the sum");
   static_assert(MI % 2 == 0 && NI % 2 == 0 && MI <= 8 && NI <= 8, "halves");
   static_assert(!TA || (MI & (MI - 1)) == 0, "lanes of a row");
   static_assert(!TB || (NI & (NI - 1)) == 0, "lanes of a row");
@@ -312,7 +322,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   __shared__ __attribute__((aligned(16))) uint8_t bs0_[KG][SB], bs1_[KG][SB];
   __shared__ __attribute__((aligned(16))) uint8_t as2_[KG][S3 ? SA : 16], as3_[KG][S4 ? SA : 16];
   __shared__ __attribute__((aligned(16))) uint8_t bs2_[KG][S3 ? SB : 16], bs3_[KG][S4 ? SB : 16];
-  __shared__ __attribute__((aligned(16))) u32x2 rows_[KG][4][2][G == kSums ? 64 : 1];
+  __shared__ __attribute__((aligned(16))) u32x4 rows_[KG][4][2][G == kSums ? 64 : 1];
 
   const int lane = threadIdx.x & 63;
   const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
@@ -352,12 +362,13 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   int sum = (int)j.K;                              // length of the sum
   const int32_t* ids = j.g.sorted_ids;
   const uint16_t* A = j.A;
-  const uint16_t* B = (const uint16_t*)j.B.p;
+  const uint8_t* B = (const uint8_t*)j.B.p;
+  constexpr int BB = C8 ? 1 : 2;                   // bytes of an element of B
   uint16_t* C = j.C;
   if constexpr (G == kRows) {
     e = j.g.expert_ids[m0 / j.g.B];
     if (e < 0 || e >= j.g.E || (uint32_t)ids[m0] >= (uint32_t)j.g.P) return;
-    B += e * j.N * j.K;
+    B += e * j.N * j.K * BB;
   }
   if constexpr (G == kSums) {
     const Segment seg = segment(j.g, cap, (int)e);
@@ -380,7 +391,11 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   // from the tile's first column (TA, TB) or row on
   const __amdgpu_buffer_rsrc_t ar =
       rsrc(A + (TA ? m0 : (G == kRows ? 0 : m0 * lda)), (rows_a * lda - (TA ? m0 : 0)) * 2);
-  const __amdgpu_buffer_rsrc_t br = rsrc(B + (TB ? n0 : n0 * ldb), (rows_b * ldb - (TB ? n0 : 0)) * 2);
+  const __amdgpu_buffer_rsrc_t br =
+      rsrc(B + (TB ? n0 : n0 * ldb) * BB, (rows_b * ldb - (TB ? n0 : 0)) * BB);
+  const int64_t lds = w8_cols(j.N);                // C8: scales of a row
+  const __amdgpu_buffer_rsrc_t sr =
+      rsrc(C8 ? j.B.scales + (n0 >> 7) : nullptr, C8 ? rows_b * lds - (n0 >> 7) : 0);
   const __amdgpu_buffer_rsrc_t ir = rsrc(ids, G == kSums ? (int64_t)sum * 4 : 0);
 
   // Load I of a stage.  Rows along the sum: it fills rows 8 I .. 8 I + 7, lane l
@@ -390,8 +405,10 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   auto piece = [&](int I) { return (lane & 7) ^ ((4 * I + (lane >> 4)) & 7); };
   auto trow = [&](int I, int LR) { return I * (64 / LR) + lane / LR; };
   auto tcol = [&](int slot, int swz) { return 8 * (((slot >> 1) ^ swz) << 1 | (slot & 1)); };
+  constexpr int CPR = BN / 16;                     // codes: lanes of a row
+  auto crow = [&](int i) { return (i * 256 + wave * 64 + lane) / CPR; };
   // byte offset of the lane's 16 bytes at step 0; of its column alone (kSums); past the end: kOOB
-  uint32_t aoff[XA], boff[XB];
+  uint32_t aoff[XA], boff[C8 ? 1 : XB];
 #pragma unroll
   for (int i = 0; i < XA; ++i) {
     const int I = wave * XA + i;
@@ -409,7 +426,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     }
   }
 #pragma unroll
-  for (int i = 0; i < XB; ++i) {
+  for (int i = 0; i < XB; ++i) {                   // (none of codes)
     const int I = wave * XB + i;
     if constexpr (TB) {
       const int row = trow(I, LRB), col = tcol(lane % LRB, tr_swizzle<2 * BN>(row));
@@ -422,25 +439,71 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   // kSums: lane l holds the pair of row l of a coming step (loaded a step before it
   // is needed), turns it into the byte offsets of that row in A and B (kOOB: none),
   // and the loads' lanes take theirs out of a corner of LDS that is the wave's own
-  uint32_t arow[G == kSums ? XA : 1], brow[G == kSums ? XB : 1];
+  uint32_t arow[G == kSums ? XA : 1], brow[G == kSums ? (C8 ? XC : XB) : 1], srow[C8 ? XC : 1];
   auto load_id = [&](int step) __attribute__((always_inline)) {
     return G == kSums ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ir, (step * 64 + lane) * 4, 0, 0) : 0u;
   };
   auto next_rows = [&](int step, uint32_t f) __attribute__((always_inline)) {
     if constexpr (G == kSums) {
-      u32x2* q = rows_[kg][wave][step & 1];
+      u32x4* q = rows_[kg][wave][step & 1];
       const bool ok = step * 64 + lane < k_end && f < (uint32_t)j.g.P;
-      q[lane] = ok ? u32x2{div_by(f, da) * (uint32_t)lda * 2u, div_by(f, db) * (uint32_t)ldb * 2u}
-                   : u32x2{kOOB, kOOB};
+      const uint32_t fb = div_by(f, db);
+      q[lane] = ok ? u32x4{div_by(f, da) * (uint32_t)lda * 2u, fb * (uint32_t)ldb * BB, C8 ? fb * (uint32_t)lds : 0u, 0u}
+                   : u32x4{kOOB, kOOB, kOOB, 0u};
 #pragma unroll
       for (int i = 0; i < XA; ++i) {
-        const u32x2 o = q[trow(wave * XA + i, LRA)];
+        const u32x2 o = *(const u32x2*)&q[trow(wave * XA + i, LRA)];
         arow[i] = o.x;
         if constexpr (XA == XB) brow[i] = o.y;
       }
-      if constexpr (XA != XB) {
+      if constexpr (XA != XB && !C8) {
 #pragma unroll
         for (int i = 0; i < XB; ++i) brow[i] = q[trow(wave * XB + i, LRB)].y;
+      }
+      if constexpr (C8) {
+#pragma unroll
+        for (int i = 0; i < XC; ++i) {
+          const u32x4 o = q[crow(i)];
+          brow[i] = o.y;
+          srow[i] = o.z;
+        }
+      }
+    }
+  };
+  // load i of the codes: 16 of row crow(i), from the lane's column on
+  u32x4 code[C8 ? (NST == 4 ? 2 : 1) : 1][C8 ? XC : 1];
+  uint32_t scale[C8 ? (NST == 4 ? 2 : 1) : 1][C8 ? XC : 1];
+  const int ccol = 16 * (lane % CPR);
+  const bool cok = n0 + ccol < j.N;
+  const uint32_t cs = (uint32_t)(((n0 + ccol) >> 7) - (n0 >> 7));
+  auto load_codes = [&](int set, int step) __attribute__((always_inline)) {
+    if constexpr (C8) {
+#pragma unroll
+      for (int i = 0; i < XC; ++i) {
+        if constexpr (G == kSums) {
+          code[set][i] = __builtin_amdgcn_raw_buffer_load_b128(br, cok ? (int)(brow[i] + ccol) : (int)kOOB, 0, 0);
+          scale[set][i] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(srow[i] + cs), 0, 0);
+        } else {
+          const int k0 = step * 64;
+          const bool ok = cok && crow(i) < k_end - k0;
+          code[set][i] = __builtin_amdgcn_raw_buffer_load_b128(
+              br, ok ? (int)(crow(i) * (uint32_t)ldb + ccol) : (int)kOOB, (int)((uint32_t)k0 * (uint32_t)ldb), 0);
+          scale[set][i] = __builtin_amdgcn_raw_buffer_load_b8(
+              sr, ok ? (int)(crow(i) * (uint32_t)lds + cs) : (int)kOOB, (int)((uint32_t)k0 * (uint32_t)lds), 0);
+        }
+      }
+    }
+  };
+  auto put_codes = [&](int set, uint8_t* sb) __attribute__((always_inline)) {
+    if constexpr (C8) {
+#pragma unroll
+      for (int i = 0; i < XC; ++i) {
+        const int row = crow(i);
+        u32x4* d = (u32x4*)(sb + row * 2 * BN + ((2 * ccol) ^ (32 * tr_swizzle<2 * BN>(row))));
+        const float s = __uint_as_float(scale[set][i] << 23);
+        const u32x4 c = code[set][i];
+        d[0] = u32x4{cvt2(c.x, s), cvt2h(c.x, s), cvt2(c.y, s), cvt2h(c.y, s)};
+        d[1] = u32x4{cvt2(c.z, s), cvt2h(c.z, s), cvt2(c.w, s), cvt2h(c.w, s)};
       }
     }
   };
@@ -545,11 +608,13 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
 
   // small tiles, one step: its operands are in set S; the next one's are read
   // into the other while they multiply
-  auto body_whole = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
+  // (codes: two steps on their way in registers, then put into the stage tb of two
+  // steps ahead)
+  auto body_whole = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb, uint8_t* tb)
       __attribute__((always_inline)) {
     constexpr int s = decltype(S)::value;
     // the loads of the two steps after the next may be in flight
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NST - 2) * (XA + XB)) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NST - 2) * (XA + XB + 2 * XC)) : "memory");
     __builtin_amdgcn_s_barrier();
     fence();
     const uint32_t coming = load_id(step + 1 + NST);
@@ -560,6 +625,8 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     next_rows(step + NST, id);
     id = coming;
     fence();
+    put_codes(s, tb);
+    load_codes(s, step + NST);
 #pragma unroll
     for (int i = 0; i < XA + XB; ++i) load_one(i, step + NST, sa, sb);
 #pragma unroll
@@ -596,14 +663,20 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     quarter(lo, hi, 1 - s, none, 0, 0, [&](int i) { load_one(i, step + NST, sa, sb); }, L2, nothing);
     // the next stage has landed; the loads just issued, and with three stages
     // those of the step before, may be in flight
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * (XA + XB) + EX + L2) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * (XA + XB + 2 * XC) + EX + L2 + 2 * XC) : "memory");
     __builtin_amdgcn_s_barrier();
     fence();
     quarter(hi, hi, 1 - s, [&](int i) { x[0][i] = read_a(na, i); }, HI, HI * RA,
             [&](int i) { load_one(L2 + i, step + NST, sa, sb); }, L3, nothing);
     quarter(hi, lo, s, [&](int i) { w[1 - s][i] = read_b(nb, i); }, HJ, HJ * RBN,
             [&](int i) { load_one(L2 + L3 + i, step + NST, sa, sb); }, XA + XB - L2 - L3,
-            [&] { next_rows(step + 1 + NST, id); });
+            [&] {
+              put_codes(0, sb);
+              next_rows(step + 1 + NST, id);
+            });
+    // behind the fence: the wait above counts these as the step's last loads
+    load_codes(0, step + 1 + NST);
+    fence();
     id = coming;
   };
 
@@ -614,16 +687,23 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     for (int i = 0; i < NST + 2; ++i) f[i] = load_id(first + i);
     auto load_stage = [&](int i, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
       next_rows(first + i, f[i]);
+      load_codes(WHOLE ? i & 1 : 0, first + i);
 #pragma unroll
       for (int n = 0; n < XA + XB; ++n) load_one(n, first + i, sa, sb);
+      if (!WHOLE || i < 2) put_codes(WHOLE ? i & 1 : 0, sb);
     };
     load_stage(0, as0, bs0);
     load_stage(1, as1, bs1);
     if constexpr (S3) load_stage(2, as2, bs2);
     if constexpr (S4) load_stage(3, as3, bs3);
-    if constexpr (!WHOLE) next_rows(first + NST, f[NST]);
+    if constexpr (!WHOLE) {
+      next_rows(first + NST, f[NST]);
+      fence();
+      load_codes(0, first + NST);
+    }
     id = f[WHOLE ? NST : NST + 1];
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 1) * (XA + XB)) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C8 ? (WHOLE ? 0 : 2 * XC) : (NST - 1) * (XA + XB))
+                 : "memory");
     __builtin_amdgcn_s_barrier();
     fence();
 #pragma unroll
@@ -642,10 +722,10 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
         body_halves(lo, step + 4, as1, bs1, as2, bs2);
         body_halves(hi, step + 5, as2, bs2, as0, bs0);
       } else if constexpr (WHOLE) {
-        body_whole(lo, step, as0, bs0, as1, bs1);
-        body_whole(hi, step + 1, as1, bs1, as2, bs2);
-        body_whole(lo, step + 2, as2, bs2, as3, bs3);
-        body_whole(hi, step + 3, as3, bs3, as0, bs0);
+        body_whole(lo, step, as0, bs0, as1, bs1, bs2);
+        body_whole(hi, step + 1, as1, bs1, as2, bs2, bs3);
+        body_whole(lo, step + 2, as2, bs2, as3, bs3, bs0);
+        body_whole(hi, step + 3, as3, bs3, as0, bs0, bs1);
       } else {
         body_halves(lo, step, as0, bs0, as1, bs1);
         body_halves(hi, step + 1, as1, bs1, as0, bs0);
@@ -708,10 +788,10 @@ hipError_t run_simple(const Job& j, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int MI, int NI, int KG, int NST, Group G, bool TA, bool TB>
+template <int MI, int NI, int KG, int NST, Group G, bool TA, bool TB, bool C8>
 hipError_t run_tile(const Job& j, hipStream_t st) {
   const int64_t per = (tiles_of(j.M, j.N, 32 * MI, 32 * NI) + 7) / 8;
-  hipLaunchKernelGGL((k_bf16_tile<MI, NI, KG, NST, G, TA, TB>),
+  hipLaunchKernelGGL((k_bf16_tile<MI, NI, KG, NST, G, TA, TB, C8>),
                      dim3((unsigned)(8 * per * (G == kSums ? j.g.E : 1))), dim3(256 * KG), 0, st, j,
                      divisor(j.a_div), divisor(j.b_div));
   return hipGetLastError();
@@ -748,15 +828,15 @@ int pick(int64_t M, int64_t N, int64_t groups, int64_t sum, int bm) {
   return best;
 }
 
-template <Group G, bool TA, bool TB>
+template <Group G, bool TA, bool TB, bool C8 = false>
 hipError_t run_kind(int kind, const Job& j, hipStream_t st) {
   switch (kind) {
-    case 0: return run_tile<2, 2, 2, 4, G, TA, TB>(j, st);
-    case 1: return run_tile<2, 4, 1, 4, G, TA, TB>(j, st);
-    case 2: return run_tile<2, 8, 1, 3, G, TA, TB>(j, st);
-    case 3: return run_tile<4, 4, 1, 4, G, TA, TB>(j, st);
-    case 4: return run_tile<4, 8, 1, 3, G, TA, TB>(j, st);
-    default: return run_tile<8, 8, 1, 2, G, TA, TB>(j, st);
+    case 0: return run_tile<2, 2, 2, 4, G, TA, TB, C8>(j, st);
+    case 1: return run_tile<2, 4, 1, 4, G, TA, TB, C8>(j, st);
+    case 2: return run_tile<2, 8, 1, 3, G, TA, TB, C8>(j, st);
+    case 3: return run_tile<4, 4, 1, 4, G, TA, TB, C8>(j, st);
+    case 4: return run_tile<4, 8, 1, 3, G, TA, TB, C8>(j, st);
+    default: return run_tile<8, 8, 1, 2, G, TA, TB, C8>(j, st);
   }
 }
 
@@ -794,18 +874,23 @@ hipError_t launch_bf16_moe_wgrad(const uint16_t* dY, const Bf16Rows& X, uint16_t
                                  const Bf16Plan& plan, int64_t N, int64_t K, int32_t dy_div,
                                  int32_t x_div, hipStream_t st) {
   const Job j = {dY, X, dW, N, K, 0, plan, dy_div, x_div};
-  if (X.scales) return run_simple<kSums, true, true, true>(j, st);
   if (!fits(plan.P / dy_div * N) || !fits(plan.P / x_div * K))
-    return run_simple<kSums, true, true, false>(j, st);
-  return run_kind<kSums, true, true>(pick(N, K, plan.E, plan.P / plan.E, 0), j, st);
+    return X.scales ? run_simple<kSums, true, true, true>(j, st)
+                    : run_simple<kSums, true, true, false>(j, st);
+  const int kind = pick(N, K, plan.E, plan.P / plan.E, 0);
+  return X.scales ? run_kind<kSums, true, true, true>(kind, j, st)
+                  : run_kind<kSums, true, true>(kind, j, st);
 }
 
 hipError_t launch_bf16_gemm_tn(const uint16_t* A, const Bf16Rows& B, uint16_t* C, int64_t M,
                                int64_t N, int64_t K, hipStream_t st) {
   const Job j = {A, B, C, N, K, M, {}, 1, 1};
-  if (B.scales) return run_simple<kDense, true, true, true>(j, st);
-  if (!fits(M * N) || !fits(M * K)) return run_simple<kDense, true, true, false>(j, st);
-  return run_kind<kDense, true, true>(pick(N, K, 1, M, 0), j, st);
+  if (!fits(M * N) || !fits(M * K))
+    return B.scales ? run_simple<kDense, true, true, true>(j, st)
+                    : run_simple<kDense, true, true, false>(j, st);
+  const int kind = pick(N, K, 1, M, 0);
+  return B.scales ? run_kind<kDense, true, true, true>(kind, j, st)
+                  : run_kind<kDense, true, true>(kind, j, st);
 }
 
 }  // namespace w4

@@ -506,3 +506,66 @@ def test_another_stream_and_twice_the_same_bits():
     for r in results:
         for a, b in zip(one, r):
             assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------- larger sizes --
+# Sizes at which each shape of tile is chosen, against fp64 sums on the GPU (the
+# oracle's loops in another place).
+
+def check_large(got, want, mag, n, what):
+    tol = HALF * want.abs() + n * 2.0 ** -23 * mag * (1 + HALF) + TINY
+    err = (got.double() - want).abs()
+    assert bool((err <= tol).all()), f"{what}: worst {float((err / tol).max()):.3g} of the tolerance"
+
+
+def stored(x, s):
+    if s is None:
+        return x.double()
+    v = torch.exp2(s.view(torch.uint8).double() - 127).repeat_interleave(128, 1)[:, : x.shape[1]]
+    return x.float().double() * v
+
+
+@pytest.mark.parametrize("M,N,K", [(700, 4096, 4096), (2050, 2304, 4112), (1500, 1024, 2064), (900, 1096, 1040),
+                                   (2048, 512, 768), (4100, 264, 272), (20000, 64, 80)])
+@pytest.mark.parametrize("codes", [False, True])
+def test_large_gemm_tn(M, N, K, codes):
+    say(f"large gemm_tn M={M} N={N} K={K} codes={codes}")
+    A, B, SB = normal((M, N), 1).to(dev()), normal((M, K), 2).to(dev()), None
+    if codes:
+        B, SB = w4.w8_quantize_rows(B)
+    b = stored(B, SB)
+    check_large(w4.w4_bf16_gemm_tn(A, B, SB=SB), A.double().t() @ b, A.double().abs().t() @ b.abs(), M, "C")
+
+
+@pytest.mark.parametrize("T,k,E,N,K", [(2000, 2, 4, 4096, 2048), (1500, 4, 16, 1040, 2064), (3000, 2, 8, 520, 784),
+                                       (700, 4, 8, 256, 512), (900, 8, 32, 136, 272), (4000, 1, 2, 64, 64),
+                                       (300, 2, 64, 1408, 1024)])
+@pytest.mark.parametrize("codes", [False, True])
+def test_large_grouped(T, k, E, N, K, codes):
+    """The three directions on skewed experts."""
+    say(f"large grouped T={T} k={k} E={E} N={N} K={K} codes={codes}")
+    g = torch.Generator().manual_seed(4)
+    lg = torch.randn((T, E), generator=g)
+    lg[:, : max(1, E // 8)] += 1.5
+    ids = torch.topk(lg, k, 1).indices.to(torch.int32).to(dev())
+    B = w4.w4_bf16_pick_block_size(T, k, E)
+    p = w4.moe_align_block_size(ids, E, B)
+    X, dY, SX = normal((T, K), 1).to(dev()), normal((T * k, N), 2).to(dev()), None
+    W = normal((E, N, K), 3, 0.05).to(dev())
+    flat = ids.reshape(-1)
+    if not codes:
+        Y = w4.w4_bf16_moe_gemm(X, W, *p, T, k, B, k)
+        dX = w4.w4_bf16_moe_gemm(dY, W, *p, T, k, B, 1, transposed=True)
+        few = w4.w4_bf16_moe_gemm(X, W, *w4.moe_align_block_size(ids, E, 64), T, k, 64, k)
+    else:
+        X, SX = w4.w8_quantize_rows(X)
+    dW = w4.w4_bf16_moe_wgrad(dY, X, *p, E, T, k, B, 1, k, SX=SX)
+    x = stored(X, SX)
+    for e in range(E):
+        f = torch.nonzero(flat == e)[:, 0]
+        xe, ye, we = x[f // k], dY[f].double(), W[e].double()
+        check_large(dW[e], ye.t() @ xe, ye.abs().t() @ xe.abs(), T, f"dW[{e}]")
+        if not codes:
+            check_large(Y[f], xe @ we.t(), xe.abs() @ we.abs().t(), K, f"Y of {e}")
+            check_large(few[f], xe @ we.t(), xe.abs() @ we.abs().t(), K, f"Y of {e}, small blocks")
+            check_large(dX[f], ye @ we, ye.abs() @ we.abs(), N, f"dX of {e}")
