@@ -46,19 +46,41 @@ __device__ __forceinline__ int first_not(int n, Below below) {
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// The slots of expert e: [first, first + count).
+// The slots of expert e: [first, first + count), the last block's rest padding.
+// Both ends of its run of blocks are searched for together (the loads of a pass
+// depend on the pass before, about 0.7 us each).
 struct Segment {
-  int first, count;
+  int first, count, blocks;
 };
 __device__ __forceinline__ Segment segment(const Bf16Plan& g, int64_t cap, int e) {
-  const int nblk = (int)(min(max((int64_t)g.ntpp[0], (int64_t)0), cap) / g.B);
-  const int lo = first_not(nblk, [&](int b) { return g.expert_ids[b] < e; });
-  const int hi = first_not(nblk, [&](int b) { return g.expert_ids[b] <= e; });
-  if (hi <= lo) return {0, 0};
-  const int last = (hi - 1) * g.B;
-  const int tail =
-      first_not(g.B, [&](int i) { return (uint32_t)g.sorted_ids[last + i] < (uint32_t)g.P; });
-  return {lo * g.B, last - lo * g.B + tail};
+  const int lane = threadIdx.x & 63;
+  const int total = g.ntpp[0];
+  const int all = (int)(cap / g.B);
+  auto key = [&](int b) { return (uint32_t)g.expert_ids[b]; };     // -1 past the end: last
+  int lo, hi;
+  if (all <= 64 * 64) {
+    const int step = (all + 63) / 64;
+    const uint32_t k = lane * step < all ? key(lane * step) : ~0u;
+    const int below_lo = __popcll(__ballot(k < (uint32_t)e)), below_hi = __popcll(__ballot(k <= (uint32_t)e));
+    lo = max((below_lo - 1) * step + 1, 0);
+    hi = max((below_hi - 1) * step + 1, 0);
+    if (step > 1) {
+      const uint32_t a = lane < step - 1 && lo + lane < all ? key(lo + lane) : ~0u;
+      const uint32_t b = lane < step - 1 && hi + lane < all ? key(hi + lane) : ~0u;
+      lo += below_lo == 0 ? 0 : __popcll(__ballot(a < (uint32_t)e));
+      hi += below_hi == 0 ? 0 : __popcll(__ballot(b <= (uint32_t)e));
+    }
+  } else {
+    lo = first_not(all, [&](int b) { return key(b) < (uint32_t)e; });
+    hi = first_not(all, [&](int b) { return key(b) <= (uint32_t)e; });
+  }
+  hi = __builtin_amdgcn_readfirstlane(min(hi, total / g.B));
+  lo = __builtin_amdgcn_readfirstlane(min(lo, hi));
+  if (lo == hi) return {0, 0, 0};
+  int tail = 0;
+  for (int i = 0; i < g.B; i += 64)
+    tail += __popcll(__ballot((uint32_t)g.sorted_ids[(hi - 1) * g.B + i + lane] < (uint32_t)g.P));
+  return {lo * g.B, (hi - 1 - lo) * g.B + __builtin_amdgcn_readfirstlane(tail), hi - lo};
 }
 
 // The lower and the upper two of four e4m3 codes times a power of two, as bf16.
@@ -339,9 +361,9 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   uint8_t* const bs3 = bs3_[kg];
 
   // tile order: XCD x (workgroups round-robin over 8) walks a contiguous range
-  // of tiles in groups of 8 row blocks, which share operands in its L2; an
-  // expert's tiles of a weight gradient are spread over all XCDs, since hot
-  // experts would keep one busy
+  // of tiles in groups of 8 row blocks, which share operands in its L2.  An expert's
+  // tiles of a weight gradient are spread over all XCDs, since hot experts would
+  // keep one busy.
   int64_t cap = 0, M = j.M;
   if constexpr (G != kDense) cap = (j.g.P + (int64_t)j.g.E * (j.g.B - 1) + j.g.B - 1) / j.g.B * j.g.B;
   if constexpr (G == kRows) M = min(M, min(cap, (int64_t)j.g.ntpp[0]));
@@ -359,7 +381,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   const int gm = (int)min((int64_t)8, mt - band * 8);
   const int64_t m0 = (band * 8 + in_band % gm) * BM, n0 = in_band / gm * BN;
 
-  int sum = (int)j.K;                              // length of the sum
+  int sum = (int)j.K, slots = 0;                   // length of the sum; kSums: with padding
   const int32_t* ids = j.g.sorted_ids;
   const uint16_t* A = j.A;
   const uint8_t* B = (const uint8_t*)j.B.p;
@@ -374,7 +396,15 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     const Segment seg = segment(j.g, cap, (int)e);
     ids += seg.first;
     sum = seg.count;
+    slots = seg.blocks * j.g.B;
     C += e * M * j.N;
+    if (sum == 0) {                                // no pairs: zeros
+      for (int64_t i = threadIdx.x; i < BM * (BN / 8); i += 256 * KG) {
+        const int64_t row = m0 + i / (BN / 8), col = n0 + i % (BN / 8) * 8;
+        if (row < M && col < j.N) *(u32x4*)(C + row * j.N + col) = u32x4{0u, 0u, 0u, 0u};
+      }
+      return;
+    }
   }
   const int steps = (sum + 63) / 64;
   // this group's steps, a multiple of the stages for every group (those past
@@ -396,7 +426,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   const int64_t lds = w8_cols(j.N);                // C8: scales of a row
   const __amdgpu_buffer_rsrc_t sr =
       rsrc(C8 ? j.B.scales + (n0 >> 7) : nullptr, C8 ? rows_b * lds - (n0 >> 7) : 0);
-  const __amdgpu_buffer_rsrc_t ir = rsrc(ids, G == kSums ? (int64_t)sum * 4 : 0);
+  const __amdgpu_buffer_rsrc_t ir = rsrc(ids, (int64_t)slots * 4);
 
   // Load I of a stage.  Rows along the sum: it fills rows 8 I .. 8 I + 7, lane l
   // slot l % 8 of row l / 8, which holds piece (l % 8) ^ ((row / 2) % 8).
@@ -680,7 +710,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     id = coming;
   };
 
-  if (G != kSums || sum > 0) {
+  {
     // the pairs of the first stages together, then the stages
     uint32_t f[NST + 2];
 #pragma unroll
