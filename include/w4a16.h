@@ -706,7 +706,8 @@ int32_t w4_bf16_pick_block_size(int64_t T, int32_t k, int32_t E);
 int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted_token_ids,
                      const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
                      uint16_t* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K,
-                     int32_t B, int32_t x_row_div, int32_t transposed, void* stream);
+                     int32_t B, int32_t x_row_div, int32_t transposed, float* workspace,
+                     void* stream);
 
 /*
  * w4_bf16_moe_wgrad -- the weight gradient of w4_bf16_moe_gemm (transposed == 0):
@@ -717,12 +718,15 @@ int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted
  * or with SX a checkpoint of such rows; dW bf16 [E, N, K], written whole; all
  * 16-byte aligned, SX 4-byte.  N % 8 == 0, K % 8 == 0 (16 with SX), both >= 1;
  * dy_row_div and x_row_div in {1, k} (W4_ERR_SHAPE).  T == 0 writes zeros.
+ * workspace: fp32 [w4_bf16_moe_wgrad_workspace(T, k, E, N, K)] or NULL, as
+ * w4_bf16_moe_gemm's.
  */
+int64_t w4_bf16_moe_wgrad_workspace(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K);
 int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,
                       const int32_t* sorted_token_ids, const int32_t* expert_ids,
                       const int32_t* num_tokens_post_padded, uint16_t* dW, int64_t T, int32_t k,
                       int32_t E, int64_t N, int64_t K, int32_t B, int32_t dy_row_div,
-                      int32_t x_row_div, void* stream);
+                      int32_t x_row_div, float* workspace, void* stream);
 
 /*
  * w4_bf16_gemm_tn -- C = A^T B, summed over the rows that both have (a linear
@@ -731,10 +735,12 @@ int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,
  * with fp32 accumulation (order unspecified but fixed).  A bf16 [M, N]; B bf16
  * [M, K], or with SB a checkpoint of such rows; C bf16 [N, K]; all 16-byte
  * aligned, SB 4-byte.  N % 8 == 0, K % 8 == 0 (16 with SB) (W4_ERR_SHAPE).
- * N*K == 0 is a no-op; M == 0 writes zeros.
+ * N*K == 0 is a no-op; M == 0 writes zeros.  workspace: fp32
+ * [w4_bf16_gemm_tn_workspace(M, N, K)] or NULL, as w4_bf16_moe_gemm's.
  */
+int64_t w4_bf16_gemm_tn_workspace(int64_t M, int64_t N, int64_t K);
 int w4_bf16_gemm_tn(const uint16_t* A, const void* B, const uint8_t* SB, uint16_t* C, int64_t M,
-                    int64_t N, int64_t K, void* stream);
+                    int64_t N, int64_t K, float* workspace, void* stream);
 
 /*
  * w4_silu_mul_bwd -- gradient of the SwiGLU between the expert projections and

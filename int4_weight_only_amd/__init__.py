@@ -25,6 +25,7 @@ Layouts (all row-major, contiguous, on one GPU):
           training take in place of the bf16 rows
 """
 
+import functools
 import math
 
 import torch
@@ -46,7 +47,7 @@ __all__ = [
     "w8_pick_block_size", "w8a8_moe_gemm", "w8a8_moe_gemm_swiglu", "w4_moe_route_scored",
     "w4_moe_route_scored_bwd",
     "w4_bf16_pick_block_size", "w4_bf16_moe_gemm", "w4_bf16_moe_wgrad", "w4_bf16_gemm_tn",
-    "w4_silu_mul_bwd",
+    "w4_bf16_moe_gemm_workspace", "w4_bf16_moe_wgrad_workspace", "w4_bf16_gemm_tn_workspace", "w4_silu_mul_bwd",
 ]
 
 
@@ -1052,14 +1053,53 @@ def _rows_or_codes(scales):
     return _BF16 if scales is None else _E4M3
 
 
+@functools.lru_cache(1024)
+def w4_bf16_moe_gemm_workspace(T, k, E, N, K, B):
+    """fp32 values of ``w4_bf16_moe_gemm``'s workspace (0: it needs none)."""
+    n = int(_lib.load().w4_bf16_moe_gemm_workspace(T, k, E, N, K, B))
+    if n < 0:
+        raise ValueError("invalid T, k, E, N, K or B")
+    return n
+
+
+@functools.lru_cache(1024)
+def w4_bf16_moe_wgrad_workspace(T, k, E, N, K):
+    """fp32 values of ``w4_bf16_moe_wgrad``'s workspace (0: it needs none)."""
+    n = int(_lib.load().w4_bf16_moe_wgrad_workspace(T, k, E, N, K))
+    if n < 0:
+        raise ValueError("invalid T, k, E, N or K")
+    return n
+
+
+@functools.lru_cache(1024)
+def w4_bf16_gemm_tn_workspace(M, N, K):
+    """fp32 values of ``w4_bf16_gemm_tn``'s workspace (0: it needs none)."""
+    n = int(_lib.load().w4_bf16_gemm_tn_workspace(M, N, K))
+    if n < 0:
+        raise ValueError("invalid M, N or K")
+    return n
+
+
+def _workspace(t, size, like):
+    """The pointer to ``t``, checked, or to a new tensor; None where none is needed."""
+    if size == 0:
+        return None, None
+    if t is None:
+        t = like.new_empty(size, dtype=_F32)
+    elif _in(t, "workspace", _F32, 1, like.get_device()) is not None and t.numel() < size:
+        raise ValueError(f"workspace needs {size} values")
+    return t, t.data_ptr()
+
+
 def w4_bf16_moe_gemm(X, W, sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, B, x_row_div,
-                     transposed=False, out=None):
+                     transposed=False, out=None, workspace=None):
     """Grouped bf16 expert product over aligned blocks of B (a multiple of 64).
 
     Row f of ``out`` bf16 [T*k, N] = row f // x_row_div of X bf16 times W[e]^T
     (W bf16 [E, N, K]), or times W[e] (``transposed``, W [E, K, N]: the input
     gradient), for every valid slot f of every block with e = expert_ids[b].
-    Other rows are not written.
+    Other rows are not written.  ``workspace`` fp32
+    [w4_bf16_moe_gemm_workspace(...)], allocated when omitted.
     """
     device, K = _pair_rows(X, "X", _BF16, T, k, x_row_div)
     _in(W, "W", _BF16, 3, device)
@@ -1070,16 +1110,19 @@ def w4_bf16_moe_gemm(X, W, sorted_token_ids, expert_ids, num_tokens_post_padded,
         raise ValueError(f"shape mismatch: X {tuple(X.shape)} W {tuple(W.shape)}")
     plan = _bf16_plan(sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, E, B, device)
     out = _out(out, "out", (T * k, N), _BF16, X)
+    size = w4_bf16_moe_gemm_workspace(T, k, E, N, K, B) if N and K and B % 64 == 0 else 0
+    kept, pointer = _workspace(workspace, size, X)
     _call("w4_bf16_moe_gemm", device, X.data_ptr(), W.data_ptr(), *plan, out.data_ptr(), T, k, E, N, K,
-          B, x_row_div, int(transposed))
+          B, x_row_div, int(transposed), pointer)
     return out
 
 
 def w4_bf16_moe_wgrad(dY, X, sorted_token_ids, expert_ids, num_tokens_post_padded, E, T, k, B,
-                      dy_row_div, x_row_div, SX=None, out=None):
+                      dy_row_div, x_row_div, SX=None, out=None, workspace=None):
     """Weight gradient of ``w4_bf16_moe_gemm``: bf16 [E, N, K], expert e's the sum
     over its pairs f of dY[f // dy_row_div]^T X[f // x_row_div], zeros where it has
-    none.  dY bf16; X bf16, or with SX a checkpoint (``w8_quantize_rows``)."""
+    none.  dY bf16; X bf16, or with SX a checkpoint (``w8_quantize_rows``).
+    ``workspace`` fp32 [w4_bf16_moe_wgrad_workspace(...)], allocated when omitted."""
     device, N = _pair_rows(dY, "dY", _BF16, T, k, dy_row_div)
     _, K = _pair_rows(X, "X", _rows_or_codes(SX), T, k, x_row_div, device)
     if SX is not None:
@@ -1088,14 +1131,16 @@ def w4_bf16_moe_wgrad(dY, X, sorted_token_ids, expert_ids, num_tokens_post_padde
         raise ValueError("E must be at least 1")
     plan = _bf16_plan(sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, E, B, device)
     out = _out(out, "out", (E, N, K), _BF16, dY)
+    kept, pointer = _workspace(workspace, w4_bf16_moe_wgrad_workspace(T, k, E, N, K) if N and K else 0, dY)
     _call("w4_bf16_moe_wgrad", device, dY.data_ptr(), X.data_ptr(), _ptr(SX), *plan, out.data_ptr(), T, k,
-          E, N, K, B, dy_row_div, x_row_div)
+          E, N, K, B, dy_row_div, x_row_div, pointer)
     return out
 
 
-def w4_bf16_gemm_tn(A, B, SB=None, out=None):
+def w4_bf16_gemm_tn(A, B, SB=None, out=None, workspace=None):
     """bf16 A [M, N], B [M, K] -> bf16 [N, K] = A^T B; B bf16, or with SB a
-    checkpoint (``w8_quantize_rows``)."""
+    checkpoint (``w8_quantize_rows``).  ``workspace`` fp32
+    [w4_bf16_gemm_tn_workspace(M, N, K)], allocated when omitted."""
     device = _in(A, "A", _BF16, 2)
     _in(B, "B", _rows_or_codes(SB), 2, device)
     M, N = A.shape
@@ -1105,7 +1150,8 @@ def w4_bf16_gemm_tn(A, B, SB=None, out=None):
     if SB is not None:
         _shape(SB, "SB", _E8M0, (M, w8_scale_cols(K)), device)
     out = _out(out, "out", (N, K), _BF16, A)
-    _call("w4_bf16_gemm_tn", device, A.data_ptr(), B.data_ptr(), _ptr(SB), out.data_ptr(), M, N, K)
+    kept, pointer = _workspace(workspace, w4_bf16_gemm_tn_workspace(M, N, K), A)
+    _call("w4_bf16_gemm_tn", device, A.data_ptr(), B.data_ptr(), _ptr(SB), out.data_ptr(), M, N, K, pointer)
     return out
 
 

@@ -75,10 +75,13 @@ SIGNATURES = {
                                                ctypes.c_float, _p, _p]),
     "w4_bf16_pick_block_size": (_i32, [_i64, _i32, _i32]),
     "w4_bf16_moe_gemm": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i64, _i64, _i32,
-                                        _i32, _i32, _p]),
+                                        _i32, _i32, _p, _p]),
+    "w4_bf16_moe_gemm_workspace": (_i64, [_i64, _i32, _i32, _i64, _i64, _i32]),
     "w4_bf16_moe_wgrad": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i64, _i64,
-                                         _i32, _i32, _i32, _p]),
-    "w4_bf16_gemm_tn": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _i64, _p]),
+                                         _i32, _i32, _i32, _p, _p]),
+    "w4_bf16_moe_wgrad_workspace": (_i64, [_i64, _i32, _i32, _i64, _i64]),
+    "w4_bf16_gemm_tn": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p]),
+    "w4_bf16_gemm_tn_workspace": (_i64, [_i64, _i64, _i64]),
     "w4_silu_mul_bwd": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _p, _p, _p, _p]),
 }
 

@@ -818,10 +818,18 @@ int32_t w4_bf16_pick_block_size(int64_t T, int32_t k, int32_t E) {
   return B;
 }
 
+int64_t w4_bf16_moe_gemm_workspace(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B) {
+  if (T < 0 || k < 1 || E < 1 || N < 1 || K < 1 || B < 64 || B % 64 != 0 || T > kMaxI32 ||
+      N > kBf16MaxCols || K > kBf16MaxCols || T * k + (int64_t)E * B >= kMaxI32)
+    return -1;
+  return T == 0 ? 0 : w4::bf16_moe_workspace(T * k, E, N, K, B);
+}
+
 int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted_token_ids,
                      const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
                      uint16_t* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K,
-                     int32_t B, int32_t x_row_div, int32_t transposed, void* stream) {
+                     int32_t B, int32_t x_row_div, int32_t transposed, float* workspace,
+                     void* stream) {
   const int v = bf16_moe_validate(sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, E, N,
                                   K, B);
   if (v == W4_ERR_SHAPE) return v;
@@ -831,17 +839,18 @@ int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted
   if (T == 0) return W4_OK;
   if (v != W4_OK) return v;
   if (!X || !W || !Y) return W4_ERR_NULL;
-  if (!aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 2)) return W4_ERR_MISALIGNED;
+  if (!aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 2) || !aligned(workspace, 16))
+    return W4_ERR_MISALIGNED;
   const w4::Bf16Plan plan = {sorted_token_ids, expert_ids, num_tokens_post_padded, T * k, E, B};
   return hip_status(w4::launch_bf16_moe_gemm(X, W, Y, plan, N, K, x_row_div, transposed != 0,
-                                             as_stream(stream)));
+                                             workspace, as_stream(stream)));
 }
 
 int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,
                       const int32_t* sorted_token_ids, const int32_t* expert_ids,
                       const int32_t* num_tokens_post_padded, uint16_t* dW, int64_t T, int32_t k,
                       int32_t E, int64_t N, int64_t K, int32_t B, int32_t dy_row_div,
-                      int32_t x_row_div, void* stream) {
+                      int32_t x_row_div, float* workspace, void* stream) {
   const int v = bf16_moe_validate(sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, E, N,
                                   K, B);
   if (v == W4_ERR_SHAPE) return v;
@@ -852,15 +861,30 @@ int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,
     return W4_ERR_UNSUPPORTED;
   if (v != W4_OK) return v;
   if (!dW || (T > 0 && (!dY || !X))) return W4_ERR_NULL;
-  if (!aligned(dY, 16) || !aligned(X, 16) || !aligned(SX, 4) || !aligned(dW, 16))
+  if (!aligned(dY, 16) || !aligned(X, 16) || !aligned(SX, 4) || !aligned(dW, 16) ||
+      !aligned(workspace, 16))
     return W4_ERR_MISALIGNED;
   const w4::Bf16Plan plan = {sorted_token_ids, expert_ids, num_tokens_post_padded, T * k, E, B};
   return hip_status(w4::launch_bf16_moe_wgrad(dY, {X, SX}, dW, plan, N, K, dy_row_div, x_row_div,
-                                              as_stream(stream)));
+                                              workspace, as_stream(stream)));
+}
+
+int64_t w4_bf16_moe_wgrad_workspace(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K) {
+  if (T < 0 || k < 1 || E < 1 || N < 1 || K < 1 || T > kMaxI32 || N > kBf16MaxCols ||
+      K > kBf16MaxCols || T * k > kMaxI32 || E * (N * K) > kMaxElems)
+    return -1;
+  return w4::bf16_sums_workspace(E, T * k / E, N, K);
+}
+
+int64_t w4_bf16_gemm_tn_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0 || M > kMaxI32 || N > kBf16MaxCols || K > kBf16MaxCols ||
+      N * K > kMaxElems)
+    return -1;
+  return N == 0 || K == 0 ? 0 : w4::bf16_sums_workspace(1, M, N, K);
 }
 
 int w4_bf16_gemm_tn(const uint16_t* A, const void* B, const uint8_t* SB, uint16_t* C, int64_t M,
-                    int64_t N, int64_t K, void* stream) {
+                    int64_t N, int64_t K, float* workspace, void* stream) {
   if (M < 0 || N < 0 || K < 0 || N % 8 != 0 || K % 8 != 0 || (SB && K % 16 != 0))
     return W4_ERR_SHAPE;
   if (M > kMaxI32 || N > kBf16MaxCols || K > kBf16MaxCols || M * N > kMaxElems ||
@@ -868,10 +892,11 @@ int w4_bf16_gemm_tn(const uint16_t* A, const void* B, const uint8_t* SB, uint16_
     return W4_ERR_UNSUPPORTED;
   if (N == 0 || K == 0) return W4_OK;
   if (!C || (M > 0 && (!A || !B))) return W4_ERR_NULL;
-  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(SB, 4) || !aligned(C, 16))
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(SB, 4) || !aligned(C, 16) ||
+      !aligned(workspace, 16))
     return W4_ERR_MISALIGNED;
   if (M == 0) return hip_status(w4::launch_zero_bf16(C, N * K, as_stream(stream)));
-  return hip_status(w4::launch_bf16_gemm_tn(A, {B, SB}, C, M, N, K, as_stream(stream)));
+  return hip_status(w4::launch_bf16_gemm_tn(A, {B, SB}, C, M, N, K, workspace, as_stream(stream)));
 }
 
 int w4_silu_mul_bwd(const void* H1, const uint8_t* SH, const uint16_t* dA, const float* weights,

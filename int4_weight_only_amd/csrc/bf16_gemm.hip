@@ -26,7 +26,10 @@ struct Job {
   int64_t M, N, K;          // C is M x N (kRows: M slots; a row of C a pair), K the summed dimension
   Bf16Plan g;
   int32_t a_div, b_div;     // pairs per row of A, of B
+  float* part;              // splits > 1: that many partial sums of each C, fp32, one after another
+  int32_t splits;
 };
+
 
 // First of n ascending numbers that is not below e, by 64 probes at a time;
 // always within [0, n], whatever the numbers are.
@@ -233,6 +236,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t by
                                            0x00020000);
 }
 
+// Small tiles leave room for others on their CU: one loads or stores while another
+// multiplies.
+constexpr int workgroups_per_cu(int mi, int ni) {
+  return mi * ni <= 4 ? 4 : mi * ni <= 8 ? 3 : mi * ni <= 16 ? 2 : 1;
+}
+
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
@@ -303,19 +312,16 @@ struct Operand {           // 16 rows x 64 of the sum: two MFMA operands
 
 }  // namespace
 
-// Large tiles (NST 2 or 3 stages) multiply a step in four quarters, (A low, B low),
-// (A low, B high), (A high, B high), (A high, B low), so that a wave holds its
-// operands once and reads them during the quarters before: the high halves in the
-// first, then, when the next stage has landed, its low halves in the third and
-// fourth, into registers whose half is done (B's two sets swap roles every step).
-// After the first quarter a stage has been read and its buffer takes the loads of
-// NST steps ahead, spread over the other three quarters.  An odd number of steps is
-// made even by one of zeros.  Small tiles (four stages) hold two steps' operands:
-// one multiplies while the next is read, one barrier a step.
+// A step is multiplied in four quarters, (A low, B low), (A low, B high), (A high, B
+// high), (A high, B low), so that a wave holds its operands once and reads them during
+// the quarters before: the high halves in the first, then, when the next stage has
+// landed, its low halves in the third and fourth, into registers whose half is done
+// (B's two sets swap roles every step).  After the first quarter a stage has been read
+// and its buffer takes the loads of two steps ahead, spread over the other three
+// quarters.  An odd number of steps is made even by one of zeros.
 //
-// KG > 1: KG such groups of four waves share the tile and split the steps between
-// them, each with stages of its own; their sums are joined through LDS in group
-// order.
+// Splits: workgroups that take a run of the steps each and leave fp32 sums to be
+// joined (k_bf16_join).
 //
 // kRows: the rows of a tile are sorted pairs of one expert, gathered by the loads.
 // kSums: the summed rows of both operands are the pairs of one expert, which
@@ -325,8 +331,8 @@ struct Operand {           // 16 rows x 64 of the sum: two MFMA operands
 // scale a lane, become bf16 by v_cvt_scalef32_pk_bf16_fp8 (which applies the power of
 // two) and go into the stage as bf16 rows would, so that each element is converted
 // once a workgroup and memory sees half the bytes.
-template <int MI, int NI, int KG, int NST, Group G, bool TA, bool TB, bool C8 = false>
-__global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db) {
+template <int MI, int NI, Group G, bool TA, bool TB, bool C8>
+__global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Job j, Div da, Div db) {
   constexpr int BM = 32 * MI, BN = 32 * NI;
   constexpr int XA = BM / 32, XB = C8 ? 0 : BN / 32;   // 1 KB loads per wave and stage
   constexpr int XC = C8 ? BN / 64 : 0;             // 16 codes each, and their scales
@@ -334,31 +340,19 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   static_assert(MI % 2 == 0 && NI % 2 == 0 && MI <= 8 && NI <= 8, "halves");
   static_assert(!TA || (MI & (MI - 1)) == 0, "lanes of a row");
   static_assert(!TB || (NI & (NI - 1)) == 0, "lanes of a row");
-  static_assert(NST >= 2 && NST <= 4, "stages");
+  constexpr bool PARTS = MI * NI <= 16;            // large tiles are not for few results
   static_assert(G == kSums ? TA && TB : true, "pairs run across both operands");
   constexpr int SA = BM * 128, SB = BN * 128;
-  constexpr bool S3 = NST > 2, S4 = NST > 3;
   // each stage an object of its own: the compiler then knows which loads an
   // operand read has to wait for
-  __shared__ __attribute__((aligned(16))) uint8_t as0_[KG][SA], as1_[KG][SA];
-  __shared__ __attribute__((aligned(16))) uint8_t bs0_[KG][SB], bs1_[KG][SB];
-  __shared__ __attribute__((aligned(16))) uint8_t as2_[KG][S3 ? SA : 16], as3_[KG][S4 ? SA : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t bs2_[KG][S3 ? SB : 16], bs3_[KG][S4 ? SB : 16];
-  __shared__ __attribute__((aligned(16))) u32x4 rows_[KG][4][2][G == kSums ? 64 : 1];
+  __shared__ __attribute__((aligned(16))) uint8_t as0[SA], as1[SA];
+  __shared__ __attribute__((aligned(16))) uint8_t bs0[SB], bs1[SB];
+  __shared__ __attribute__((aligned(16))) u32x4 rows_[4][G == kSums ? 64 : 1];
 
   const int lane = threadIdx.x & 63;
-  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
   const int wm = wave >> 1, wn = wave & 1;
   const int r16 = lane & 15, h = lane >> 4;
-  uint8_t* const as0 = as0_[kg];
-  uint8_t* const as1 = as1_[kg];
-  uint8_t* const as2 = as2_[kg];
-  uint8_t* const as3 = as3_[kg];
-  uint8_t* const bs0 = bs0_[kg];
-  uint8_t* const bs1 = bs1_[kg];
-  uint8_t* const bs2 = bs2_[kg];
-  uint8_t* const bs3 = bs3_[kg];
 
   // tile order: XCD x (workgroups round-robin over 8) walks a contiguous range
   // of tiles in groups of 8 row blocks, which share operands in its L2.  An expert's
@@ -368,15 +362,15 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   if constexpr (G != kDense) cap = (j.g.P + (int64_t)j.g.E * (j.g.B - 1) + j.g.B - 1) / j.g.B * j.g.B;
   if constexpr (G == kRows) M = min(M, min(cap, (int64_t)j.g.ntpp[0]));
   const int64_t mt = (M + BM - 1) / BM, nt = (j.N + BN - 1) / BN, tiles = mt * nt;
-  const int64_t per = (tiles + 7) / 8;
+  const int64_t per = max((tiles + 7) / 8, (int64_t)1);
   int64_t at = blockIdx.x / 8, e = 0, chunk = blockIdx.x % 8;
-  if constexpr (G == kSums) {
-    e = at / per;
-    at -= e * per;
-    chunk = (chunk + 8 - e * tiles % 8) % 8;       // few tiles: another XCD for the next expert
-  }
+  const int64_t part = at / per;                   // which sum, or part of one
+  at -= part * per;
+  if constexpr (G == kSums) e = part / j.splits;
+  const int split = (int)(part - e * j.splits);
+  chunk = (chunk + 8 - part * tiles % 8) % 8;      // few tiles: another XCD for the next one
   const int64_t t = chunk * per + at;
-  if (t >= tiles || at >= per) return;
+  if (t >= tiles || split >= j.splits) return;
   const int64_t band = t / (8 * nt), in_band = t - band * 8 * nt;
   const int gm = (int)min((int64_t)8, mt - band * 8);
   const int64_t m0 = (band * 8 + in_band % gm) * BM, n0 = in_band / gm * BN;
@@ -398,8 +392,8 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     sum = seg.count;
     slots = seg.blocks * j.g.B;
     C += e * M * j.N;
-    if (sum == 0) {                                // no pairs: zeros
-      for (int64_t i = threadIdx.x; i < BM * (BN / 8); i += 256 * KG) {
+    if (sum == 0 && j.splits == 1) {               // no pairs: zeros
+      for (int64_t i = threadIdx.x; i < BM * (BN / 8); i += 256) {
         const int64_t row = m0 + i / (BN / 8), col = n0 + i % (BN / 8) * 8;
         if (row < M && col < j.N) *(u32x4*)(C + row * j.N + col) = u32x4{0u, 0u, 0u, 0u};
       }
@@ -407,11 +401,9 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     }
   }
   const int steps = (sum + 63) / 64;
-  // this group's steps, a multiple of the stages for every group (those past
-  // its own part of the sum are zeros)
-  constexpr int ROUND = NST == 3 ? 2 : NST;
-  const int share = ((steps + KG - 1) / KG + ROUND - 1) / ROUND * ROUND;
-  const int first = kg * share, last = first + share;
+  // this part's steps, an even number for every part (those past the sum are zeros)
+  const int share = ((steps + j.splits - 1) / j.splits + 1) / 2 * 2;
+  const int first = split * share, last = first + share;
   const int k_end = min(sum, last * 64);
 
   const int64_t lda = TA ? M : j.K, ldb = TB ? j.N : j.K;     // elements of a row in memory
@@ -475,7 +467,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   };
   auto next_rows = [&](int step, uint32_t f) __attribute__((always_inline)) {
     if constexpr (G == kSums) {
-      u32x4* q = rows_[kg][wave][step & 1];
+      u32x4* q = rows_[wave];                  // a wave's LDS operations keep their order
       const bool ok = step * 64 + lane < k_end && f < (uint32_t)j.g.P;
       const uint32_t fb = div_by(f, db);
       q[lane] = ok ? u32x4{div_by(f, da) * (uint32_t)lda * 2u, fb * (uint32_t)ldb * BB, C8 ? fb * (uint32_t)lds : 0u, 0u}
@@ -501,37 +493,37 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     }
   };
   // load i of the codes: 16 of row crow(i), from the lane's column on
-  u32x4 code[C8 ? (NST == 4 ? 2 : 1) : 1][C8 ? XC : 1];
-  uint32_t scale[C8 ? (NST == 4 ? 2 : 1) : 1][C8 ? XC : 1];
+  u32x4 code[C8 ? XC : 1];
+  uint32_t scale[C8 ? XC : 1];
   const int ccol = 16 * (lane % CPR);
   const bool cok = n0 + ccol < j.N;
   const uint32_t cs = (uint32_t)(((n0 + ccol) >> 7) - (n0 >> 7));
-  auto load_codes = [&](int set, int step) __attribute__((always_inline)) {
+  auto load_codes = [&](int step) __attribute__((always_inline)) {
     if constexpr (C8) {
 #pragma unroll
       for (int i = 0; i < XC; ++i) {
         if constexpr (G == kSums) {
-          code[set][i] = __builtin_amdgcn_raw_buffer_load_b128(br, cok ? (int)(brow[i] + ccol) : (int)kOOB, 0, 0);
-          scale[set][i] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(srow[i] + cs), 0, 0);
+          code[i] = __builtin_amdgcn_raw_buffer_load_b128(br, cok ? (int)(brow[i] + ccol) : (int)kOOB, 0, 0);
+          scale[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(srow[i] + cs), 0, 0);
         } else {
           const int k0 = step * 64;
           const bool ok = cok && crow(i) < k_end - k0;
-          code[set][i] = __builtin_amdgcn_raw_buffer_load_b128(
+          code[i] = __builtin_amdgcn_raw_buffer_load_b128(
               br, ok ? (int)(crow(i) * (uint32_t)ldb + ccol) : (int)kOOB, (int)((uint32_t)k0 * (uint32_t)ldb), 0);
-          scale[set][i] = __builtin_amdgcn_raw_buffer_load_b8(
+          scale[i] = __builtin_amdgcn_raw_buffer_load_b8(
               sr, ok ? (int)(crow(i) * (uint32_t)lds + cs) : (int)kOOB, (int)((uint32_t)k0 * (uint32_t)lds), 0);
         }
       }
     }
   };
-  auto put_codes = [&](int set, uint8_t* sb) __attribute__((always_inline)) {
+  auto put_codes = [&](uint8_t* sb) __attribute__((always_inline)) {
     if constexpr (C8) {
 #pragma unroll
       for (int i = 0; i < XC; ++i) {
         const int row = crow(i);
         u32x4* d = (u32x4*)(sb + row * 2 * BN + ((2 * ccol) ^ (32 * tr_swizzle<2 * BN>(row))));
-        const float s = __uint_as_float(scale[set][i] << 23);
-        const u32x4 c = code[set][i];
+        const float s = __uint_as_float(scale[i] << 23);
+        const u32x4 c = code[i];
         d[0] = u32x4{cvt2(c.x, s), cvt2h(c.x, s), cvt2(c.y, s), cvt2h(c.y, s)};
         d[1] = u32x4{cvt2(c.z, s), cvt2h(c.z, s), cvt2(c.w, s), cvt2h(c.w, s)};
       }
@@ -590,11 +582,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int n = 0; n < NI; ++n) acc[i][n] = zero;
-  // small tiles hold two steps' operands (WHOLE), large ones halves
-  constexpr bool WHOLE = MI + NI <= 8;
-  static_assert(WHOLE == (NST == 4), "stages of the two schedules");
-  static_assert(NST != 3 || KG == 1, "three stages: any even number of steps");
-  constexpr int HI = WHOLE ? MI : MI / 2, HJ = WHOLE ? NI : NI / 2;
+  constexpr int HI = MI / 2, HJ = NI / 2;
   Operand x[2][HI], w[2][HJ];
   uint32_t id = 0;                                 // kSums: the pair that next_rows turns next
   auto fence = [] __attribute__((always_inline)) {
@@ -636,44 +624,9 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
   auto none = [](int) {};
   auto nothing = [] {};
 
-  // small tiles, one step: its operands are in set S; the next one's are read
-  // into the other while they multiply
-  // (codes: two steps on their way in registers, then put into the stage tb of two
-  // steps ahead)
-  auto body_whole = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb, uint8_t* tb)
-      __attribute__((always_inline)) {
-    constexpr int s = decltype(S)::value;
-    // the loads of the two steps after the next may be in flight
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NST - 2) * (XA + XB + 2 * XC)) : "memory");
-    __builtin_amdgcn_s_barrier();
-    fence();
-    const uint32_t coming = load_id(step + 1 + NST);
-#pragma unroll
-    for (int n = 0; n < NI; ++n) w[1 - s][n] = read_b(nb, n);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) x[1 - s][i] = read_a(na, i);
-    next_rows(step + NST, id);
-    id = coming;
-    fence();
-    put_codes(s, tb);
-    load_codes(s, step + NST);
-#pragma unroll
-    for (int i = 0; i < XA + XB; ++i) load_one(i, step + NST, sa, sb);
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int n = 0; n < NI; ++n) multiply(acc[i][n], w[s][n], x[s][i]);
-#pragma unroll
-    for (int q = 0; q < 2 * MI * NI; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                    // one MFMA
-      if (q < XA + XB) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // one load
-    }
-    fence();
-  };
-
   // one step on stage (sa, sb); (na, nb) is the next one's; the step's low
   // half of B is in set S
-  auto body_halves = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
+  auto body = [&](auto S, int step, uint8_t* sa, uint8_t* sb, uint8_t* na, uint8_t* nb)
       __attribute__((always_inline)) {
     constexpr int s = decltype(S)::value;
     constexpr int L2 = (XA + XB) * 3 / 8, L3 = (XA + XB) * 3 / 8;   // loads per quarter
@@ -689,100 +642,79 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     fence();
-    const uint32_t coming = load_id(step + 2 + NST);
-    quarter(lo, hi, 1 - s, none, 0, 0, [&](int i) { load_one(i, step + NST, sa, sb); }, L2, nothing);
-    // the next stage has landed; the loads just issued, and with three stages
-    // those of the step before, may be in flight
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * (XA + XB + 2 * XC) + EX + L2 + 2 * XC) : "memory");
+    const uint32_t coming = load_id(step + 4);
+    quarter(lo, hi, 1 - s, none, 0, 0, [&](int i) { load_one(i, step + 2, sa, sb); }, L2, nothing);
+    // the next stage has landed; the loads just issued may be in flight, and the codes
+    // of the step before, its last loads
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(EX + L2 + 2 * XC) : "memory");
     __builtin_amdgcn_s_barrier();
     fence();
     quarter(hi, hi, 1 - s, [&](int i) { x[0][i] = read_a(na, i); }, HI, HI * RA,
-            [&](int i) { load_one(L2 + i, step + NST, sa, sb); }, L3, nothing);
+            [&](int i) { load_one(L2 + i, step + 2, sa, sb); }, L3, nothing);
     quarter(hi, lo, s, [&](int i) { w[1 - s][i] = read_b(nb, i); }, HJ, HJ * RBN,
-            [&](int i) { load_one(L2 + L3 + i, step + NST, sa, sb); }, XA + XB - L2 - L3,
+            [&](int i) { load_one(L2 + L3 + i, step + 2, sa, sb); }, XA + XB - L2 - L3,
             [&] {
-              put_codes(0, sb);
-              next_rows(step + 1 + NST, id);
+              put_codes(sb);
+              next_rows(step + 3, id);
             });
     // behind the fence: the wait above counts these as the step's last loads
-    load_codes(0, step + 1 + NST);
+    load_codes(step + 3);
     fence();
     id = coming;
   };
 
-  {
-    // the pairs of the first stages together, then the stages
-    uint32_t f[NST + 2];
+  // the pairs of the first stages together, then the stages
+  uint32_t f[4];
 #pragma unroll
-    for (int i = 0; i < NST + 2; ++i) f[i] = load_id(first + i);
-    auto load_stage = [&](int i, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
-      next_rows(first + i, f[i]);
-      load_codes(WHOLE ? i & 1 : 0, first + i);
+  for (int i = 0; i < 4; ++i) f[i] = load_id(first + i);
+  auto load_stage = [&](int i, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
+    next_rows(first + i, f[i]);
+    load_codes(first + i);
 #pragma unroll
-      for (int n = 0; n < XA + XB; ++n) load_one(n, first + i, sa, sb);
-      if (!WHOLE || i < 2) put_codes(WHOLE ? i & 1 : 0, sb);
-    };
-    load_stage(0, as0, bs0);
-    load_stage(1, as1, bs1);
-    if constexpr (S3) load_stage(2, as2, bs2);
-    if constexpr (S4) load_stage(3, as3, bs3);
-    if constexpr (!WHOLE) {
-      next_rows(first + NST, f[NST]);
-      fence();
-      load_codes(0, first + NST);
-    }
-    id = f[WHOLE ? NST : NST + 1];
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C8 ? (WHOLE ? 0 : 2 * XC) : (NST - 1) * (XA + XB))
-                 : "memory");
-    __builtin_amdgcn_s_barrier();
-    fence();
+    for (int n = 0; n < XA + XB; ++n) load_one(n, first + i, sa, sb);
+    put_codes(sb);
+  };
+  load_stage(0, as0, bs0);
+  load_stage(1, as1, bs1);
+  next_rows(first + 2, f[2]);
+  id = f[3];
+  fence();
+  load_codes(first + 2);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C8 ? 2 * XC : XA + XB) : "memory");
+  __builtin_amdgcn_s_barrier();
+  fence();
 #pragma unroll
-    for (int i = 0; i < HI; ++i) x[0][i] = read_a(as0, i);
+  for (int i = 0; i < HI; ++i) x[0][i] = read_a(as0, i);
 #pragma unroll
-    for (int n = 0; n < HJ; ++n) w[0][n] = read_b(bs0, n);
-    fence();
-    for (int step = first; step < last; step += NST == 3 ? 6 : NST) {
-      if constexpr (NST == 3) {
-        body_halves(lo, step, as0, bs0, as1, bs1);
-        body_halves(hi, step + 1, as1, bs1, as2, bs2);
-        if (step + 2 >= last) break;
-        body_halves(lo, step + 2, as2, bs2, as0, bs0);
-        body_halves(hi, step + 3, as0, bs0, as1, bs1);
-        if (step + 4 >= last) break;
-        body_halves(lo, step + 4, as1, bs1, as2, bs2);
-        body_halves(hi, step + 5, as2, bs2, as0, bs0);
-      } else if constexpr (WHOLE) {
-        body_whole(lo, step, as0, bs0, as1, bs1, bs2);
-        body_whole(hi, step + 1, as1, bs1, as2, bs2, bs3);
-        body_whole(lo, step + 2, as2, bs2, as3, bs3, bs0);
-        body_whole(hi, step + 3, as3, bs3, as0, bs0, bs1);
-      } else {
-        body_halves(lo, step, as0, bs0, as1, bs1);
-        body_halves(hi, step + 1, as1, bs1, as0, bs0);
-      }
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // loads past the end drained
+  for (int n = 0; n < HJ; ++n) w[0][n] = read_b(bs0, n);
+  fence();
+  for (int step = first; step < last; step += 2) {
+    body(lo, step, as0, bs0, as1, bs1);
+    body(hi, step + 1, as1, bs1, as0, bs0);
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // loads past the end drained
 
-  if constexpr (KG > 1) {
-    // one column of tiles per round through the stages that are done with
-    f32x4(*part)[4][MI][64] = (f32x4(*)[4][MI][64])as0_;
-#pragma unroll
-    for (int n = 0; n < NI; ++n) {
-      __syncthreads();
-      if (kg > 0) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) part[kg][wave][i][lane] = acc[i][n];
+  if constexpr (PARTS) {
+    if (j.splits > 1) {
+      // kRows: a row a pair, filled up to whole pieces of eight
+      const int64_t width = G == kRows ? (j.N + 7) / 8 * 8 : j.N;
+      float* const sums = j.part + ((G == kSums ? e : 0) * j.splits + split) * (G == kRows ? j.g.P : M) * width;
+  #pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        int64_t row = m0 + arow0 + r16 + 16 * i;
+        bool ok = row < M;
+        if constexpr (G == kRows) {
+          row = ids[row];
+          ok = (uint32_t)row < (uint32_t)j.g.P;
+        }
+  #pragma unroll
+        for (int n = 0; n < NI; ++n) {
+          const int64_t col = n0 + brow0 + 16 * n + 4 * h;
+          if (ok && col < width) *(f32x4*)(sums + row * width + col) = acc[i][n];
+        }
       }
-      __syncthreads();
-      if (kg == 0) {
-#pragma unroll
-        for (int g = 1; g < KG; ++g)
-#pragma unroll
-          for (int i = 0; i < MI; ++i) acc[i][n] += part[g][wave][i][lane];
-      }
+      return;
     }
-    if (kg > 0) return;
   }
   const bool vec = (j.N & 7) == 0 && ((uintptr_t)C & 15) == 0;
 #pragma unroll
@@ -799,6 +731,36 @@ __global__ __launch_bounds__(256 * KG, 1) void k_bf16_tile(Job j, Div da, Div db
       if (ok) store8(C + row * j.N, n0 + brow0 + 16 * n + 8 * h, j.N, v, vec);
     }
   }
+}
+
+// Partial sums joined in their order and rounded to bf16, eight columns a thread: of
+// groups of `rows` rows, or (kRows) of the pairs that slots name.
+template <Group G>
+__global__ __launch_bounds__(256) void k_bf16_join(Job j, int64_t rows, int64_t pieces) {
+  const int64_t width = (j.N + 7) / 8 * 8;
+  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (p >= pieces) return;
+  int64_t row = p / (width / 8), group = 0;
+  const int64_t col = (p - row * (width / 8)) * 8;
+  if constexpr (G == kRows) {
+    if (row >= j.g.ntpp[0]) return;
+    row = j.g.sorted_ids[row];
+    if ((uint32_t)row >= (uint32_t)j.g.P) return;
+    const int e = j.g.expert_ids[(p / (width / 8)) / j.g.B];
+    if (e < 0 || e >= j.g.E) return;
+  } else {
+    group = row / rows;
+    row -= group * rows;
+  }
+  const float* q = j.part + (group * j.splits * rows + row) * width + col;
+  f32x4 a = *(const f32x4*)q, b = *(const f32x4*)(q + 4);
+  for (int s = 1; s < j.splits; ++s) {
+    q += rows * width;
+    a += *(const f32x4*)q;
+    b += *(const f32x4*)(q + 4);
+  }
+  const u32x4 v = {pk_bf16(a.x, a.y), pk_bf16(a.z, a.w), pk_bf16(b.x, b.y), pk_bf16(b.z, b.w)};
+  store8(j.C + (group * rows + row) * j.N, col, j.N, v, (j.N & 7) == 0 && ((uintptr_t)j.C & 15) == 0);
 }
 
 namespace {
@@ -818,55 +780,94 @@ hipError_t run_simple(const Job& j, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int MI, int NI, int KG, int NST, Group G, bool TA, bool TB, bool C8>
+template <int MI, int NI, Group G, bool TA, bool TB, bool C8>
 hipError_t run_tile(const Job& j, hipStream_t st) {
   const int64_t per = (tiles_of(j.M, j.N, 32 * MI, 32 * NI) + 7) / 8;
-  hipLaunchKernelGGL((k_bf16_tile<MI, NI, KG, NST, G, TA, TB, C8>),
-                     dim3((unsigned)(8 * per * (G == kSums ? j.g.E : 1))), dim3(256 * KG), 0, st, j,
-                     divisor(j.a_div), divisor(j.b_div));
+  const int64_t sums = (G == kSums ? j.g.E : 1) * (int64_t)j.splits;
+  hipLaunchKernelGGL((k_bf16_tile<MI, NI, G, TA, TB, C8>), dim3((unsigned)(8 * per * sums)),
+                     dim3(256), 0, st, j, divisor(j.a_div), divisor(j.b_div));
   return hipGetLastError();
 }
 
-// The tiles and what they cost: a round of one workgroup per CU takes step_us per
-// 64 of the sum and fixed_us besides (launch, first loads, stores).
+// The tiles and what they cost, in us: `fixed` and `step` (64 of the sum) for each
+// tile of a CU that is kept busy, `latency` for tiles that have their CU to themselves;
+// measured for products by rows (first) and for sums (second).  256 x 256 moves the
+// least data and wins in long sums on full rounds of the CUs (4096 x 8 pairs over 64 of
+// [4096, 2048]: 587 us, 801 in 128 x 128); 128 x 128 has two workgroups a CU, whose
+// stores and first loads hide under each other's products (4096 x 5120 over 2050
+// rows, 1.25 rounds of large tiles: 87 and 110; 512 x 4 pairs over 16 of [1024, 1024]:
+// 14 and 28); the small ones are for few rows.
 struct Kind {
-  int bm, bn, kg;
-  float step_us, fixed_us;
+  int bm, bn, occupancy;
+  float fixed[2], step[2], latency[2], latency_step[2];
 };
 constexpr Kind kKinds[] = {
-    {64, 64, 2, 0.32f, 6.0f},   {64, 128, 1, 0.40f, 6.0f},  {64, 256, 1, 0.70f, 8.0f},
-    {128, 128, 1, 0.60f, 6.0f}, {128, 256, 1, 1.05f, 10.0f}, {256, 256, 1, 1.35f, 12.0f},
+    {64, 64, 4, {1.1f, 1.2f}, {0.20f, 0.23f}, {2.2f, 2.3f}, {0.30f, 0.33f}},
+    {64, 128, 3, {1.45f, 1.5f}, {0.33f, 0.38f}, {2.3f, 2.6f}, {0.33f, 0.37f}},
+    {128, 128, 2, {2.3f, 2.3f}, {0.60f, 0.56f}, {3.6f, 3.8f}, {0.50f, 0.62f}},
+    {256, 256, 1, {9.3f, 9.3f}, {1.45f, 1.58f}, {9.3f, 9.3f}, {1.45f, 1.58f}},
 };
-constexpr int kKindCount = 6;
+constexpr int kKindCount = 4;
 
-// The kind that is done first for `tiles` groups of rows and columns, among those
-// with bm rows (0: any).
-int pick(int64_t M, int64_t N, int64_t groups, int64_t sum, int bm) {
-  int best = -1;
+float estimate(const Kind& t, int64_t tiles, int64_t steps, bool sums) {
+  const int64_t cus = cu_count(), mine = (tiles + cus - 1) / cus;
+  const int64_t waves = (mine + t.occupancy - 1) / t.occupancy;
+  const float busy = (float)mine * (t.fixed[sums] + (float)steps * t.step[sums]);
+  const float alone = (float)waves * (t.latency[sums] + (float)steps * t.latency_step[sums]);
+  return 3.0f + std::max(busy, alone);
+}
+
+int64_t steps_of(int64_t sum) { return std::max((sum + 127) / 128 * 2, (int64_t)2); }
+
+struct Choice {
+  int kind, splits;
+};
+
+// The kind that is done first, and in how many parts: few tiles of long sums are split
+// between workgroups, whose fp32 sums a second launch joins (8192 rows into 64 x 64:
+// 40 us whole, 15 in parts; one row of [4096, 4096]: 16 and 12).  groups sums of M x N
+// results; B > 0: rows in blocks of B, the padding of an expert's last tile half full.
+Choice choose(int64_t groups, int64_t M, int64_t N, int64_t sum, int32_t B, int32_t E, bool workspace) {
+  Choice best = {0, 1};
   float least = 0.0f;
-  const int64_t steps = std::max((sum + 63) / 64, (int64_t)1), cus = cu_count();
-  for (int i = 0; i < kKindCount; ++i) {
-    const Kind& t = kKinds[i];
-    if (bm != 0 && t.bm != bm) continue;
-    const int64_t rounds = (groups * tiles_of(M, N, t.bm, t.bn) + cus - 1) / cus;
-    const float us = (float)rounds * ((float)((steps + t.kg - 1) / t.kg) * t.step_us + t.fixed_us);
-    if (best < 0 || us < least) {
-      best = i;
-      least = us;
+  const int64_t steps = steps_of(sum);
+  for (int splits = 1; splits <= (workspace ? 32 : 1); splits *= 2) {
+    if (splits > 1 && steps < 4 * splits) break;
+    const float join =
+        splits == 1 ? 0.0f : 5.0f + (float)(groups * splits * M * N) * (8.0f / 4e6f);   // 4 TB/s
+    for (int i = 0; i < kKindCount; ++i) {
+      const Kind& t = kKinds[i];
+      if ((B > 0 && B % t.bm != 0) || (splits > 1 && t.bm * t.bn > 128 * 128)) continue;
+      int64_t high = (M + t.bm - 1) / t.bm;
+      if (B > 0) {
+        const int64_t used = std::min(M, (int64_t)E);
+        high = std::max(used, high + used / 2);
+      }
+      const int64_t tiles = groups * splits * high * ((N + t.bn - 1) / t.bn);
+      const float us = join + estimate(t, tiles, steps_of((sum + splits - 1) / splits), B == 0);
+      if (least == 0.0f || us < least) {
+        best = {i, splits};
+        least = us;
+      }
     }
   }
   return best;
 }
 
+Choice choose_rows(const Bf16Plan& p, int64_t N, int64_t K, bool workspace) {
+  return choose(1, p.P, N, K, p.B, p.E, workspace);
+}
+Choice choose_sums(int64_t groups, int64_t sum, int64_t M, int64_t N, bool workspace) {
+  return choose(groups, M, N, sum, 0, 0, workspace);
+}
+
 template <Group G, bool TA, bool TB, bool C8 = false>
 hipError_t run_kind(int kind, const Job& j, hipStream_t st) {
   switch (kind) {
-    case 0: return run_tile<2, 2, 2, 4, G, TA, TB, C8>(j, st);
-    case 1: return run_tile<2, 4, 1, 4, G, TA, TB, C8>(j, st);
-    case 2: return run_tile<2, 8, 1, 3, G, TA, TB, C8>(j, st);
-    case 3: return run_tile<4, 4, 1, 4, G, TA, TB, C8>(j, st);
-    case 4: return run_tile<4, 8, 1, 3, G, TA, TB, C8>(j, st);
-    default: return run_tile<8, 8, 1, 2, G, TA, TB, C8>(j, st);
+    case 0: return run_tile<2, 2, G, TA, TB, C8>(j, st);
+    case 1: return run_tile<2, 4, G, TA, TB, C8>(j, st);
+    case 2: return run_tile<4, 4, G, TA, TB, C8>(j, st);
+    default: return run_tile<8, 8, G, TA, TB, C8>(j, st);
   }
 }
 
@@ -874,53 +875,76 @@ hipError_t run_kind(int kind, const Job& j, hipStream_t st) {
 // goes through the simple kernel.
 bool fits(int64_t elems) { return elems * 2 < (int64_t)kOOB; }
 
+bool sums_fit(const Job& j, int64_t rows_a, int64_t rows_b) {
+  return fits(rows_a * j.M) && fits(rows_b * j.N);
+}
+
+template <Group G>
+hipError_t join(const Job& j, int64_t groups, int64_t rows, int64_t lines, hipStream_t st) {
+  const int64_t pieces = groups * lines * ((j.N + 7) / 8);
+  hipLaunchKernelGGL(k_bf16_join<G>, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, st, j, rows,
+                     pieces);
+  return hipGetLastError();
+}
+
+template <Group G>
+hipError_t run_sums(Job j, const Choice& c, hipStream_t st) {
+  j.splits = c.splits;
+  const hipError_t e = j.B.scales ? run_kind<G, true, true, true>(c.kind, j, st)
+                                  : run_kind<G, true, true>(c.kind, j, st);
+  return e != hipSuccess || j.splits == 1 ? e : join<G>(j, G == kSums ? j.g.E : 1, j.M, j.M, st);
+}
+
 }  // namespace
 
-// (the simple tile is the smallest of all: most workgroups, of 256 threads; KG = 2
-// makes as many of 512)
+// (64 x 64 tiles are the most workgroups; parts are for few)
 int64_t bf16_moe_threads(int64_t P, int32_t E, int64_t N, int64_t K, int32_t B) {
-  return (tiles_of(moe_cap(P, E, B), N, 64, 64) + 8) * 512;
+  return (tiles_of(moe_cap(P, E, B), N, 64, 64) + 8) * 256;
 }
 int64_t bf16_wgrad_threads(int32_t E, int64_t N, int64_t K) {
-  return E * (tiles_of(N, K, 64, 64) + 8) * 512;
+  return E * (tiles_of(N, K, 64, 64) + 8) * 256;
+}
+
+int64_t bf16_moe_workspace(int64_t P, int32_t E, int64_t N, int64_t K, int32_t B) {
+  const int splits = choose(1, P, N, K, B, E, true).splits;
+  return splits == 1 ? 0 : splits * P * ((N + 7) / 8 * 8);
+}
+int64_t bf16_sums_workspace(int64_t groups, int64_t sum, int64_t N, int64_t K) {
+  const int splits = choose_sums(groups, sum, N, K, true).splits;
+  return splits == 1 ? 0 : groups * splits * N * K;
 }
 
 hipError_t launch_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, uint16_t* Y,
                                 const Bf16Plan& plan, int64_t N, int64_t K, int32_t div,
-                                bool transposed, hipStream_t st) {
-  const Job j = {X, {W, nullptr}, Y, moe_cap(plan.P, plan.E, plan.B), N, K, plan, div, 1};
+                                bool transposed, float* workspace, hipStream_t st) {
+  Job j = {X, {W, nullptr}, Y, moe_cap(plan.P, plan.E, plan.B), N, K, plan, div, 1, workspace, 1};
   if (!fits(plan.P / div * K) || !fits(transposed ? N * K : std::min(N, (int64_t)256) * K))
     return transposed ? run_simple<kRows, false, true, false>(j, st)
                       : run_simple<kRows, false, false, false>(j, st);
-  const int bm = plan.B % 256 == 0 ? 256 : plan.B % 128 == 0 ? 128 : 64;
-  // rows that are not padding, an expert's last block half full
-  const int64_t rows = plan.P + std::min(plan.P, (int64_t)plan.E) * (bm / 2);
-  const int kind = pick(rows, N, 1, K, bm);
-  return transposed ? run_kind<kRows, false, true>(kind, j, st)
-                    : run_kind<kRows, false, false>(kind, j, st);
+  const Choice c = choose_rows(plan, N, K, workspace != nullptr);
+  j.splits = c.splits;
+  const hipError_t e = transposed ? run_kind<kRows, false, true>(c.kind, j, st)
+                                  : run_kind<kRows, false, false>(c.kind, j, st);
+  return e != hipSuccess || j.splits == 1 ? e : join<kRows>(j, 1, plan.P, j.M, st);
 }
 
 hipError_t launch_bf16_moe_wgrad(const uint16_t* dY, const Bf16Rows& X, uint16_t* dW,
                                  const Bf16Plan& plan, int64_t N, int64_t K, int32_t dy_div,
-                                 int32_t x_div, hipStream_t st) {
-  const Job j = {dY, X, dW, N, K, 0, plan, dy_div, x_div};
-  if (!fits(plan.P / dy_div * N) || !fits(plan.P / x_div * K))
+                                 int32_t x_div, float* workspace, hipStream_t st) {
+  const Job j = {dY, X, dW, N, K, 0, plan, dy_div, x_div, workspace, 1};
+  if (!sums_fit(j, plan.P / dy_div, plan.P / x_div))
     return X.scales ? run_simple<kSums, true, true, true>(j, st)
                     : run_simple<kSums, true, true, false>(j, st);
-  const int kind = pick(N, K, plan.E, plan.P / plan.E, 0);
-  return X.scales ? run_kind<kSums, true, true, true>(kind, j, st)
-                  : run_kind<kSums, true, true>(kind, j, st);
+  return run_sums<kSums>(j, choose_sums(plan.E, plan.P / plan.E, N, K, workspace != nullptr), st);
 }
 
 hipError_t launch_bf16_gemm_tn(const uint16_t* A, const Bf16Rows& B, uint16_t* C, int64_t M,
-                               int64_t N, int64_t K, hipStream_t st) {
-  const Job j = {A, B, C, N, K, M, {}, 1, 1};
-  if (!fits(M * N) || !fits(M * K))
+                               int64_t N, int64_t K, float* workspace, hipStream_t st) {
+  const Job j = {A, B, C, N, K, M, {}, 1, 1, workspace, 1};
+  if (!sums_fit(j, M, M))
     return B.scales ? run_simple<kDense, true, true, true>(j, st)
                     : run_simple<kDense, true, true, false>(j, st);
-  const int kind = pick(N, K, 1, M, 0);
-  return B.scales ? run_kind<kDense, true, true, true>(kind, j, st)
-                  : run_kind<kDense, true, true>(kind, j, st);
+  return run_sums<kDense>(j, choose_sums(1, M, N, K, workspace != nullptr), st);
 }
 
 }  // namespace w4

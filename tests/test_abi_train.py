@@ -26,12 +26,12 @@ def test_pick_block_size(lib):
     assert f(-1, 1, 1) == f(1, 0, 1) == f(1, 1, 0) == 0
 
 
-def moe_gemm(lib, X=A16, W=A16, s=A4, e=A4, n=A4, Y=A2, T=4, k=2, E=8, N=64, K=64, B=64, div=2, tr=0):
-    return lib.w4_bf16_moe_gemm(X, W, s, e, n, Y, T, k, E, N, K, B, div, tr, None)
+def moe_gemm(lib, X=A16, W=A16, s=A4, e=A4, n=A4, Y=A2, T=4, k=2, E=8, N=64, K=64, B=64, div=2, tr=0, ws=None):
+    return lib.w4_bf16_moe_gemm(X, W, s, e, n, Y, T, k, E, N, K, B, div, tr, ws, None)
 
 
-def wgrad(lib, dY=A16, X=A16, SX=None, s=A4, e=A4, n=A4, dW=A16, T=4, k=2, E=8, N=64, K=64, B=64, dd=1, dx=2):
-    return lib.w4_bf16_moe_wgrad(dY, X, SX, s, e, n, dW, T, k, E, N, K, B, dd, dx, None)
+def wgrad(lib, dY=A16, X=A16, SX=None, s=A4, e=A4, n=A4, dW=A16, T=4, k=2, E=8, N=64, K=64, B=64, dd=1, dx=2, ws=None):
+    return lib.w4_bf16_moe_wgrad(dY, X, SX, s, e, n, dW, T, k, E, N, K, B, dd, dx, ws, None)
 
 
 @pytest.mark.parametrize("f", [moe_gemm, wgrad])
@@ -53,7 +53,7 @@ def test_moe_gemm_refusals(lib):
     assert f(lib, N=60, tr=1) == SHAPE
     for name in ("X", "W", "Y"):
         assert f(lib, **{name: None}) == NULL
-    assert f(lib, X=A4) == f(lib, W=A4) == f(lib, Y=ctypes.c_void_p(0x10001)) == MISALIGNED
+    assert f(lib, X=A4) == f(lib, W=A4) == f(lib, ws=A4) == f(lib, Y=ctypes.c_void_p(0x10001)) == MISALIGNED
     assert f(lib, X=None, W=None, s=None, e=None, n=None, Y=None, T=0) == OK
 
 
@@ -64,12 +64,12 @@ def test_wgrad_refusals(lib):
     for name in ("dY", "X", "dW"):
         assert f(lib, **{name: None}) == NULL
         assert f(lib, **{name: A4}) == MISALIGNED
-    assert f(lib, SX=A2) == MISALIGNED
+    assert f(lib, SX=A2) == f(lib, ws=A4) == MISALIGNED
     assert f(lib, T=0, dW=None) == NULL
 
 
 def test_gemm_tn_refusals(lib):
-    f = lib.w4_bf16_gemm_tn
+    f = lambda *a, ws=None: lib.w4_bf16_gemm_tn(*a[:-1], ws, a[-1])
     for M, N, K, SB in ((-1, 8, 8, None), (4, -8, 8, None), (4, 8, -8, None), (4, 12, 8, None), (4, 8, 12, None),
                         (4, 8, 24, A4)):
         assert f(A16, A16, SB, A16, M, N, K, None) == SHAPE
@@ -81,10 +81,31 @@ def test_gemm_tn_refusals(lib):
     assert f(A16, A4, None, A16, 4, 8, 8, None) == MISALIGNED
     assert f(A16, A16, A2, A16, 4, 16, 16, None) == MISALIGNED
     assert f(A16, A16, None, A4, 4, 8, 8, None) == MISALIGNED
+    assert f(A16, A16, None, A16, 4, 8, 8, None, ws=A4) == MISALIGNED
     assert f(A16, A16, None, A16, 1 << 31, 8, 8, None) == UNSUPPORTED
     assert f(A16, A16, None, A16, 4, (1 << 22) + 8, 8, None) == UNSUPPORTED
     assert f(A16, A16, None, A16, 4, 8, (1 << 22) + 8, None) == UNSUPPORTED
     assert f(A16, A16, None, A16, 4, 1 << 21, 1 << 20, None) == UNSUPPORTED
+
+
+def test_workspaces(lib):
+    """Only few results of long sums are split; the parts fill whole results."""
+    f, g = lib.w4_bf16_gemm_tn_workspace, lib.w4_bf16_moe_wgrad_workspace
+    assert f(8192, 8192, 8192) == f(64, 64, 64) == f(0, 64, 64) == f(64, 0, 64) == 0
+    assert f(8192, 64, 64) > 0 and f(8192, 64, 64) % (64 * 64) == 0
+    assert f(-1, 8, 8) == f(8, -8, 8) == f(8, 8, (1 << 22) + 8) == f(1 << 31, 8, 8) == -1
+    assert g(4096, 8, 64, 4096, 4096) == 0 and g(8192, 1, 1, 64, 64) == f(8192, 64, 64)
+    assert g(-1, 1, 1, 8, 8) == g(1, 0, 1, 8, 8) == g(1, 1, 0, 8, 8) == g(1, 1, 1, 0, 8) == -1
+    m = lib.w4_bf16_moe_gemm_workspace
+    assert m(4096, 8, 64, 4096, 4096, 256) == m(0, 1, 1, 64, 64, 64) == 0
+    assert m(1, 1, 1, 4095, 4096, 64) > 0 and m(1, 1, 1, 4095, 4096, 64) % 4096 == 0
+    assert m(-1, 1, 1, 8, 8, 64) == m(1, 1, 1, 8, 8, 32) == m(1 << 30, 2, 1, 8, 8, 64) == -1
+    with pytest.raises(ValueError):
+        w4.w4_bf16_moe_gemm_workspace(1, 1, 1, 8, 8, 100)
+    with pytest.raises(ValueError):
+        w4.w4_bf16_gemm_tn_workspace(-1, 8, 8)
+    with pytest.raises(ValueError):
+        w4.w4_bf16_moe_wgrad_workspace(1, 0, 1, 8, 8)
 
 
 def test_silu_mul_bwd_refusals(lib):

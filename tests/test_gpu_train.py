@@ -569,3 +569,130 @@ def test_large_grouped(T, k, E, N, K, codes):
             check_large(Y[f], xe @ we.t(), xe.abs() @ we.abs().t(), K, f"Y of {e}")
             check_large(few[f], xe @ we.t(), xe.abs() @ we.abs().t(), K, f"Y of {e}, small blocks")
             check_large(dX[f], ye @ we, ye.abs() @ we.abs(), N, f"dX of {e}")
+
+
+# -------------------------------------------------- sums in parts, workspaces --
+
+@pytest.mark.parametrize("M,N,K", [(8192, 64, 64), (1024, 8, 16), (3000, 200, 136), (513, 64, 1040)])
+@pytest.mark.parametrize("codes", [False, True])
+def test_gemm_tn_in_parts(M, N, K, codes, monkeypatch):
+    K = -(-K // 16) * 16 if codes else K              # rows of codes are whole 16-byte pieces
+    say(f"gemm_tn in parts M={M} N={N} K={K} codes={codes}")
+    size = w4.w4_bf16_gemm_tn_workspace(M, N, K)
+    assert size % (N * K) == 0                        # 0: the rule takes these whole either way
+    A, B, SB = normal((M, N), 1).to(dev()), normal((M, K), 2).to(dev()), None
+    if codes:
+        B, SB = w4.w8_quantize_rows(B)
+    b = stored(B, SB)
+    want, mag = A.double().t() @ b, A.double().abs().t() @ b.abs()
+    ws = torch.full((size,), float("nan"), device=dev())
+    parts = w4.w4_bf16_gemm_tn(A, B, SB=SB, workspace=ws)
+    check_large(parts, want, mag, M, "parts")
+    assert torch.equal(parts, w4.w4_bf16_gemm_tn(A, B, SB=SB))
+    monkeypatch.setattr(w4, "w4_bf16_gemm_tn_workspace", lambda *a: 0)        # a caller without one
+    check_large(w4.w4_bf16_gemm_tn(A, B, SB=SB), want, mag, M, "whole")
+    monkeypatch.undo()
+    if size:
+        with pytest.raises(ValueError):
+            w4.w4_bf16_gemm_tn(A, B, SB=SB, workspace=ws[:-1])
+        with pytest.raises(TypeError):
+            w4.w4_bf16_gemm_tn(A, B, SB=SB, workspace=ws.bfloat16())
+
+
+@pytest.mark.parametrize("T,k,E,N,K", [(1, 1, 1, 4096, 4096), (3, 2, 4, 264, 2048), (5, 1, 2, 8, 8192)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_moe_gemm_in_parts(T, k, E, N, K, transposed, monkeypatch):
+    say(f"moe_gemm in parts T={T} k={k} E={E} N={N} K={K} transposed={transposed}")
+    N = N if transposed else N - 3
+    B = 64
+    size = w4.w4_bf16_moe_gemm_workspace(T, k, E, N, K, B)
+    assert size or K < 4096
+    ids = picks(T, k, E, 3, outside=1 if T > 2 else 0)
+    X, W = normal((T, K), 1), normal((E, K, N) if transposed else (E, N, K), 2, 0.1)
+    want, mag = train.moe_gemm(f64(X), f64(W), ids, k, transposed)
+    named = ~np.isnan(want[:, 0])
+    args = (X.to(dev()), W.to(dev()), *plan_of(ids, E, B), T, k, B, k)
+    for parts in (True, False):
+        out = canary_bf16((T * k, N))
+        if parts:
+            ws = torch.full((size,), float("nan"), device=dev())
+            w4.w4_bf16_moe_gemm(*args, transposed=transposed, out=out, workspace=ws)
+        else:
+            monkeypatch.setattr(w4, "w4_bf16_moe_gemm_workspace", lambda *a: 0)
+            w4.w4_bf16_moe_gemm(*args, transposed=transposed, out=out)
+        assert (down_bits(out)[~named] == CANARY).all()
+        check(out[torch.from_numpy(named).to(dev())], want[named], mag[named], K, f"parts={parts}")
+
+
+def test_moe_wgrad_in_parts():
+    """Parts of experts with many, few and no pairs."""
+    T, k, E, N, K, B = 4000, 1, 3, 72, 80, 256
+    size = w4.w4_bf16_moe_wgrad_workspace(T, k, E, N, K)
+    assert size > 0
+    ids = np.zeros((T, k), np.int32)
+    ids[:70] = 2
+    dY, X = normal((T, N), 1), normal((T, K), 2)
+    out = canary_bf16((E, N, K))
+    ws = torch.full((size,), float("nan"), device=dev())
+    w4.w4_bf16_moe_wgrad(dY.to(dev()), X.to(dev()), *plan_of(ids, E, B), E, T, k, B, 1, 1, out=out, workspace=ws)
+    want, mag = train.moe_wgrad(f64(dY), f64(X), ids, E, 1, 1)
+    check(out, want, mag, T, "dW")
+    assert (down_bits(out)[1] == 0).all()
+
+
+def test_graph_replays_of_products_in_parts():
+    A, B = normal((4096, 64), 1).to(dev()), normal((4096, 72), 2).to(dev())
+    X, W = normal((2, 4096), 3).to(dev()), normal((1, 512, 4096), 4).to(dev())
+    ids = torch.zeros((2, 1), dtype=torch.int32, device=dev())
+    assert w4.w4_bf16_gemm_tn_workspace(4096, 64, 72) and w4.w4_bf16_moe_gemm_workspace(2, 1, 1, 512, 4096, 64)
+
+    def run():
+        return (w4.w4_bf16_gemm_tn(A, B),
+                w4.w4_bf16_moe_gemm(X, W, *w4.moe_align_block_size(ids, 1, 64), 2, 1, 64, 1))
+    run()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):                                # two graphs, each with workspaces of its own
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, run()))
+    for seed in (5, 6, 7):
+        A.copy_(normal((4096, 64), seed))
+        X.copy_(normal((2, 4096), seed))
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for _, got in graphs:
+            for a, b in zip(got, run()):
+                assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------- wide operands --
+
+def test_operands_of_two_gib_and_more():
+    """Rows past 2^31 bytes: the last rows' values are where they belong."""
+    T, K, N, E, B = (1 << 17) + 70, 8192, 64, 2, 256
+    g = torch.Generator(device=dev()).manual_seed(1)
+    X = torch.randn((T, K), generator=g, device=dev(), dtype=torch.bfloat16)
+    W, dY = normal((E, N, K), 2, 0.05).to(dev()), normal((T, N), 3).to(dev())
+    ids = torch.randint(0, E, (T, 1), generator=g, device=dev(), dtype=torch.int32)
+    p = w4.moe_align_block_size(ids, E, B)
+    Y = w4.w4_bf16_moe_gemm(X, W, *p, T, 1, B, 1)
+    rows = torch.cat([torch.arange(0, 40), torch.arange(T - 200, T)]).to(dev())
+    e = ids[rows, 0].long()
+    x = X[rows].double()
+    want = torch.einsum("rk,rnk->rn", x, W.double()[e])
+    mag = torch.einsum("rk,rnk->rn", x.abs(), W.double().abs()[e])
+    check_large(Y[rows], want, mag, K, "Y")
+    cols = slice(0, 64)
+    dW = w4.w4_bf16_moe_wgrad(dY, X, *p, E, T, 1, B, 1, 1)
+    C = w4.w4_bf16_gemm_tn(dY, X)
+    X8, SX = w4.w8_quantize_rows(X)
+    C8 = w4.w4_bf16_gemm_tn(dY, X8, SB=SX)
+    xc, d = X[:, cols].double(), dY.double()
+    for i in range(E):
+        f = (ids[:, 0] == i)[:, None]
+        check_large(dW[i][:, cols], (d * f).t() @ xc, (d * f).abs().t() @ xc.abs(), T, f"dW[{i}]")
+    check_large(C[:, cols], d.t() @ xc, d.abs().t() @ xc.abs(), T, "C")
+    x8 = stored(X8[:, :128].contiguous(), SX[:, :1].contiguous())[:, cols]
+    check_large(C8[:, cols], d.t() @ x8, d.abs().t() @ x8.abs(), T, "C from codes")
