@@ -242,6 +242,21 @@ constexpr int workgroups_per_cu(int mi, int ni) {
   return mi * ni <= 4 ? 4 : mi * ni <= 8 ? 3 : mi * ni <= 16 ? 2 : 1;
 }
 
+// Order of the large tiles of a product by rows: groups of rows x cols tiles, `across`
+// of them side by side, `groups` in all; what an XCD holds at a time (32) where there
+// is enough, else about four groups for each.
+struct Order {
+  int rows, cols;
+  int64_t across, groups;
+};
+__host__ __device__ __forceinline__ Order order(int64_t mt, int64_t nt) {
+  const int rows = mt < 8 ? (int)mt : 8;
+  const int64_t share = mt * nt / (32 * rows);
+  const int cols = share < 1 ? 1 : share < 4 ? (int)share : 4;
+  const int64_t across = (nt + cols - 1) / cols;
+  return {rows, cols, across, (mt + rows - 1) / rows * across};
+}
+
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
@@ -354,26 +369,44 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
   const int wm = wave >> 1, wn = wave & 1;
   const int r16 = lane & 15, h = lane >> 4;
 
-  // tile order: XCD x (workgroups round-robin over 8) walks a contiguous range
-  // of tiles in groups of 8 row blocks, which share operands in its L2.  An expert's
-  // tiles of a weight gradient are spread over all XCDs, since hot experts would
-  // keep one busy.
-  int64_t cap = 0, M = j.M;
+  // tile order (workgroups go round-robin over 8 XCDs): the tiles that an XCD runs
+  // at a time are groups of 8 row blocks by some columns, which share operands in
+  // its L2.
+  int64_t cap = 0, M = j.M, m0, n0, e = 0;
   if constexpr (G != kDense) cap = (j.g.P + (int64_t)j.g.E * (j.g.B - 1) + j.g.B - 1) / j.g.B * j.g.B;
-  if constexpr (G == kRows) M = min(M, min(cap, (int64_t)j.g.ntpp[0]));
+  constexpr bool DEALT = G == kRows && workgroups_per_cu(MI, NI) == 1;
+  if constexpr (G == kRows && !DEALT) M = min(M, min(cap, (int64_t)j.g.ntpp[0]));
   const int64_t mt = (M + BM - 1) / BM, nt = (j.N + BN - 1) / BN, tiles = mt * nt;
-  const int64_t per = max((tiles + 7) / 8, (int64_t)1);
-  int64_t at = blockIdx.x / 8, e = 0, chunk = blockIdx.x % 8;
-  const int64_t part = at / per;                   // which sum, or part of one
-  at -= part * per;
-  if constexpr (G == kSums) e = part / j.splits;
-  const int split = (int)(part - e * j.splits);
-  chunk = (chunk + 8 - part * tiles % 8) % 8;      // few tiles: another XCD for the next one
-  const int64_t t = chunk * per + at;
-  if (t >= tiles || split >= j.splits) return;
-  const int64_t band = t / (8 * nt), in_band = t - band * 8 * nt;
-  const int gm = (int)min((int64_t)8, mt - band * 8);
-  const int64_t m0 = (band * 8 + in_band % gm) * BM, n0 = in_band / gm * BN;
+  int split = 0;
+  if constexpr (DEALT) {
+    // such groups are dealt to the XCDs in turn, over all the blocks that there may
+    // be: how many there are need not be known to begin, and the last ones, which are
+    // not there, are missed by every XCD alike
+    const Order o = order(mt, nt);
+    const int64_t i = blockIdx.x / 8, round = i / (o.rows * o.cols);
+    const int w = (int)(i - round * o.rows * o.cols);
+    const int64_t group = round * 8 + blockIdx.x % 8, band = group / o.across;
+    const int64_t row = band * o.rows + w % o.rows, col = (group - band * o.across) * o.cols + w / o.rows;
+    if (row >= mt || col >= nt) return;            // (with it the groups past the last)
+    m0 = row * BM;
+    n0 = col * BN;
+  } else {
+    // XCD x walks a contiguous range; an expert's tiles are spread over all XCDs,
+    // since hot experts would keep one busy
+    const int64_t per = max((tiles + 7) / 8, (int64_t)1);
+    int64_t at = blockIdx.x / 8, chunk = blockIdx.x % 8;
+    const int64_t part = at / per;                 // which sum, or part of one
+    at -= part * per;
+    if constexpr (G == kSums) e = part / j.splits;
+    split = (int)(part - e * j.splits);
+    chunk = (chunk + 8 - part * tiles % 8) % 8;    // few tiles: another XCD for the next one
+    const int64_t t = chunk * per + at;
+    if (t >= tiles || split >= j.splits) return;
+    const int64_t band = t / (8 * nt), in_band = t - band * 8 * nt;
+    const int gm = (int)min((int64_t)8, mt - band * 8);
+    m0 = (band * 8 + in_band % gm) * BM;
+    n0 = in_band / gm * BN;
+  }
 
   int sum = (int)j.K, slots = 0;                   // length of the sum; kSums: with padding
   const int32_t* ids = j.g.sorted_ids;
@@ -382,8 +415,9 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
   constexpr int BB = C8 ? 1 : 2;                   // bytes of an element of B
   uint16_t* C = j.C;
   if constexpr (G == kRows) {
+    const int total = j.g.ntpp[0];
     e = j.g.expert_ids[m0 / j.g.B];
-    if (e < 0 || e >= j.g.E || (uint32_t)ids[m0] >= (uint32_t)j.g.P) return;
+    if (m0 >= total || e < 0 || e >= j.g.E || (uint32_t)ids[m0] >= (uint32_t)j.g.P) return;
     B += e * j.N * j.K * BB;
   }
   if constexpr (G == kSums) {
@@ -782,9 +816,14 @@ hipError_t run_simple(const Job& j, hipStream_t st) {
 
 template <int MI, int NI, Group G, bool TA, bool TB, bool C8>
 hipError_t run_tile(const Job& j, hipStream_t st) {
-  const int64_t per = (tiles_of(j.M, j.N, 32 * MI, 32 * NI) + 7) / 8;
-  const int64_t sums = (G == kSums ? j.g.E : 1) * (int64_t)j.splits;
-  hipLaunchKernelGGL((k_bf16_tile<MI, NI, G, TA, TB, C8>), dim3((unsigned)(8 * per * sums)),
+  int64_t per;                                     // workgroups of an XCD
+  if constexpr (G == kRows && workgroups_per_cu(MI, NI) == 1) {
+    const Order o = order((j.M + 32 * MI - 1) / (32 * MI), (j.N + 32 * NI - 1) / (32 * NI));
+    per = (o.groups + 7) / 8 * o.rows * o.cols;
+  } else {
+    per = (tiles_of(j.M, j.N, 32 * MI, 32 * NI) + 7) / 8 * (G == kSums ? j.g.E : 1) * j.splits;
+  }
+  hipLaunchKernelGGL((k_bf16_tile<MI, NI, G, TA, TB, C8>), dim3((unsigned)(8 * per)),
                      dim3(256), 0, st, j, divisor(j.a_div), divisor(j.b_div));
   return hipGetLastError();
 }
@@ -804,8 +843,8 @@ struct Kind {
 constexpr Kind kKinds[] = {
     {64, 64, 4, {1.1f, 1.2f}, {0.20f, 0.23f}, {2.2f, 2.3f}, {0.30f, 0.33f}},
     {64, 128, 3, {1.45f, 1.5f}, {0.33f, 0.38f}, {2.3f, 2.6f}, {0.33f, 0.37f}},
-    {128, 128, 2, {2.3f, 2.3f}, {0.60f, 0.56f}, {3.6f, 3.8f}, {0.50f, 0.62f}},
-    {256, 256, 1, {9.3f, 9.3f}, {1.45f, 1.58f}, {9.3f, 9.3f}, {1.45f, 1.58f}},
+    {128, 128, 2, {2.3f, 2.1f}, {0.60f, 0.56f}, {3.6f, 3.8f}, {0.50f, 0.62f}},
+    {256, 256, 1, {9.3f, 9.8f}, {1.45f, 1.58f}, {9.3f, 9.8f}, {1.45f, 1.58f}},
 };
 constexpr int kKindCount = 4;
 
@@ -899,7 +938,7 @@ hipError_t run_sums(Job j, const Choice& c, hipStream_t st) {
 
 // (64 x 64 tiles are the most workgroups; parts are for few)
 int64_t bf16_moe_threads(int64_t P, int32_t E, int64_t N, int64_t K, int32_t B) {
-  return (tiles_of(moe_cap(P, E, B), N, 64, 64) + 8) * 256;
+  return (tiles_of(moe_cap(P, E, B), N, 64, 64) + 8 * 32) * 256;
 }
 int64_t bf16_wgrad_threads(int32_t E, int64_t N, int64_t K) {
   return E * (tiles_of(N, K, 64, 64) + 8) * 256;
