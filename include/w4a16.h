@@ -702,7 +702,15 @@ int32_t w4_bf16_pick_block_size(int64_t T, int32_t k, int32_t E);
  * X bf16 [(T*k) / x_row_div, K], W bf16 [E, N, K] or [E, K, N], both 16-byte
  * aligned; Y bf16 [T*k, N], 2-byte aligned.  K % 8 == 0, and N % 8 == 0 where
  * transposed; N, K >= 1; x_row_div in {1, k} (W4_ERR_SHAPE).  T == 0 is a no-op.
+ * workspace: fp32 [w4_bf16_moe_gemm_workspace(T, k, E, N, K, B)], 16-byte aligned, of
+ * any content, written and read by the call's two launches (calls that share one must
+ * not overlap in time); or NULL.  With it few results of long sums are computed in
+ * parts, faster, whose order of addition differs from the call's without.
+ *
+ * w4_bf16_moe_gemm_workspace -- its size in fp32 values; 0: no use for one; -1 on sizes
+ * that the call refuses.
  */
+int64_t w4_bf16_moe_gemm_workspace(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B);
 int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted_token_ids,
                      const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
                      uint16_t* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K,

@@ -306,6 +306,8 @@ def w4_moe_align_capacity(T, k, E, B):
 def moe_align_block_size(topk_ids, E, B, sorted_token_ids=None, expert_ids=None,
                          num_tokens_post_padded=None):
     """int32 topk_ids [T, k] -> (sorted_token_ids [cap], expert_ids [cap/B], ntpp [1])."""
+    if sorted_token_ids is None and expert_ids is None and num_tokens_post_padded is None:
+        return _align_new(topk_ids, E, B)
     _need(topk_ids, "topk_ids", torch.int32, 2)
     T, k = topk_ids.shape
     cap = w4_moe_align_capacity(T, k, E, B)
@@ -1023,6 +1025,21 @@ def w4_moe_route_scored_bwd(logits, topk_ids, topk_weights, grad_weights, sigmoi
 
 
 # ------------------------------------------------- training the routed experts --
+
+def _align_new(topk_ids, E, B):
+    """``moe_align_block_size`` into one new allocation."""
+    device = _in(topk_ids, "topk_ids", _I32, 2)
+    T, k = topk_ids.shape
+    if k < 1 or E < 1 or B < 1:
+        raise ValueError("invalid T, k, E or B")
+    blocks = (T * k + E * (B - 1) + B - 1) // B
+    cap = blocks * B
+    plan = topk_ids.new_empty(cap + blocks + 1)
+    at = plan.data_ptr()
+    _call("moe_align_block_size", device, topk_ids.data_ptr(), T, k, E, B, at, at + 4 * cap,
+          at + 4 * (cap + blocks))
+    return plan.split((cap, blocks, 1))
+
 
 def w4_bf16_pick_block_size(T, k, E):
     return int(_lib.load().w4_bf16_pick_block_size(T, k, E))

@@ -48,11 +48,11 @@ from dataclasses import dataclass
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (_in, _shape, moe_align_block_size, w4_bf16_moe_gemm, w4_bf16_moe_wgrad,
-               w4_bf16_pick_block_size, w4_dequant, w4_moe_align_capacity, w4_moe_combine_workspace_words,
+from . import (_call, _in, _ptr, _shape, moe_align_block_size, w4_bf16_moe_gemm_workspace,
+               w4_bf16_moe_wgrad_workspace, w4_bf16_pick_block_size, w4_moe_align_capacity, w4_moe_combine_workspace_words,
                w4_moe_route, w4_moe_sum, w4a16_moe_gemm_combine,
                w4_pick_block_size, w4_quantize_pack, w4_quantize_pack_asym, w4_repack,
-               w4_repack_groups, w4_silu_mul, w4_silu_mul_bwd, w4a16_moe_gemm, w4a16_moe_gemm_asym, w4a16_moe_gemm_swiglu,
+               w4_repack_groups, w4_silu_mul, w4a16_moe_gemm, w4a16_moe_gemm_asym, w4a16_moe_gemm_swiglu,
                w4a16_moe_gemm_swiglu_asym, w4a16_moe_gemm_swiglu_tiled, w4a16_moe_gemm_tiled,
                w4_moe_route_scored, w4_moe_route_scored_bwd, w8_pick_block_size,
                w8_quantize_blocks, w8_quantize_rows, w8_scale_cols, w8_silu_mul_quantize,
@@ -415,35 +415,52 @@ def moe_layer_w8(X, logits, k, gate_up, down, sigmoid=False, bias=None, groups=1
 
 class RoutedExperts(torch.autograd.Function):
     """The routed layer behind ``moe_train``: out [T, H], with gradients to X,
-    the top-k weights and both stacks of experts."""
+    the top-k weights and both stacks of experts.
+
+    A step on few tokens takes the host longer than the GPU, so the entry points
+    are called with the sizes that ``moe_train`` has checked once."""
 
     @staticmethod
     def forward(ctx, X, weights, gate_up, down, topk_ids, int4, checkpoint, B, grad):
-        with _on_device_of(X):
-            T, H = X.shape
-            k = topk_ids.shape[1]
-            E, I = gate_up.shape[0], down.shape[2]
-            plan = moe_align_block_size(topk_ids, E, B)
+        device = X.get_device()
+        T, H = X.shape
+        k = topk_ids.shape[1]
+        E, I = gate_up.shape[0], down.shape[2]
+        P = T * k
+        plan = moe_align_block_size(topk_ids, E, B)
+        at = _plan_at(plan)
 
-            def product(x, w, div):
-                if int4:
-                    return w4a16_moe_gemm(x, *w, *plan, T, k, B, div), w
-                return w4_bf16_moe_gemm(x, w, *plan, T, k, B, div), (w, None)
-            H1, up = product(X, _int4_codes(gate_up) if int4 else gate_up, k)
-            H2, dn = product(w4_silu_mul(H1), _int4_codes(down) if int4 else down, 1)
-            out = w4_moe_sum(H2, weights, T, k)
-            need_x, need_w, need_up, need_dn = (n and grad for n in ctx.needs_input_grad[:4])
-            inner = need_x or need_up
-            XS = HS = None
-            if checkpoint:
-                if need_up:
-                    X, XS = w8_quantize_rows(X)
-                if inner or need_w or need_dn:
-                    H1, HS = w8_quantize_rows(H1)
-            ctx.save_for_backward(X if need_up else None, XS, H1 if inner or need_w or need_dn else None,
-                                  HS, weights, *(up if need_x else (None, None)),
-                                  *(dn if inner or need_w else (None, None)), *plan)
-            ctx.sizes = T, k, E, H, I, B
+        def product(x, W, N, K, div):
+            """(rows of the pairs, the weights as the backward wants them)"""
+            y = x.new_empty((P, N))
+            if not int4:
+                _bf16_product(device, x, W, at, y, T, k, E, N, K, B, div, 0)
+                return y, (W, None)
+            Wq = x.new_empty((E * N, K // 8), dtype=torch.int32)
+            S = x.new_empty((E * N, K // 32))
+            _call("w4_quantize_pack", device, W.data_ptr(), E * N, K, Wq.data_ptr(), S.data_ptr())
+            _call("w4a16_moe_gemm", device, x.data_ptr(), Wq.data_ptr(), S.data_ptr(), *at, None, y.data_ptr(),
+                  T, k, E, N, K, B, div)
+            return y, (Wq, S)
+        H1, up = product(X, gate_up, 2 * I, H, k)
+        A = X.new_empty((P, I))
+        _call("w4_silu_mul", device, H1.data_ptr(), A.data_ptr(), P, I)
+        H2, dn = product(A, down, H, I, 1)
+        out = torch.empty_like(X)
+        _call("w4_moe_sum", device, H2.data_ptr(), weights.data_ptr(), out.data_ptr(), T, k, H)
+        # needs_input_grad goes by the inputs alone, also under torch.no_grad()
+        need_x, need_w, need_up, need_dn = (n and grad for n in ctx.needs_input_grad[:4])
+        inner = need_x or need_up
+        XS = HS = None
+        if checkpoint:
+            if need_up:
+                X, XS = w8_quantize_rows(X)
+            if inner or need_w or need_dn:
+                H1, HS = w8_quantize_rows(H1)
+        ctx.save_for_backward(X if need_up else None, XS, H1 if inner or need_w or need_dn else None, HS,
+                              weights, *(up if need_x else (None, None)),
+                              *(dn if inner or need_w else (None, None)), *plan)
+        ctx.sizes = T, k, E, H, I, B
         return out
 
     @staticmethod
@@ -452,31 +469,58 @@ class RoutedExperts(torch.autograd.Function):
         X, XS, H1, HS, weights, up, up_s, dn, dn_s, *plan = ctx.saved_tensors
         T, k, E, H, I, B = ctx.sizes
         need_x, need_w, need_up, need_dn = ctx.needs_input_grad[:4]
+        P, at = T * k, _plan_at(plan)
+        dO = grad_out.to(torch.bfloat16).contiguous()
+        device = dO.get_device()
+
+        def back(dy, W, S, N, K, div):
+            """dy W: rows of the pairs, W the weights or their codes"""
+            if S is not None:
+                w = dy.new_empty((E, K, N))
+                _call("w4_dequant", device, W.data_ptr(), S.data_ptr(), E * K, N, w.data_ptr())
+                W = w
+            y = dy.new_empty((P, N))
+            _bf16_product(device, dy, W, at, y, T, k, E, N, K, B, div, 1)
+            return y
+
+        def outer(dy, x, scales, N, K, dy_div, x_div):
+            dW = dy.new_empty((E, N, K))
+            size = w4_bf16_moe_wgrad_workspace(T, k, E, N, K)
+            parts = dy.new_empty(size, dtype=torch.float32) if size else None
+            _call("w4_bf16_moe_wgrad", device, dy.data_ptr(), x.data_ptr(), _ptr(scales), *at, dW.data_ptr(),
+                  T, k, E, N, K, B, dy_div, x_div, _ptr(parts))
+            return dW
         dX = dw = d_up = d_dn = None
-        with _on_device_of(grad_out):
-            dO = grad_out.to(torch.bfloat16).contiguous()
-            if need_x or need_up or need_w:
-                Wd = dn if dn_s is None else w4_dequant(dn.view(E * H, I // 8), dn_s.view(E * H, I // 32))
-                G = w4_bf16_moe_gemm(dO, Wd.view(E, H, I), *plan, T, k, B, k, transposed=True)
-            else:                                  # only the activation is needed
-                G = H1.new_zeros((T * k, I), dtype=torch.bfloat16)
-            dH1, A, dw = w4_silu_mul_bwd(H1, G, weights, HS)
-            if need_dn:
-                d_dn = w4_bf16_moe_wgrad(dO, A, *plan, E, T, k, B, k, 1)
-            if need_up:
-                d_up = w4_bf16_moe_wgrad(dH1, X, *plan, E, T, k, B, 1, k, XS)
-            if need_x:
-                Wu = up if up_s is None else w4_dequant(up.view(E * 2 * I, H // 8), up_s.view(E * 2 * I, H // 32))
-                dXp = w4_bf16_moe_gemm(dH1, Wu.view(E, 2 * I, H), *plan, T, k, B, 1, transposed=True)
-                dX = w4_moe_sum(dXp, None, T, k)
-        return (dX, dw.view(T, k) if need_w else None, d_up, d_dn, *(None,) * 5)
+        if need_x or need_up or need_w:
+            G = back(dO, dn, dn_s, I, H, k)
+        else:                                      # only the activation is needed
+            G = dO.new_zeros((P, I))
+        dH1, A = dO.new_empty((P, 2 * I)), dO.new_empty((P, I)) if need_dn else None
+        if need_w:
+            dw = weights.new_empty((T, k))
+        _call("w4_silu_mul_bwd", device, H1.data_ptr(), _ptr(HS), G.data_ptr(), weights.data_ptr(), P, I,
+              dH1.data_ptr(), _ptr(A), _ptr(dw))
+        if need_dn:
+            d_dn = outer(dO, A, None, H, I, k, 1)
+        if need_up:
+            d_up = outer(dH1, X, XS, 2 * I, H, 1, k)
+        if need_x:
+            dXp = back(dH1, up, up_s, H, 2 * I, 1)
+            dX = dO.new_empty((T, H))
+            _call("w4_moe_sum", device, dXp.data_ptr(), None, dX.data_ptr(), T, k, H)
+        return dX, dw, d_up, d_dn, None, None, None, None, None
 
 
-def _int4_codes(W):
-    """Packed codes and scales of stacked experts bf16 [E, N, K]."""
-    E, N, K = W.shape
-    Wq, S = w4_quantize_pack(W.view(E * N, K))
-    return Wq.view(E, N, K // 8), S.view(E, N, K // 32)
+def _plan_at(plan):
+    return tuple(t.data_ptr() for t in plan)
+
+
+def _bf16_product(device, x, W, at, y, T, k, E, N, K, B, div, transposed):
+    """``w4_bf16_moe_gemm`` with its workspace."""
+    size = w4_bf16_moe_gemm_workspace(T, k, E, N, K, B)
+    parts = x.new_empty(size, dtype=torch.float32) if size else None
+    _call("w4_bf16_moe_gemm", device, x.data_ptr(), W.data_ptr(), *at, y.data_ptr(), T, k, E, N, K, B, div,
+          transposed, _ptr(parts))
 
 
 def moe_train(X, topk_ids, topk_weights, gate_up, down, int4=False, checkpoint=False, B=None):
