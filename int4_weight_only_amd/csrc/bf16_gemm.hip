@@ -19,6 +19,16 @@ namespace {
 // Which dimension the expert's pairs are.
 enum Group { kDense, kRows, kSums };
 
+// f / d for f < 2^31, with m = floor((2^32 - 1) / d): the high product is the
+// quotient or one less.
+struct Div {
+  uint32_t d, m;
+};
+__device__ __forceinline__ int div_by(uint32_t f, Div v) {
+  const uint32_t q = __umulhi(f, v.m);
+  return (int)(f - q * v.d >= v.d ? q + 1 : q);
+}
+
 struct Job {
   const uint16_t* A;        // [*, K] rows summed along, or (TA) [*, M] with the sum down the rows
   Bf16Rows B;
@@ -28,6 +38,12 @@ struct Job {
   int32_t a_div, b_div;     // pairs per row of A, of B
   float* part;              // splits > 1: that many partial sums of each C, fp32, one after another
   int32_t splits;
+  int32_t blocks;           // blocks that there may be: cap / B
+  Div by_a, by_b;           // a_div, b_div
+  Div by_block;             // B
+  // a tile kernel's: columns of tiles (8 of them a band), tiles of an XCD for a sum
+  int32_t mt, nt, per;
+  Div by_band, by_per, by_splits;
 };
 
 
@@ -49,16 +65,16 @@ __device__ __forceinline__ int first_not(int n, Below below) {
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// The slots of expert e: [first, first + count), the last block's rest padding.
-// Both ends of its run of blocks are searched for together (the loads of a pass
-// depend on the pass before, about 0.7 us each).
-struct Segment {
-  int first, count, blocks;
+// The blocks of expert e: [first, last).  Both ends are searched for together (the
+// loads of a pass depend on the pass before, about 0.7 us each).
+struct Blocks {
+  int first, last;
 };
-__device__ __forceinline__ Segment segment(const Bf16Plan& g, int64_t cap, int e) {
+__device__ __forceinline__ Blocks blocks_of(const Job& j, int e) {
+  const Bf16Plan& g = j.g;
   const int lane = threadIdx.x & 63;
   const int total = g.ntpp[0];
-  const int all = (int)(cap / g.B);
+  const int all = j.blocks;
   auto key = [&](int b) { return (uint32_t)g.expert_ids[b]; };     // -1 past the end: last
   int lo, hi;
   if (all <= 64 * 64) {
@@ -77,13 +93,26 @@ __device__ __forceinline__ Segment segment(const Bf16Plan& g, int64_t cap, int e
     lo = first_not(all, [&](int b) { return key(b) < (uint32_t)e; });
     hi = first_not(all, [&](int b) { return key(b) <= (uint32_t)e; });
   }
-  hi = __builtin_amdgcn_readfirstlane(min(hi, total / g.B));
+  hi = __builtin_amdgcn_readfirstlane(min(hi, div_by((uint32_t)max(total, 0), j.by_block)));
   lo = __builtin_amdgcn_readfirstlane(min(lo, hi));
-  if (lo == hi) return {0, 0, 0};
-  int tail = 0;
-  for (int i = 0; i < g.B; i += 64)
-    tail += __popcll(__ballot((uint32_t)g.sorted_ids[(hi - 1) * g.B + i + lane] < (uint32_t)g.P));
-  return {lo * g.B, (hi - 1 - lo) * g.B + __builtin_amdgcn_readfirstlane(tail), hi - lo};
+  return {lo, hi};
+}
+
+// Pairs in an expert's last block: a prefix of its slots.
+__device__ __forceinline__ int pairs_of_block(const Bf16Plan& g, int block) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  for (int i = 0; i < g.B; i += 256) {
+    uint32_t f[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int at = i + 64 * q + lane;
+      f[q] = at < g.B ? (uint32_t)g.sorted_ids[block * g.B + at] : ~0u;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) n += __popcll(__ballot(f[q] < (uint32_t)g.P));
+  }
+  return __builtin_amdgcn_readfirstlane(n);
 }
 
 // The lower and the upper two of four e4m3 codes times a power of two, as bf16.
@@ -124,7 +153,9 @@ __global__ __launch_bounds__(256) void k_bf16_simple(Job j) {
     tile -= e * mt * nt;
   }
   const int64_t m0 = tile / nt * 64, n0 = tile % nt * 64;
-  Segment seg = {0, 0};
+  struct {
+    int first, count;
+  } seg = {0, 0};
   int64_t steps = (j.K + 31) / 32, cap = 0;
   if constexpr (G != kDense) cap = (j.g.P + (int64_t)j.g.E * (j.g.B - 1) + j.g.B - 1) / j.g.B * j.g.B;
   if constexpr (G == kRows) {
@@ -134,7 +165,9 @@ __global__ __launch_bounds__(256) void k_bf16_simple(Job j) {
     j.B.p = (const uint16_t*)j.B.p + e * j.N * j.K;
   }
   if constexpr (G == kSums) {
-    seg = segment(j.g, cap, (int)e);
+    const Blocks b = blocks_of(j, (int)e);
+    seg.first = b.first * j.g.B;
+    if (b.last > b.first) seg.count = (b.last - 1 - b.first) * j.g.B + pairs_of_block(j.g, b.last - 1);
     steps = (seg.count + 31) / 32;
     j.C += e * j.M * j.N;
   }
@@ -246,14 +279,12 @@ constexpr int workgroups_per_cu(int mi, int ni) {
 // of them side by side, `groups` in all; what an XCD holds at a time (32) where there
 // is enough, else about four groups for each.
 struct Order {
-  int rows, cols;
-  int64_t across, groups;
+  int rows, cols, across, groups;
 };
-__host__ __device__ __forceinline__ Order order(int64_t mt, int64_t nt) {
-  const int rows = mt < 8 ? (int)mt : 8;
-  const int64_t share = mt * nt / (32 * rows);
-  const int cols = share < 1 ? 1 : share < 4 ? (int)share : 4;
-  const int64_t across = (nt + cols - 1) / cols;
+__host__ __device__ __forceinline__ Order order(int mt, int nt) {
+  const int rows = mt < 8 ? mt : 8, share = mt * nt / (32 * rows);
+  const int cols = share < 1 ? 1 : share < 4 ? share : 4;
+  const int across = (nt + cols - 1) / cols;
   return {rows, cols, across, (mt + rows - 1) / rows * across};
 }
 
@@ -303,16 +334,6 @@ __device__ __forceinline__ void store8(uint16_t* row, int64_t n, int64_t N, u32x
     if (n + i < N) row[n + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
 }
 
-// f / d for f < 2^31, with m = floor((2^32 - 1) / d): the high product is the
-// quotient or one less.
-struct Div {
-  uint32_t d, m;
-};
-__device__ __forceinline__ uint32_t div_by(uint32_t f, Div v) {
-  const uint32_t q = __umulhi(f, v.m);
-  return f - q * v.d >= v.d ? q + 1 : q;
-}
-
 // Swizzle of a row (of the summed dimension) in units of 32 bytes: the eight
 // rows {0..3, 8..11} (or {4..7, 12..15}) that 32 lanes read together get eight
 // different places in 256 bytes.
@@ -347,7 +368,7 @@ struct Operand {           // 16 rows x 64 of the sum: two MFMA operands
 // two) and go into the stage as bf16 rows would, so that each element is converted
 // once a workgroup and memory sees half the bytes.
 template <int MI, int NI, Group G, bool TA, bool TB, bool C8>
-__global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Job j, Div da, Div db) {
+__global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Job j) {
   constexpr int BM = 32 * MI, BN = 32 * NI;
   constexpr int XA = BM / 32, XB = C8 ? 0 : BN / 32;   // 1 KB loads per wave and stage
   constexpr int XC = C8 ? BN / 64 : 0;             // 16 codes each, and their scales
@@ -372,43 +393,47 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
   // tile order (workgroups go round-robin over 8 XCDs): the tiles that an XCD runs
   // at a time are groups of 8 row blocks by some columns, which share operands in
   // its L2.
-  int64_t cap = 0, M = j.M, m0, n0, e = 0;
-  if constexpr (G != kDense) cap = (j.g.P + (int64_t)j.g.E * (j.g.B - 1) + j.g.B - 1) / j.g.B * j.g.B;
+  // (32-bit arithmetic and divisors prepared by the host: every tile begins with it)
+  const int M = (int)j.M, nt = j.nt;
   constexpr bool DEALT = G == kRows && workgroups_per_cu(MI, NI) == 1;
-  if constexpr (G == kRows && !DEALT) M = min(M, min(cap, (int64_t)j.g.ntpp[0]));
-  const int64_t mt = (M + BM - 1) / BM, nt = (j.N + BN - 1) / BN, tiles = mt * nt;
-  int split = 0;
+  int mt = j.mt, m0, n0, e = 0, split = 0;
   if constexpr (DEALT) {
     // such groups are dealt to the XCDs in turn, over all the blocks that there may
     // be: how many there are need not be known to begin, and the last ones, which are
     // not there, are missed by every XCD alike
     const Order o = order(mt, nt);
-    const int64_t i = blockIdx.x / 8, round = i / (o.rows * o.cols);
-    const int w = (int)(i - round * o.rows * o.cols);
-    const int64_t group = round * 8 + blockIdx.x % 8, band = group / o.across;
-    const int64_t row = band * o.rows + w % o.rows, col = (group - band * o.across) * o.cols + w / o.rows;
+    const int i = blockIdx.x / 8, size = o.rows * o.cols, round = i / size, w = i - round * size;
+    const int group = round * 8 + blockIdx.x % 8, band = group / o.across;
+    const int row = band * o.rows + w % o.rows, col = (group - band * o.across) * o.cols + w / o.rows;
     if (row >= mt || col >= nt) return;            // (with it the groups past the last)
     m0 = row * BM;
     n0 = col * BN;
   } else {
     // XCD x walks a contiguous range; an expert's tiles are spread over all XCDs,
     // since hot experts would keep one busy
-    const int64_t per = max((tiles + 7) / 8, (int64_t)1);
-    int64_t at = blockIdx.x / 8, chunk = blockIdx.x % 8;
-    const int64_t part = at / per;                 // which sum, or part of one
+    int per = j.per, at = blockIdx.x / 8, chunk = blockIdx.x % 8, part;   // which sum, or part of one
+    if constexpr (G == kRows) {
+      mt = (min(M, j.g.ntpp[0]) + BM - 1) / BM;
+      per = max((mt * nt + 7) / 8, 1);
+      part = at / per;
+    } else {
+      part = div_by((uint32_t)at, j.by_per);
+    }
     at -= part * per;
-    if constexpr (G == kSums) e = part / j.splits;
-    split = (int)(part - e * j.splits);
-    chunk = (chunk + 8 - part * tiles % 8) % 8;    // few tiles: another XCD for the next one
-    const int64_t t = chunk * per + at;
+    if constexpr (G == kSums) e = div_by((uint32_t)part, j.by_splits);
+    split = part - e * j.splits;
+    const int tiles = mt * nt;
+    chunk = (chunk + 8 - (int)((uint32_t)part * (uint32_t)tiles % 8)) % 8;   // few tiles: another XCD for the next one
+    const int t = chunk * per + at;
     if (t >= tiles || split >= j.splits) return;
-    const int64_t band = t / (8 * nt), in_band = t - band * 8 * nt;
-    const int gm = (int)min((int64_t)8, mt - band * 8);
-    m0 = (band * 8 + in_band % gm) * BM;
-    n0 = in_band / gm * BN;
+    const int band = div_by((uint32_t)t, j.by_band), in_band = t - band * 8 * nt;
+    const int gm = min(8, mt - band * 8);
+    const int col = in_band / gm;
+    m0 = (band * 8 + in_band - col * gm) * BM;
+    n0 = col * BN;
   }
 
-  int sum = (int)j.K, slots = 0;                   // length of the sum; kSums: with padding
+  int sum = G == kSums ? 0 : (int)j.K;             // length of the sum
   const int32_t* ids = j.g.sorted_ids;
   const uint16_t* A = j.A;
   const uint8_t* B = (const uint8_t*)j.B.p;
@@ -416,43 +441,57 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
   uint16_t* C = j.C;
   if constexpr (G == kRows) {
     const int total = j.g.ntpp[0];
-    e = j.g.expert_ids[m0 / j.g.B];
+    e = j.g.expert_ids[div_by((uint32_t)m0, j.by_block)];
     if (m0 >= total || e < 0 || e >= j.g.E || (uint32_t)ids[m0] >= (uint32_t)j.g.P) return;
-    B += e * j.N * j.K * BB;
+    B += (int64_t)e * j.N * j.K * BB;
   }
+  __amdgpu_buffer_rsrc_t ir = rsrc(nullptr, 0);
+  // kSums: lane l's pair of a coming step, row l of the 64
+  auto load_id = [&](int step) __attribute__((always_inline)) {
+    return G == kSums ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ir, (step * 64 + lane) * 4, 0, 0) : 0u;
+  };
+  uint32_t f[4] = {0u, 0u, 0u, 0u};                // the pairs of the first steps
   if constexpr (G == kSums) {
-    const Segment seg = segment(j.g, cap, (int)e);
-    ids += seg.first;
-    sum = seg.count;
-    slots = seg.blocks * j.g.B;
-    C += e * M * j.N;
-    if (sum == 0 && j.splits == 1) {               // no pairs: zeros
-      for (int64_t i = threadIdx.x; i < BM * (BN / 8); i += 256) {
-        const int64_t row = m0 + i / (BN / 8), col = n0 + i % (BN / 8) * 8;
-        if (row < M && col < j.N) *(u32x4*)(C + row * j.N + col) = u32x4{0u, 0u, 0u, 0u};
+    const Blocks b = blocks_of(j, e);
+    C += (int64_t)e * M * j.N;
+    if (b.first == b.last) {                       // no pairs: zeros
+      if (j.splits == 1) {
+        for (int i = threadIdx.x; i < BM * (BN / 8); i += 256) {
+          const int row = m0 + i / (BN / 8), col = n0 + i % (BN / 8) * 8;
+          if (row < M && col < j.N) *(u32x4*)(C + (int64_t)row * j.N + col) = u32x4{0u, 0u, 0u, 0u};
+        }
+        return;
       }
-      return;
+    } else {
+      const int start = b.first * j.g.B;
+      ir = rsrc(ids + start, (int64_t)(b.last - b.first) * j.g.B * 4);
+      if constexpr (!PARTS) {                      // on their way beside the last block's
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = load_id(i);
+      }
+      sum = (b.last - 1 - b.first) * j.g.B + pairs_of_block(j.g, b.last - 1);
     }
   }
   const int steps = (sum + 63) / 64;
   // this part's steps, an even number for every part (those past the sum are zeros)
-  const int share = ((steps + j.splits - 1) / j.splits + 1) / 2 * 2;
-  const int first = split * share, last = first + share;
+  const int share = PARTS ? (div_by((uint32_t)(steps + j.splits - 1), j.by_splits) + 1) / 2 * 2 : (steps + 1) / 2 * 2;
+  const int first = PARTS ? split * share : 0, last = first + share;
   const int k_end = min(sum, last * 64);
 
   const int64_t lda = TA ? M : j.K, ldb = TB ? j.N : j.K;     // elements of a row in memory
-  const int64_t rows_a = TA ? (G == kSums ? j.g.P / (int)da.d : sum)
-                            : (G == kRows ? j.g.P / (int)da.d : min((int64_t)BM, M - m0));
-  const int64_t rows_b = TB ? (G == kSums ? j.g.P / (int)db.d : sum) : min((int64_t)BN, j.N - n0);
+  const int pairs = (int)j.g.P;
+  const int64_t rows_a = TA ? (G == kSums ? div_by((uint32_t)pairs, j.by_a) : sum)
+                            : (G == kRows ? div_by((uint32_t)pairs, j.by_a) : min(BM, M - m0));
+  const int64_t rows_b =
+      TB ? (G == kSums ? div_by((uint32_t)pairs, j.by_b) : sum) : min((int64_t)BN, j.N - n0);
   // from the tile's first column (TA, TB) or row on
   const __amdgpu_buffer_rsrc_t ar =
-      rsrc(A + (TA ? m0 : (G == kRows ? 0 : m0 * lda)), (rows_a * lda - (TA ? m0 : 0)) * 2);
+      rsrc(A + (TA ? (int64_t)m0 : (G == kRows ? 0 : m0 * lda)), (rows_a * lda - (TA ? m0 : 0)) * 2);
   const __amdgpu_buffer_rsrc_t br =
       rsrc(B + (TB ? n0 : n0 * ldb) * BB, (rows_b * ldb - (TB ? n0 : 0)) * BB);
   const int64_t lds = w8_cols(j.N);                // C8: scales of a row
   const __amdgpu_buffer_rsrc_t sr =
       rsrc(C8 ? j.B.scales + (n0 >> 7) : nullptr, C8 ? rows_b * lds - (n0 >> 7) : 0);
-  const __amdgpu_buffer_rsrc_t ir = rsrc(ids, (int64_t)slots * 4);
 
   // Load I of a stage.  Rows along the sum: it fills rows 8 I .. 8 I + 7, lane l
   // slot l % 8 of row l / 8, which holds piece (l % 8) ^ ((row / 2) % 8).
@@ -476,7 +515,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
       int64_t row = r < rows_a ? r : -1;
       if constexpr (G == kRows) {
         const uint32_t f = (uint32_t)ids[m0 + r];
-        row = f < (uint32_t)j.g.P ? (int64_t)div_by(f, da) : -1;
+        row = f < (uint32_t)j.g.P ? (int64_t)div_by(f, j.by_a) : -1;
       }
       aoff[i] = row >= 0 ? (uint32_t)(row * lda + 8 * piece(I)) * 2u : kOOB;
     }
@@ -496,15 +535,12 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
   // is needed), turns it into the byte offsets of that row in A and B (kOOB: none),
   // and the loads' lanes take theirs out of a corner of LDS that is the wave's own
   uint32_t arow[G == kSums ? XA : 1], brow[G == kSums ? (C8 ? XC : XB) : 1], srow[C8 ? XC : 1];
-  auto load_id = [&](int step) __attribute__((always_inline)) {
-    return G == kSums ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ir, (step * 64 + lane) * 4, 0, 0) : 0u;
-  };
   auto next_rows = [&](int step, uint32_t f) __attribute__((always_inline)) {
     if constexpr (G == kSums) {
       u32x4* q = rows_[wave];                  // a wave's LDS operations keep their order
       const bool ok = step * 64 + lane < k_end && f < (uint32_t)j.g.P;
-      const uint32_t fb = div_by(f, db);
-      q[lane] = ok ? u32x4{div_by(f, da) * (uint32_t)lda * 2u, fb * (uint32_t)ldb * BB, C8 ? fb * (uint32_t)lds : 0u, 0u}
+      const uint32_t fb = (uint32_t)div_by(f, j.by_b);
+      q[lane] = ok ? u32x4{(uint32_t)div_by(f, j.by_a) * (uint32_t)lda * 2u, fb * (uint32_t)ldb * BB, C8 ? fb * (uint32_t)lds : 0u, 0u}
                    : u32x4{kOOB, kOOB, kOOB, 0u};
 #pragma unroll
       for (int i = 0; i < XA; ++i) {
@@ -698,9 +734,10 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
   };
 
   // the pairs of the first stages together, then the stages
-  uint32_t f[4];
+  if constexpr (PARTS) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = load_id(first + i);
+    for (int i = 0; i < 4; ++i) f[i] = load_id(first + i);
+  }
   auto load_stage = [&](int i, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
     next_rows(first + i, f[i]);
     load_codes(first + i);
@@ -815,16 +852,21 @@ hipError_t run_simple(const Job& j, hipStream_t st) {
 }
 
 template <int MI, int NI, Group G, bool TA, bool TB, bool C8>
-hipError_t run_tile(const Job& j, hipStream_t st) {
-  int64_t per;                                     // workgroups of an XCD
+hipError_t run_tile(Job j, hipStream_t st) {
+  j.mt = (int)((j.M + 32 * MI - 1) / (32 * MI));
+  j.nt = (int)((j.N + 32 * NI - 1) / (32 * NI));
+  j.per = (int)(((int64_t)j.mt * j.nt + 7) / 8);
+  j.by_band = divisor(8 * j.nt);
+  j.by_per = divisor(j.per);
+  j.by_splits = divisor(j.splits);
+  int64_t mine;                                    // workgroups of an XCD
   if constexpr (G == kRows && workgroups_per_cu(MI, NI) == 1) {
-    const Order o = order((j.M + 32 * MI - 1) / (32 * MI), (j.N + 32 * NI - 1) / (32 * NI));
-    per = (o.groups + 7) / 8 * o.rows * o.cols;
+    const Order o = order(j.mt, j.nt);
+    mine = (int64_t)((o.groups + 7) / 8) * o.rows * o.cols;
   } else {
-    per = (tiles_of(j.M, j.N, 32 * MI, 32 * NI) + 7) / 8 * (G == kSums ? j.g.E : 1) * j.splits;
+    mine = (int64_t)j.per * (G == kSums ? j.g.E : 1) * j.splits;
   }
-  hipLaunchKernelGGL((k_bf16_tile<MI, NI, G, TA, TB, C8>), dim3((unsigned)(8 * per)),
-                     dim3(256), 0, st, j, divisor(j.a_div), divisor(j.b_div));
+  hipLaunchKernelGGL((k_bf16_tile<MI, NI, G, TA, TB, C8>), dim3((unsigned)(8 * mine)), dim3(256), 0, st, j);
   return hipGetLastError();
 }
 
@@ -910,6 +952,16 @@ hipError_t run_kind(int kind, const Job& j, hipStream_t st) {
   }
 }
 
+Job job(const uint16_t* A, const Bf16Rows& B, uint16_t* C, int64_t M, int64_t N, int64_t K,
+        const Bf16Plan& g, int32_t a_div, int32_t b_div, float* part) {
+  Job j = {A, B, C, M, N, K, g, a_div, b_div, part, 1};
+  j.by_a = divisor(a_div);
+  j.by_b = divisor(b_div);
+  j.by_block = divisor(std::max(g.B, 1));
+  j.blocks = g.B == 0 ? 0 : (int)(moe_cap(g.P, g.E, g.B) / g.B);
+  return j;
+}
+
 // The tiles address an operand's rows with 32-bit offsets; what they do not cover
 // goes through the simple kernel.
 bool fits(int64_t elems) { return elems * 2 < (int64_t)kOOB; }
@@ -956,7 +1008,7 @@ int64_t bf16_sums_workspace(int64_t groups, int64_t sum, int64_t N, int64_t K) {
 hipError_t launch_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, uint16_t* Y,
                                 const Bf16Plan& plan, int64_t N, int64_t K, int32_t div,
                                 bool transposed, float* workspace, hipStream_t st) {
-  Job j = {X, {W, nullptr}, Y, moe_cap(plan.P, plan.E, plan.B), N, K, plan, div, 1, workspace, 1};
+  Job j = job(X, {W, nullptr}, Y, moe_cap(plan.P, plan.E, plan.B), N, K, plan, div, 1, workspace);
   if (!fits(plan.P / div * K) || !fits(transposed ? N * K : std::min(N, (int64_t)256) * K))
     return transposed ? run_simple<kRows, false, true, false>(j, st)
                       : run_simple<kRows, false, false, false>(j, st);
@@ -970,7 +1022,7 @@ hipError_t launch_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, uint16_t* 
 hipError_t launch_bf16_moe_wgrad(const uint16_t* dY, const Bf16Rows& X, uint16_t* dW,
                                  const Bf16Plan& plan, int64_t N, int64_t K, int32_t dy_div,
                                  int32_t x_div, float* workspace, hipStream_t st) {
-  const Job j = {dY, X, dW, N, K, 0, plan, dy_div, x_div, workspace, 1};
+  const Job j = job(dY, X, dW, N, K, 0, plan, dy_div, x_div, workspace);
   if (!sums_fit(j, plan.P / dy_div, plan.P / x_div))
     return X.scales ? run_simple<kSums, true, true, true>(j, st)
                     : run_simple<kSums, true, true, false>(j, st);
@@ -979,7 +1031,7 @@ hipError_t launch_bf16_moe_wgrad(const uint16_t* dY, const Bf16Rows& X, uint16_t
 
 hipError_t launch_bf16_gemm_tn(const uint16_t* A, const Bf16Rows& B, uint16_t* C, int64_t M,
                                int64_t N, int64_t K, float* workspace, hipStream_t st) {
-  const Job j = {A, B, C, N, K, M, {}, 1, 1, workspace, 1};
+  const Job j = job(A, B, C, N, K, M, {}, 1, 1, workspace);
   if (!sums_fit(j, M, M))
     return B.scales ? run_simple<kDense, true, true, true>(j, st)
                     : run_simple<kDense, true, true, false>(j, st);
