@@ -576,12 +576,13 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
           code[i] = __builtin_amdgcn_raw_buffer_load_b128(br, cok ? (int)(brow[i] + ccol) : (int)kOOB, 0, 0);
           scale[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(srow[i] + cs), 0, 0);
         } else {
-          const int k0 = step * 64;
-          const bool ok = cok && crow(i) < k_end - k0;
+          const int left = k_end - step * 64;
+          const uint32_t from = left > 0 ? (uint32_t)step * 64u : 0u;
+          const bool ok = cok && crow(i) < left;
           code[i] = __builtin_amdgcn_raw_buffer_load_b128(
-              br, ok ? (int)(crow(i) * (uint32_t)ldb + ccol) : (int)kOOB, (int)((uint32_t)k0 * (uint32_t)ldb), 0);
+              br, ok ? (int)(crow(i) * (uint32_t)ldb + ccol) : (int)kOOB, (int)(from * (uint32_t)ldb), 0);
           scale[i] = __builtin_amdgcn_raw_buffer_load_b8(
-              sr, ok ? (int)(crow(i) * (uint32_t)lds + cs) : (int)kOOB, (int)((uint32_t)k0 * (uint32_t)lds), 0);
+              sr, ok ? (int)(crow(i) * (uint32_t)lds + cs) : (int)kOOB, (int)(from * (uint32_t)lds), 0);
         }
       }
     }
@@ -601,24 +602,25 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
   };
   // load i of a wave's XA + XB of a stage
   auto load_one = [&](int i, int step, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
-    const int k0 = step * 64, left = k_end - k0;   // what lies past the end reads zero
+    const int k0 = step * 64, left = k_end - k0;   // what lies past the end reads zero,
+    const uint32_t from = left > 0 ? (uint32_t)k0 * 2u : 0u;       // at offsets inside 32 bits
     if (i < XA) {
       const int I = wave * XA + i;
       if constexpr (G == kSums) {
         load_lds16(ar, sa + I * 1024, aoff[i] != kOOB ? arow[i] + aoff[i] : kOOB, 0);
       } else if constexpr (TA) {
-        load_lds16(ar, sa + I * 1024, trow(I, LRA) < left ? aoff[i] : kOOB, (uint32_t)k0 * (uint32_t)lda * 2u);
+        load_lds16(ar, sa + I * 1024, trow(I, LRA) < left ? aoff[i] : kOOB, from * (uint32_t)lda);
       } else {
-        load_lds16(ar, sa + I * 1024, 8 * piece(I) < left ? aoff[i] : kOOB, (uint32_t)k0 * 2u);
+        load_lds16(ar, sa + I * 1024, 8 * piece(I) < left ? aoff[i] : kOOB, from);
       }
     } else {
       const int b = i - XA, I = wave * XB + b;
       if constexpr (G == kSums) {
         load_lds16(br, sb + I * 1024, boff[b] != kOOB ? brow[b] + boff[b] : kOOB, 0);
       } else if constexpr (TB) {
-        load_lds16(br, sb + I * 1024, trow(I, LRB) < left ? boff[b] : kOOB, (uint32_t)k0 * (uint32_t)ldb * 2u);
+        load_lds16(br, sb + I * 1024, trow(I, LRB) < left ? boff[b] : kOOB, from * (uint32_t)ldb);
       } else {
-        load_lds16(br, sb + I * 1024, 8 * piece(I) < left ? boff[b] : kOOB, (uint32_t)k0 * 2u);
+        load_lds16(br, sb + I * 1024, 8 * piece(I) < left ? boff[b] : kOOB, from);
       }
     }
   };
