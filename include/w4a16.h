@@ -727,7 +727,7 @@ int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted
  * 16-byte aligned, SX 4-byte.  N % 8 == 0, K % 8 == 0 (16 with SX), both >= 1;
  * dy_row_div and x_row_div in {1, k} (W4_ERR_SHAPE).  T == 0 writes zeros.
  * workspace: fp32 [w4_bf16_moe_wgrad_workspace(T, k, E, N, K)] or NULL, as
- * w4_bf16_moe_gemm's.
+ * w4_bf16_moe_gemm's.  T*k + E*B <= 2^28 (W4_ERR_UNSUPPORTED).
  */
 int64_t w4_bf16_moe_wgrad_workspace(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K);
 int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,

@@ -787,6 +787,8 @@ int w4_moe_route_scored_bwd(const float* logits, const int32_t* topk_ids,
 namespace {
 
 constexpr int64_t kBf16MaxCols = (int64_t)1 << 22;
+// slots of an expert's pairs that the sums reach with 32-bit byte offsets
+constexpr int64_t kBf16MaxSumSlots = (int64_t)1 << 28;
 
 // Sizes and alignment arrays shared by the grouped bf16 products; W4_OK or an
 // error status.
@@ -820,7 +822,8 @@ int32_t w4_bf16_pick_block_size(int64_t T, int32_t k, int32_t E) {
 
 int64_t w4_bf16_moe_gemm_workspace(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B) {
   if (T < 0 || k < 1 || E < 1 || N < 1 || K < 1 || B < 64 || B % 64 != 0 || T > kMaxI32 ||
-      N > kBf16MaxCols || K > kBf16MaxCols || T * k + (int64_t)E * B >= kMaxI32)
+      N > kBf16MaxCols || K > kBf16MaxCols || E > 1024 || B > 1024 ||
+      T * k + (int64_t)E * B >= kMaxI32)
     return -1;
   return T == 0 ? 0 : w4::bf16_moe_workspace(T * k, E, N, K, B);
 }
@@ -857,7 +860,8 @@ int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,
   if ((dy_row_div != 1 && dy_row_div != k) || (x_row_div != 1 && x_row_div != k) || N % 8 != 0 ||
       (SX && K % 16 != 0))
     return W4_ERR_SHAPE;
-  if (v == W4_ERR_UNSUPPORTED || w4::bf16_wgrad_threads(E, N, K) >= kMaxGrid)
+  if (v == W4_ERR_UNSUPPORTED || T * k + (int64_t)E * B > kBf16MaxSumSlots ||
+      w4::bf16_wgrad_threads(E, N, K) >= kMaxGrid)
     return W4_ERR_UNSUPPORTED;
   if (v != W4_OK) return v;
   if (!dW || (T > 0 && (!dY || !X))) return W4_ERR_NULL;
@@ -871,7 +875,7 @@ int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,
 
 int64_t w4_bf16_moe_wgrad_workspace(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K) {
   if (T < 0 || k < 1 || E < 1 || N < 1 || K < 1 || T > kMaxI32 || N > kBf16MaxCols ||
-      K > kBf16MaxCols || T * k > kMaxI32 || E * (N * K) > kMaxElems)
+      K > kBf16MaxCols || E > 1024 || T * k > kBf16MaxSumSlots || E * (N * K) > kMaxElems)
     return -1;
   return w4::bf16_sums_workspace(E, T * k / E, N, K);
 }

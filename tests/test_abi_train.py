@@ -66,6 +66,10 @@ def test_wgrad_refusals(lib):
         assert f(lib, **{name: A4}) == MISALIGNED
     assert f(lib, SX=A2) == f(lib, ws=A4) == MISALIGNED
     assert f(lib, T=0, dW=None) == NULL
+    # slots past 32-bit byte offsets, which the rows' product takes
+    assert f(lib, T=1 << 24, k=16, dd=16, dx=16, N=8, K=8, dY=None) == UNSUPPORTED
+    assert f(lib, T=(1 << 24) - 32, k=16, dd=16, dx=16, N=8, K=8, dY=None) == NULL
+    assert moe_gemm(lib, T=1 << 24, k=16, div=16, N=8, K=8, X=None) == NULL
 
 
 def test_gemm_tn_refusals(lib):
@@ -96,7 +100,9 @@ def test_workspaces(lib):
     assert f(-1, 8, 8) == f(8, -8, 8) == f(8, 8, (1 << 22) + 8) == f(1 << 31, 8, 8) == -1
     assert g(4096, 8, 64, 4096, 4096) == 0 and g(8192, 1, 1, 64, 64) == f(8192, 64, 64)
     assert g(-1, 1, 1, 8, 8) == g(1, 0, 1, 8, 8) == g(1, 1, 0, 8, 8) == g(1, 1, 1, 0, 8) == -1
+    assert g(1 << 24, 17, 1, 8, 8) == g(8, 1, 1025, 8, 8) == g(8, 1, 0x7FFFFFFF, 1 << 22, 1 << 22) == -1
     m = lib.w4_bf16_moe_gemm_workspace
+    assert m(8, 1, 1025, 8, 8, 64) == m(8, 1, 1, 8, 8, 1088) == -1
     assert m(4096, 8, 64, 4096, 4096, 256) == m(0, 1, 1, 64, 64, 64) == 0
     assert m(1, 1, 1, 4095, 4096, 64) > 0 and m(1, 1, 1, 4095, 4096, 64) % 4096 == 0
     assert m(-1, 1, 1, 8, 8, 64) == m(1, 1, 1, 8, 8, 32) == m(1 << 30, 2, 1, 8, 8, 64) == -1
