@@ -44,8 +44,8 @@ struct Job {
   // a tile kernel's: columns of tiles (8 of them a band), tiles of an XCD for a sum
   int32_t mt, nt, per;
   Div by_band, by_per, by_splits;
+  int32_t run;              // k_bf16_short: tiles of a workgroup, side by side (nt counts such runs)
 };
-
 
 // First of n ascending numbers that is not below e, by 64 probes at a time;
 // always within [0, n], whatever the numbers are.
@@ -806,6 +806,206 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
   }
 }
 
+// ---------------------------------------------------------------- short sums --
+// Sums over few pairs write far more than they read and multiply, so that what a tile
+// costs is its beginning (the search for the expert's pairs, their rows, the first
+// loads: one load after the other) and its stores.  A workgroup therefore computes a
+// run of 128 x 128 tiles side by side: it begins once, A's rows stay in LDS where they
+// are one stage, and the loads of the next tile are under way below the products and
+// the stores of this one.  Longer sums are right too, stage after stage.
+// Measured (64 x 4 pairs over 32 of [1408, 2048]): 38 us, 63 in tiles of a workgroup
+// each; 512 x 2 over 64 of [4096, 2048]: 252 and 438, 4.3 TB/s of stores, which bound it.
+template <Group G, bool C8>
+__global__ __launch_bounds__(256, 2) void k_bf16_short(Job j) {
+  constexpr int BM = 128, BN = 128, MI = 4, NI = 4, RB = 256;
+  constexpr int X = 4, XC = C8 ? 2 : 0;            // 1 KB loads per wave and operand; codes: 16 each
+  constexpr int STORES = MI * NI / 2;
+  __shared__ __attribute__((aligned(16))) uint8_t as0[BM * 128], as1[BM * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t bs0[BN * 128], bs1[BN * 128];
+  __shared__ __attribute__((aligned(16))) u32x4 rows_[4][64];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
+  const int r16 = lane & 15, h = lane >> 4;
+  const int M = (int)j.M, N = (int)j.N, runs = j.nt, tiles = j.mt * runs;
+  const int at = blockIdx.x / 8, e = div_by((uint32_t)at, j.by_per);
+  const int chunk = (blockIdx.x % 8 + 8 - (int)((uint32_t)e * (uint32_t)tiles % 8)) % 8;
+  const int t = chunk * j.per + at - e * j.per;
+  if (t >= tiles) return;
+  const int band = div_by((uint32_t)t, j.by_band);
+  const int m0 = band * BM, first = (t - band * runs) * j.run * BN, end = min(first + j.run * BN, N);
+
+  int sum = (int)j.K;
+  __amdgpu_buffer_rsrc_t ir = rsrc(nullptr, 0);
+  auto load_id = [&](int step) __attribute__((always_inline)) {
+    const int at = step * 64 + lane;
+    return G == kSums ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ir, at * 4, 0, 0) : (uint32_t)at;
+  };
+  uint32_t id;
+  uint16_t* C = j.C;
+  if constexpr (G == kSums) {
+    const Blocks b = blocks_of(j, e);
+    C += (int64_t)e * M * N;
+    ir = rsrc(j.g.sorted_ids + b.first * j.g.B, (int64_t)(b.last - b.first) * j.g.B * 4);
+    id = load_id(0);
+    sum = b.last == b.first ? 0 : (b.last - 1 - b.first) * j.g.B + pairs_of_block(j.g, b.last - 1);
+  } else {
+    id = load_id(0);
+  }
+  const int steps = max((sum + 63) / 64, 1);       // none: one of zeros
+  const int pairs = G == kSums ? (int)j.g.P : sum;
+  const int64_t rows_a = div_by((uint32_t)pairs, j.by_a), rows_b = div_by((uint32_t)pairs, j.by_b);
+  const int64_t ls = w8_cols(N);
+  const __amdgpu_buffer_rsrc_t ar = rsrc(j.A, rows_a * M * 2), br = rsrc(j.B.p, rows_b * N * (C8 ? 1 : 2));
+  const __amdgpu_buffer_rsrc_t sr = rsrc(j.B.scales, C8 ? rows_b * ls : 0);
+  const __amdgpu_buffer_rsrc_t cr = rsrc(C, (int64_t)M * N * 2);
+
+  // load i of an operand: lane's row of the stage and its column of the tile
+  auto trow = [&](int i) { return 4 * (wave * X + i) + lane / 16; };
+  auto tcol = [&](int i) {
+    return 8 * ((((lane & 15) >> 1) ^ tr_swizzle<RB>(trow(i))) << 1 | (lane & 1));
+  };
+  auto crow = [&](int i) { return 32 * i + 8 * wave + lane / 8; };
+  const int ccol = 16 * (lane & 7);
+  uint32_t arow[X], brow[C8 ? XC : X], srow[C8 ? XC : 1];
+  auto next_rows = [&](int step, uint32_t f) __attribute__((always_inline)) {
+    u32x4* q = rows_[wave];                        // the wave's own
+    const bool ok = step * 64 + lane < sum && f < (uint32_t)pairs;
+    const uint32_t fb = (uint32_t)div_by(f, j.by_b);
+    q[lane] = ok ? u32x4{(uint32_t)div_by(f, j.by_a) * (uint32_t)M * 2u, fb * (uint32_t)N * (C8 ? 1u : 2u),
+                         C8 ? fb * (uint32_t)ls : 0u, 0u}
+                 : u32x4{kOOB, kOOB, kOOB, 0u};
+#pragma unroll
+    for (int i = 0; i < X; ++i) {
+      const u32x2 o = *(const u32x2*)&q[trow(i)];
+      arow[i] = o.x;
+      if constexpr (!C8) brow[i] = o.y;
+    }
+#pragma unroll
+    for (int i = 0; i < XC; ++i) {
+      const u32x4 o = q[crow(i)];
+      brow[i] = o.y;
+      srow[i] = o.z;
+    }
+  };
+  u32x4 code[C8 ? XC : 1];
+  uint32_t scale[C8 ? XC : 1];
+  auto load_a = [&](uint8_t* s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < X; ++i) {
+      const int col = m0 + tcol(i);
+      load_lds16(ar, s + (wave * X + i) * 1024, col < M ? arow[i] + 2 * col : kOOB, 0);
+    }
+  };
+  auto load_b = [&](int n0, uint8_t* s) __attribute__((always_inline)) {
+    if constexpr (!C8) {
+#pragma unroll
+      for (int i = 0; i < X; ++i) {
+        const int col = n0 + tcol(i);
+        load_lds16(br, s + (wave * X + i) * 1024, col < N ? brow[i] + 2 * col : kOOB, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < XC; ++i) {
+        const int col = n0 + ccol;
+        code[i] = __builtin_amdgcn_raw_buffer_load_b128(br, col < N ? (int)(brow[i] + col) : (int)kOOB, 0, 0);
+        scale[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, col < N ? (int)(srow[i] + (col >> 7)) : (int)kOOB, 0, 0);
+      }
+    }
+  };
+  auto put_codes = [&](uint8_t* s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < XC; ++i) {
+      u32x4* d = (u32x4*)(s + crow(i) * RB + ((2 * ccol) ^ (32 * tr_swizzle<RB>(crow(i)))));
+      const float f = __uint_as_float(scale[i] << 23);
+      const u32x4 c = code[i];
+      d[0] = u32x4{cvt2(c.x, f), cvt2h(c.x, f), cvt2(c.y, f), cvt2h(c.y, f)};
+      d[1] = u32x4{cvt2(c.z, f), cvt2h(c.z, f), cvt2(c.w, f), cvt2h(c.w, f)};
+    }
+  };
+  const int arow0 = (wave >> 1) * 16 * MI, brow0 = (wave & 1) * 16 * NI;
+  const int from = (8 * h + (r16 >> 2)) * RB + (r16 & 3) * 8, swz = 32 * tr_swizzle<RB>(8 * h + (r16 >> 2));
+  auto read = [&](const uint8_t* s, int col) __attribute__((always_inline)) {
+    s += from + ((2 * col) ^ swz);
+    const u32x2 a = read_tr(s), b = read_tr(s + 4 * RB), c = read_tr(s + 32 * RB), d = read_tr(s + 36 * RB);
+    return Operand{u32x4{a.x, a.y, b.x, b.y}, u32x4{c.x, c.y, d.x, d.y}};
+  };
+  uint32_t row_at[MI];                             // of C
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int row = m0 + arow0 + r16 + 16 * i;
+    row_at[i] = row < M ? (uint32_t)row * (uint32_t)N * 2u : kOOB;
+  }
+
+  f32x4 acc[MI][NI] = {};
+  int n0 = first, step = 0;
+  next_rows(0, id);
+  load_a(as0);
+  load_b(n0, bs0);
+  id = steps > 1 ? load_id(1) : id;
+  if constexpr (C8) put_codes(bs0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // one stage: its operands are (sa, sb), the next one's go into (na, nb).  Every wave's
+  // loads have been waited for when it comes here, and its reads of (na, nb) are done.
+  auto body = [&](const uint8_t* sa, const uint8_t* sb, uint8_t* na, uint8_t* nb)
+      __attribute__((always_inline)) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const bool done = step + 1 == steps;
+    const int next = done ? n0 + BN : n0;
+    const bool more = next < end;
+    step = done ? 0 : step + 1;
+    if (more) {
+      if (steps > 1) {
+        next_rows(step, id);
+        load_a(na);
+        id = load_id(step + 1 == steps ? 0 : step + 1);
+      }
+      load_b(next, nb);
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    Operand x[MI], w[NI];
+#pragma unroll
+    for (int n = 0; n < NI; ++n) w[n] = read(sb, brow0 + 16 * n);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) x[i] = read(sa, arow0 + 16 * i);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int n = 0; n < NI; ++n) {
+        acc[i][n] = mfma16(w[n].lo, x[i].lo, acc[i][n]);
+        acc[i][n] = mfma16(w[n].hi, x[i].hi, acc[i][n]);
+      }
+    if constexpr (C8) {
+      if (more) put_codes(nb);
+    }
+    if (done) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int n = 0; n < NI; n += 2) {
+          const int col = n0 + brow0 + 16 * n + 8 * h;
+          const u32x4 v = join_tiles(acc[i][n], acc[i][n + 1]);
+          __builtin_amdgcn_raw_buffer_store_b128(v, cr, col < N ? (int)(row_at[i] + 2 * col) : (int)kOOB, 0, 0);
+          acc[i][n] = acc[i][n + 1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+      // the next stage's loads came before these stores
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(STORES) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    n0 = next;
+    return more;
+  };
+  if (steps == 1) {
+    while (body(as0, bs0, as0, bs1) && body(as0, bs1, as0, bs0)) {}
+  } else {
+    while (body(as0, bs0, as1, bs1) && body(as1, bs1, as0, bs0)) {}
+  }
+}
+
 // Partial sums joined in their order and rounded to bf16, eight columns a thread: of
 // groups of `rows` rows, or (kRows) of the pairs that slots name.
 template <Group G>
@@ -846,6 +1046,10 @@ Div divisor(int32_t d) { return {(uint32_t)d, 0xFFFFFFFFu / (uint32_t)d}; }
 
 int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
+// The tiles address an operand's rows with 32-bit offsets; what they do not cover
+// goes through the simple kernel.
+bool fits(int64_t elems) { return elems * 2 < (int64_t)kOOB; }
+
 template <Group G, bool TA, bool TB, bool C8>
 hipError_t run_simple(const Job& j, hipStream_t st) {
   const int64_t tiles = tiles_of(j.M, j.N, 64, 64) * (G == kSums ? j.g.E : 1);
@@ -872,6 +1076,19 @@ hipError_t run_tile(Job j, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <Group G, bool C8>
+hipError_t run_short(Job j, hipStream_t st) {
+  const int tiles = (int)((j.N + 127) / 128);
+  j.mt = (int)((j.M + 127) / 128);
+  j.nt = (tiles + j.run - 1) / j.run;
+  j.per = (int)(((int64_t)j.mt * j.nt + 7) / 8);
+  j.by_band = divisor(j.nt);
+  j.by_per = divisor(j.per);
+  const int64_t mine = (int64_t)j.per * (G == kSums ? j.g.E : 1);
+  hipLaunchKernelGGL((k_bf16_short<G, C8>), dim3((unsigned)(8 * mine)), dim3(256), 0, st, j);
+  return hipGetLastError();
+}
+
 // The tiles and what they cost, in us: `fixed` and `step` (64 of the sum) for each
 // tile of a CU that is kept busy, `latency` for tiles that have their CU to themselves;
 // measured for products by rows (first) and for sums (second).  256 x 256 moves the
@@ -892,18 +1109,29 @@ constexpr Kind kKinds[] = {
 };
 constexpr int kKindCount = 4;
 
-float estimate(const Kind& t, int64_t tiles, int64_t steps, bool sums) {
+float estimate(const Kind& t, int64_t tiles, float steps, bool sums) {
   const int64_t cus = cu_count(), mine = (tiles + cus - 1) / cus;
   const int64_t waves = (mine + t.occupancy - 1) / t.occupancy;
-  const float busy = (float)mine * (t.fixed[sums] + (float)steps * t.step[sums]);
-  const float alone = (float)waves * (t.latency[sums] + (float)steps * t.latency_step[sums]);
+  const float busy = (float)mine * (t.fixed[sums] + steps * t.step[sums]);
+  const float alone = (float)waves * (t.latency[sums] + steps * t.latency_step[sums]);
+  return 3.0f + std::max(busy, alone);
+}
+
+// k_bf16_short, in the same measure: a workgroup begins, then costs by tile and stage;
+// a workgroup runs on when the others are done.  It wins below about 300 summed rows of
+// large results (64 x [2816, 2048] over 256 pairs each: 396 us, 432 in 128 x 128 tiles;
+// over 2050 x 6 pairs on 48 of [2808, 2064], the two are even and it loses 8%).
+float estimate_short(int run, int64_t workgroups, float steps) {
+  const int64_t cus = cu_count(), mine = (workgroups + cus - 1) / cus, waves = (mine + 1) / 2;
+  const float busy = ((float)mine + 0.25f) * (0.7f + (float)run * (1.1f + 0.65f * steps));
+  const float alone = (float)waves * (3.2f + (float)run * (0.35f + 0.9f * steps));
   return 3.0f + std::max(busy, alone);
 }
 
 int64_t steps_of(int64_t sum) { return std::max((sum + 127) / 128 * 2, (int64_t)2); }
 
 struct Choice {
-  int kind, splits;
+  int kind, splits, run;   // run > 0: k_bf16_short, with that many tiles of a workgroup
 };
 
 // The kind that is done first, and in how many parts: few tiles of long sums are split
@@ -911,7 +1139,7 @@ struct Choice {
 // 40 us whole, 15 in parts; one row of [4096, 4096]: 16 and 12).  groups sums of M x N
 // results; B > 0: rows in blocks of B, the padding of an expert's last tile half full.
 Choice choose(int64_t groups, int64_t M, int64_t N, int64_t sum, int32_t B, int32_t E, bool workspace) {
-  Choice best = {0, 1};
+  Choice best = {0, 1, 0};
   float least = 0.0f;
   const int64_t steps = steps_of(sum);
   for (int splits = 1; splits <= (workspace ? 32 : 1); splits *= 2) {
@@ -927,9 +1155,22 @@ Choice choose(int64_t groups, int64_t M, int64_t N, int64_t sum, int32_t B, int3
         high = std::max(used, high + used / 2);
       }
       const int64_t tiles = groups * splits * high * ((N + t.bn - 1) / t.bn);
-      const float us = join + estimate(t, tiles, steps_of((sum + splits - 1) / splits), B == 0);
+      const int64_t part = (sum + splits - 1) / splits;
+      const float mean = groups > 1 ? std::max((float)part / 64.0f + 1.0f, 2.0f) : (float)steps_of(part);
+      const float us = join + estimate(t, tiles, mean, B == 0);
       if (least == 0.0f || us < least) {
-        best = {i, splits};
+        best = {i, splits, 0};
+        least = us;
+      }
+    }
+  }
+  if (B == 0 && fits(M * N)) {
+    const float stages = std::max(groups > 1 ? (float)sum / 64.0f + 0.5f : (float)((sum + 63) / 64), 1.0f);
+    for (int run = 2; run <= 8; run *= 2) {
+      const int64_t workgroups = groups * ((M + 127) / 128) * (((N + 127) / 128 + run - 1) / run);
+      const float us = estimate_short(run, workgroups, stages);
+      if (us < least) {
+        best = {0, 1, run};
         least = us;
       }
     }
@@ -964,10 +1205,6 @@ Job job(const uint16_t* A, const Bf16Rows& B, uint16_t* C, int64_t M, int64_t N,
   return j;
 }
 
-// The tiles address an operand's rows with 32-bit offsets; what they do not cover
-// goes through the simple kernel.
-bool fits(int64_t elems) { return elems * 2 < (int64_t)kOOB; }
-
 bool sums_fit(const Job& j, int64_t rows_a, int64_t rows_b) {
   return fits(rows_a * j.M) && fits(rows_b * j.N);
 }
@@ -982,6 +1219,10 @@ hipError_t join(const Job& j, int64_t groups, int64_t rows, int64_t lines, hipSt
 
 template <Group G>
 hipError_t run_sums(Job j, const Choice& c, hipStream_t st) {
+  if (c.run > 0) {
+    j.run = c.run;
+    return j.B.scales ? run_short<G, true>(j, st) : run_short<G, false>(j, st);
+  }
   j.splits = c.splits;
   const hipError_t e = j.B.scales ? run_kind<G, true, true, true>(c.kind, j, st)
                                   : run_kind<G, true, true>(c.kind, j, st);

@@ -9,6 +9,8 @@ terms' magnitudes bound: n 2^-23 of their sum (2^-23, not 2^-24: the matrix unit
 need not round to nearest).
 """
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -696,3 +698,77 @@ def test_operands_of_two_gib_and_more():
     check_large(C[:, cols], d.t() @ xc, d.abs().t() @ xc.abs(), T, "C")
     x8 = stored(X8[:, :128].contiguous(), SX[:, :1].contiguous())[:, cols]
     check_large(C8[:, cols], d.t() @ x8, d.abs().t() @ x8.abs(), T, "C from codes")
+
+
+# ---------------------------------------------------------------- short sums --
+# Results that are large next to their sums, which a workgroup computes as a run of
+# tiles: one stage and several, last tiles of a run and of a row, an expert with most
+# of the pairs.
+
+def guarded(shape):
+    """bf16 tensor of ``shape`` between canaries, and a check of them."""
+    n = math.prod(shape)
+    base = canary_bf16((n + 8192,))
+
+    def check_ends():
+        bits = down_bits(base)
+        assert (bits[:4096] == CANARY).all() and (bits[n + 4096:] == CANARY).all()
+    return base[4096:4096 + n].view(shape), check_ends
+
+
+@pytest.mark.parametrize("T,k,E,N,K,hot", [(1, 1, 1, 2048, 2064, 0), (40, 2, 16, 1408, 1040, 0),
+                                           (300, 2, 32, 1032, 784, 0), (200, 4, 32, 648, 2320, 180),
+                                           (700, 1, 8, 1536, 1168, 500), (64, 1, 64, 776, 656, 64)])
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("side", ["gate_up", "down"])
+def test_short_grouped_sums(T, k, E, N, K, hot, codes, side):
+    say(f"short grouped sums T={T} k={k} E={E} N={N} K={K} hot={hot} codes={codes} {side}")
+    ids = picks(T, k, E, T, empty=(1,) if E > k + 1 else (), outside=min(2, T * k // 8))
+    ids[:hot, 0] = 0
+    dd, dx = (1, k) if side == "gate_up" else (k, 1)
+    dY, X, SX = normal((T * k // dd, N), 1).to(dev()), normal((T * k // dx, K), 2, 3.0).to(dev()), None
+    if codes:
+        X, SX = w4.w8_quantize_rows(X)
+    B = w4.w4_bf16_pick_block_size(T, k, E)
+    out, check_ends = guarded((E, N, K))
+    w4.w4_bf16_moe_wgrad(dY, X, *plan_of(ids, E, B), E, T, k, B, dd, dx, SX=SX, out=out)
+    check_ends()
+    x, flat = stored(X, SX), up(ids).reshape(-1)
+    for e in range(E):
+        f = torch.nonzero(flat == e)[:, 0]
+        xe, ye = x[f // dx], dY[f // dd].double()
+        check_large(out[e], ye.t() @ xe, ye.abs().t() @ xe.abs(), T, f"dW[{e}]")
+
+
+@pytest.mark.parametrize("M", [1, 40, 64, 65, 129])
+@pytest.mark.parametrize("N,K", [(4096, 4112), (2056, 6160)])
+@pytest.mark.parametrize("codes", [False, True])
+def test_short_dense_sums(M, N, K, codes):
+    say(f"short dense sums M={M} N={N} K={K} codes={codes}")
+    A, B, SB = normal((M, N), 1).to(dev()), normal((M, K), 2).to(dev()), None
+    if codes:
+        B, SB = w4.w8_quantize_rows(B)
+    out, check_ends = guarded((N, K))
+    w4.w4_bf16_gemm_tn(A, B, SB=SB, out=out)
+    check_ends()
+    b = stored(B, SB)
+    check_large(out, A.double().t() @ b, A.double().abs().t() @ b.abs(), M, "C")
+
+
+def test_short_sums_of_rows_that_hold_nan():
+    """NaN and infinity in rows of other experts and of skipped pairs stay there."""
+    T, k, E, N, K = 96, 2, 32, 1032, 1040
+    ids = picks(T, k, E, 5, empty=(3,), outside=6)
+    dY, X = normal((T * k, N), 1), normal((T * k, K), 2)
+    flat = torch.from_numpy(ids.reshape(-1).copy())
+    bad = (flat == 7) | (flat < 0) | (flat >= E)
+    dY[bad] = float("nan")
+    X[bad] = float("inf")
+    got = w4.w4_bf16_moe_wgrad(dY.to(dev()), X.to(dev()), *plan_of(ids, E, 64), E, T, k, 64, 1, 1)
+    for e in range(E):
+        f = torch.nonzero(flat == e)[:, 0]
+        if e == 7:
+            assert f.numel() and bool(got[e].isnan().all())
+            continue
+        ye, xe = dY[f].double().to(dev()), X[f].double().to(dev())
+        check_large(got[e], ye.t() @ xe, ye.abs().t() @ xe.abs(), T, f"dW[{e}]")
