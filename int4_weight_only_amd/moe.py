@@ -536,7 +536,9 @@ def moe_train(X, topk_ids, topk_weights, gate_up, down, int4=False, checkpoint=F
     not change, the gradients of the weights, of X and of the top-k weights are
     those at the kept values (H, 2I multiples of 16).  Otherwise H, I multiples of
     8.  B defaults to ``w4_bf16_pick_block_size``.  Returns out bf16 [T, H].  The
-    backward is not differentiable again.
+    backward is not differentiable again.  To capture it into a graph, take
+    gradients with ``torch.autograd.grad``, or let no eager graph of the same leaves
+    be alive.
     """
     device = _in(X, "X", torch.bfloat16, 2)
     T, H = X.shape

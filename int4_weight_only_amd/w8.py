@@ -15,8 +15,9 @@ identity, so
 which covers fewer than 2^22 tokens: more of them are refused in the forward
 where W needs a gradient.  With ``checkpoint`` the codes that the forward
 multiplied are kept instead of X, half the bytes, and dW = dY^T * Q_rows(X) is
-taken from them (``w4_bf16_gemm_tn``): the gradient of the product as it ran.  The master weight stays bf16.  The backward is not
-differentiable again.  To capture a backward into a graph, take gradients with
+taken from them (``w4_bf16_gemm_tn``): the gradient of the product as it ran.
+The master weight stays bf16.  The backward is not differentiable again.  To
+capture a backward into a graph, take gradients with
 ``torch.autograd.grad``, or let no eager graph of the same leaves be alive.
 """
 
