@@ -683,8 +683,10 @@ int w4_moe_route_scored_bwd(const float* logits, const int32_t* topk_ids,
  *    which is exact unless it lies below bf16's normal range.
  *  - A pair whose expert lies outside [0, E) takes no part in any product; rows
  *    of outputs that no slot names are not written.
- *  - Limits: E <= 1024, N and K <= 2^22, T*k + E*B < 2^31, 2^40 elements per
- *    matrix, 2^32 threads per launch (W4_ERR_UNSUPPORTED).
+ *  - Limits: E <= 1024, N and K <= 2^22, T*k + E*B < 2^31, fewer than 2^34 elements of
+ *    an operand's rows (of one expert's weights where transposed) and 2^31 of a
+ *    checkpoint's scales, 2^40 elements per other matrix, 2^32 threads per launch
+ *    (W4_ERR_UNSUPPORTED).
  *
  * w4_bf16_pick_block_size -- alignment block size of these products: the
  * smallest of 64, 128 and 256 that holds one and a half times the average number
@@ -743,7 +745,7 @@ int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,
  * with fp32 accumulation (order unspecified but fixed).  A bf16 [M, N]; B bf16
  * [M, K], or with SB a checkpoint of such rows; C bf16 [N, K]; all 16-byte
  * aligned, SB 4-byte.  N % 8 == 0, K % 8 == 0 (16 with SB) (W4_ERR_SHAPE).
- * N*K == 0 is a no-op; M == 0 writes zeros.  workspace: fp32
+ * N*K == 0 is a no-op; M == 0 writes zeros.  M <= 2^30.  workspace: fp32
  * [w4_bf16_gemm_tn_workspace(M, N, K)] or NULL, as w4_bf16_moe_gemm's.
  */
 int64_t w4_bf16_gemm_tn_workspace(int64_t M, int64_t N, int64_t K);

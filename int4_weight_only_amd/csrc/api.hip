@@ -789,6 +789,11 @@ namespace {
 constexpr int64_t kBf16MaxCols = (int64_t)1 << 22;
 // slots of an expert's pairs that the sums reach with 32-bit byte offsets
 constexpr int64_t kBf16MaxSumSlots = (int64_t)1 << 28;
+// rows that the products gather, addressed in units of 16 bytes: 32 GiB of bf16, and of
+// a checkpoint's scales, addressed in bytes
+bool bf16_in_reach(int64_t rows, int64_t cols, bool codes) {
+  return rows * cols < (int64_t)1 << 34 && (!codes || rows * w4::w8_cols(cols) < kMaxI32);
+}
 
 // Sizes and alignment arrays shared by the grouped bf16 products; W4_OK or an
 // error status.
@@ -837,7 +842,9 @@ int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted
                                   K, B);
   if (v == W4_ERR_SHAPE) return v;
   if ((x_row_div != 1 && x_row_div != k) || (transposed && N % 8 != 0)) return W4_ERR_SHAPE;
-  if (v == W4_ERR_UNSUPPORTED || w4::bf16_moe_threads(T * k, E, N, K, B) >= kMaxGrid)
+  if (v == W4_ERR_UNSUPPORTED || !bf16_in_reach(T * k / x_row_div, K, false) ||
+      (transposed && !bf16_in_reach(K, N, false)) ||
+      w4::bf16_moe_threads(T * k, E, N, K, B) >= kMaxGrid)
     return W4_ERR_UNSUPPORTED;
   if (T == 0) return W4_OK;
   if (v != W4_OK) return v;
@@ -861,6 +868,7 @@ int w4_bf16_moe_wgrad(const uint16_t* dY, const void* X, const uint8_t* SX,
       (SX && K % 16 != 0))
     return W4_ERR_SHAPE;
   if (v == W4_ERR_UNSUPPORTED || T * k + (int64_t)E * B > kBf16MaxSumSlots ||
+      !bf16_in_reach(T * k / dy_row_div, N, false) || !bf16_in_reach(T * k / x_row_div, K, SX != nullptr) ||
       w4::bf16_wgrad_threads(E, N, K) >= kMaxGrid)
     return W4_ERR_UNSUPPORTED;
   if (v != W4_OK) return v;
@@ -891,8 +899,9 @@ int w4_bf16_gemm_tn(const uint16_t* A, const void* B, const uint8_t* SB, uint16_
                     int64_t N, int64_t K, float* workspace, void* stream) {
   if (M < 0 || N < 0 || K < 0 || N % 8 != 0 || K % 8 != 0 || (SB && K % 16 != 0))
     return W4_ERR_SHAPE;
-  if (M > kMaxI32 || N > kBf16MaxCols || K > kBf16MaxCols || M * N > kMaxElems ||
-      M * K > kMaxElems || N * K > kMaxElems || w4::bf16_wgrad_threads(1, N, K) >= kMaxGrid)
+  if (M > (int64_t)1 << 30 || N > kBf16MaxCols || K > kBf16MaxCols || !bf16_in_reach(M, N, false) ||
+      !bf16_in_reach(M, K, SB != nullptr) || N * K > kMaxElems ||
+      w4::bf16_wgrad_threads(1, N, K) >= kMaxGrid)
     return W4_ERR_UNSUPPORTED;
   if (N == 0 || K == 0) return W4_OK;
   if (!C || (M > 0 && (!A || !B))) return W4_ERR_NULL;

@@ -10,8 +10,8 @@
 // may be a checkpoint of e4m3 codes.
 //
 // Kernels: k_bf16_tile (tiles of 64 x 64 to 256 x 256), k_bf16_short (results that are
-// large next to their sums), k_bf16_join (sums in parts), k_bf16_simple (operands of
-// 2 GiB and more).  The host picks by what each is estimated to take (choose).
+// large next to their sums), k_bf16_join (sums in parts).  The host picks by what each
+// is estimated to take (choose).
 #include <algorithm>
 #include <type_traits>
 
@@ -128,123 +128,7 @@ __device__ __forceinline__ uint32_t cvt2h(uint32_t codes, float s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, true));
 }
 
-// Eight consecutive values of a row as bf16.
-template <bool C8>
-__device__ __forceinline__ u32x4 eight(const Bf16Rows& o, int64_t row, int64_t cols, int64_t c) {
-  if constexpr (!C8) {
-    return *(const u32x4*)((const uint16_t*)o.p + row * cols + c);
-  } else {
-    const u32x2 q = *(const u32x2*)((const uint8_t*)o.p + row * cols + c);
-    const float s = __uint_as_float((uint32_t)o.scales[row * w8_cols(cols) + (c >> 7)] << 23);
-    return u32x4{cvt2(q.x, s), cvt2h(q.x, s), cvt2(q.y, s), cvt2h(q.y, s)};
-  }
-}
-
 }  // namespace
-
-// ------------------------------------------------------------ simple tile --
-// 64 x 64 of C by four waves of 32 x 32, 32 of the summed dimension a step
-// through LDS as [row][k], 64-bit addresses throughout: for operands that the others'
-// 32-bit offsets do not reach.  It waits for each step's loads (SIMPLE_FIG).
-template <Group G, bool TA, bool TB, bool C8>
-__global__ __launch_bounds__(256) void k_bf16_simple(Job j) {
-  constexpr int PAD = 8;
-  __shared__ __attribute__((aligned(16))) uint16_t as[64][32 + PAD], bs[64][32 + PAD];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r16 = lane & 15, h = lane >> 4;
-  const int64_t nt = (j.N + 63) / 64, mt = (j.M + 63) / 64;
-  int64_t tile = blockIdx.x, e = 0;
-  if constexpr (G == kSums) {
-    e = tile / (mt * nt);
-    tile -= e * mt * nt;
-  }
-  const int64_t m0 = tile / nt * 64, n0 = tile % nt * 64;
-  struct {
-    int first, count;
-  } seg = {0, 0};
-  int64_t steps = (j.K + 31) / 32, cap = 0;
-  if constexpr (G != kDense) cap = (j.g.P + (int64_t)j.g.E * (j.g.B - 1) + j.g.B - 1) / j.g.B * j.g.B;
-  if constexpr (G == kRows) {
-    if (m0 >= min((int64_t)j.g.ntpp[0], cap)) return;
-    e = j.g.expert_ids[m0 / j.g.B];
-    if (e < 0 || e >= j.g.E) return;
-    j.B.p = (const uint16_t*)j.B.p + e * j.N * j.K;
-  }
-  if constexpr (G == kSums) {
-    const Blocks b = blocks_of(j, (int)e);
-    seg.first = b.first * j.g.B;
-    if (b.last > b.first) seg.count = (b.last - 1 - b.first) * j.g.B + pairs_of_block(j.g, b.last - 1);
-    steps = (seg.count + 31) / 32;
-    j.C += e * j.M * j.N;
-  }
-  auto pair = [&](int64_t slot) { return (uint32_t)j.g.sorted_ids[slot]; };
-  // row of the operand that summed index k stands for; -1: none
-  auto sum_row = [&](int64_t k, int div) -> int64_t {
-    if constexpr (G == kSums) {
-      if (k >= seg.count) return -1;
-      const uint32_t f = pair(seg.first + k);
-      return f < (uint32_t)j.g.P ? (int64_t)(f / (uint32_t)div) : -1;
-    } else {
-      return k < j.K ? k : -1;
-    }
-  };
-  f32x4 acc[2][2] = {};
-  const u32x4 zero = {0u, 0u, 0u, 0u};
-  for (int64_t s = 0; s < steps; ++s) {
-    const int64_t k0 = s * 32;
-    __syncthreads();
-    if constexpr (!TA) {
-      const int r = tid >> 2, c = 8 * (tid & 3);
-      int64_t row = m0 + r < j.M ? m0 + r : -1;
-      if constexpr (G == kRows) {
-        const uint32_t f = pair(m0 + r);
-        row = f < (uint32_t)j.g.P ? (int64_t)(f / (uint32_t)j.a_div) : -1;
-      }
-      *(u32x4*)&as[r][c] = row >= 0 && k0 + c < j.K ? eight<false>({j.A, nullptr}, row, j.K, k0 + c) : zero;
-    } else {
-      const int k = tid >> 3, c = 8 * (tid & 7);
-      const int64_t row = sum_row(k0 + k, j.a_div);
-      const u32x4 v = row >= 0 && m0 + c < j.M ? eight<false>({j.A, nullptr}, row, j.M, m0 + c) : zero;
-      const uint16_t* q = (const uint16_t*)&v;
-      for (int i = 0; i < 8; ++i) as[c + i][k] = q[i];
-    }
-    if constexpr (!TB) {
-      const int r = tid >> 2, c = 8 * (tid & 3);
-      *(u32x4*)&bs[r][c] =
-          n0 + r < j.N && k0 + c < j.K ? eight<false>(j.B, n0 + r, j.K, k0 + c) : zero;
-    } else {
-      const int k = tid >> 3, c = 8 * (tid & 7);
-      const int64_t row = sum_row(k0 + k, j.b_div);
-      const u32x4 v = row >= 0 && n0 + c < j.N ? eight<C8>(j.B, row, j.N, n0 + c) : zero;
-      const uint16_t* q = (const uint16_t*)&v;
-      for (int i = 0; i < 8; ++i) bs[c + i][k] = q[i];
-    }
-    __syncthreads();
-    u32x4 a[2], b[2];
-    for (int i = 0; i < 2; ++i) {
-      a[i] = *(const u32x4*)&as[32 * (wave >> 1) + 16 * i + r16][8 * h];
-      b[i] = *(const u32x4*)&bs[32 * (wave & 1) + 16 * i + r16][8 * h];
-    }
-    for (int i = 0; i < 2; ++i)
-      for (int n = 0; n < 2; ++n) acc[i][n] = mfma16(b[n], a[i], acc[i][n]);
-  }
-  // lane holds columns 4 h .. + 3 of row r16 of each 16 x 16
-  for (int i = 0; i < 2; ++i) {
-    int64_t row = m0 + 32 * (wave >> 1) + 16 * i + r16;
-    if constexpr (G == kRows) {
-      const uint32_t f = pair(row);
-      row = f < (uint32_t)j.g.P ? (int64_t)f : -1;
-    } else if (row >= j.M) {
-      row = -1;
-    }
-    if (row < 0) continue;
-    for (int n = 0; n < 2; ++n)
-      for (int v = 0; v < 4; ++v) {
-        const int64_t c = n0 + 32 * (wave & 1) + 16 * n + 4 * h + v;
-        if (c < j.N) j.C[row * j.N + c] = to_bf16(acc[i][n][v]);
-      }
-  }
-}
 
 // --------------------------------------------------------------- LDS tile --
 // A workgroup of four waves computes BM = 32 MI rows of C times BN = 32 NI
@@ -312,6 +196,19 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, void* lds, 
 }
 __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 4, off, 0, 0, 0);
+}
+
+// What a lane without a row reads where addresses have 64 bits.
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
+
+// 16 bytes at the index'th 16 bytes from base; kOOB (and what is added to it): zeros.
+typedef const __attribute__((address_space(1))) uint8_t* global_ptr;
+__device__ __forceinline__ global_ptr wide_address(const uint8_t* base, uint32_t index) {
+  return (global_ptr)((int)index >= 0 ? (uint64_t)base + ((uint64_t)index << 4) : (uint64_t)kZeros);
+}
+__device__ __forceinline__ void load_lds16_wide(const uint8_t* base, void* lds, uint32_t index) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)wide_address(base, index),
+                                   (lds_ptr)lds, 16, 0, 0);
 }
 
 // Four rows of 16 columns, column-wise: lane c of each 16 gets column c.
@@ -382,7 +279,10 @@ struct Operand {           // 16 rows x 64 of the sum: two MFMA operands
 // scale a lane, become bf16 by v_cvt_scalef32_pk_bf16_fp8 (which applies the power of
 // two) and go into the stage as bf16 rows would, so that each element is converted
 // once a workgroup and memory sees half the bytes.
-template <int MI, int NI, Group G, bool TA, bool TB, bool C8>
+//
+// WIDE: offsets count 16 bytes and addresses have 64 bits, for operands of 2 GiB and
+// more, which buffer loads do not reach.
+template <int MI, int NI, Group G, bool TA, bool TB, bool C8, bool WIDE = false>
 __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Job j) {
   constexpr int BM = 32 * MI, BN = 32 * NI;
   constexpr int XA = BM / 32, XB = C8 ? 0 : BN / 32;   // 1 KB loads per wave and stage
@@ -517,14 +417,20 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
   auto tcol = [&](int slot, int swz) { return 8 * (((slot >> 1) ^ swz) << 1 | (slot & 1)); };
   constexpr int CPR = BN / 16;                     // codes: lanes of a row
   auto crow = [&](int i) { return (i * 256 + wave * 64 + lane) / CPR; };
-  // byte offset of the lane's 16 bytes at step 0; of its column alone (kSums); past the end: kOOB
+  // byte offset of the lane's 16 bytes at step 0 (WIDE: offset in units of 16, here and
+  // below); of its column alone (kSums); past the end: kOOB
+  const uint8_t* const abase = (const uint8_t*)(A + (TA ? (int64_t)m0 : (G == kRows ? 0 : m0 * lda)));
+  const uint8_t* const bbase = B + (TB ? n0 : n0 * ldb) * BB;
+  auto offset = [](int64_t bytes) __attribute__((always_inline)) {
+    return WIDE ? (uint32_t)(bytes >> 4) : (uint32_t)bytes;
+  };
   uint32_t aoff[XA], boff[C8 ? 1 : XB];
 #pragma unroll
   for (int i = 0; i < XA; ++i) {
     const int I = wave * XA + i;
     if constexpr (TA) {
       const int row = trow(I, LRA), col = tcol(lane % LRA, tr_swizzle<2 * BM>(row));
-      aoff[i] = m0 + col < M ? (uint32_t)((G == kSums ? 0 : row * lda) + col) * 2u : kOOB;
+      aoff[i] = m0 + col < M ? offset(((G == kSums ? 0 : row * lda) + col) * 2) : kOOB;
     } else {
       const int r = 8 * I + (lane >> 3);
       int64_t row = r < rows_a ? r : -1;
@@ -532,7 +438,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
         const uint32_t f = (uint32_t)ids[m0 + r];
         row = f < (uint32_t)j.g.P ? (int64_t)div_by(f, j.by_a) : -1;
       }
-      aoff[i] = row >= 0 ? (uint32_t)(row * lda + 8 * piece(I)) * 2u : kOOB;
+      aoff[i] = row >= 0 ? offset((row * lda + 8 * piece(I)) * 2) : kOOB;
     }
   }
 #pragma unroll
@@ -540,10 +446,10 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
     const int I = wave * XB + i;
     if constexpr (TB) {
       const int row = trow(I, LRB), col = tcol(lane % LRB, tr_swizzle<2 * BN>(row));
-      boff[i] = n0 + col < j.N ? (uint32_t)((G == kSums ? 0 : row * ldb) + col) * 2u : kOOB;
+      boff[i] = n0 + col < j.N ? offset(((G == kSums ? 0 : row * ldb) + col) * 2) : kOOB;
     } else {
       const int r = 8 * I + (lane >> 3);
-      boff[i] = r < rows_b ? (uint32_t)(r * ldb + 8 * piece(I)) * 2u : kOOB;
+      boff[i] = r < rows_b ? offset((r * ldb + 8 * piece(I)) * 2) : kOOB;
     }
   }
   // kSums: lane l holds the pair of row l of a coming step (loaded a step before it
@@ -555,7 +461,9 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
       u32x4* q = rows_[wave];                  // a wave's LDS operations keep their order
       const bool ok = step * 64 + lane < k_end && f < (uint32_t)j.g.P;
       const uint32_t fb = (uint32_t)div_by(f, j.by_b);
-      q[lane] = ok ? u32x4{(uint32_t)div_by(f, j.by_a) * (uint32_t)lda * 2u, fb * (uint32_t)ldb * BB, C8 ? fb * (uint32_t)lds : 0u, 0u}
+      const uint32_t fa = (uint32_t)div_by(f, j.by_a);
+      q[lane] = ok ? u32x4{WIDE ? offset(fa * lda * 2) : fa * (uint32_t)lda * 2u,
+                           WIDE ? offset(fb * ldb * BB) : fb * (uint32_t)ldb * BB, C8 ? fb * (uint32_t)lds : 0u, 0u}
                    : u32x4{kOOB, kOOB, kOOB, 0u};
 #pragma unroll
       for (int i = 0; i < XA; ++i) {
@@ -587,7 +495,14 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
     if constexpr (C8) {
 #pragma unroll
       for (int i = 0; i < XC; ++i) {
-        if constexpr (G == kSums) {
+        if constexpr (WIDE) {
+          const int left = k_end - step * 64;
+          const uint32_t from = G == kSums ? brow[i] : offset((left > 0 ? step * 64 + crow(i) : 0) * ldb);
+          const bool ok = cok && (G == kSums || crow(i) < left);
+          code[i] = *(const __attribute__((address_space(1))) u32x4*)wide_address(bbase, ok ? from + ccol / 16 : kOOB);
+          scale[i] = __builtin_amdgcn_raw_buffer_load_b8(
+              sr, G == kSums ? (int)(srow[i] + cs) : ok ? (int)((step * 64 + crow(i)) * (uint32_t)lds + cs) : (int)kOOB, 0, 0);
+        } else if constexpr (G == kSums) {
           code[i] = __builtin_amdgcn_raw_buffer_load_b128(br, cok ? (int)(brow[i] + ccol) : (int)kOOB, 0, 0);
           scale[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(srow[i] + cs), 0, 0);
         } else {
@@ -619,7 +534,20 @@ __global__ __launch_bounds__(256, workgroups_per_cu(MI, NI)) void k_bf16_tile(Jo
   auto load_one = [&](int i, int step, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
     const int k0 = step * 64, left = k_end - k0;   // what lies past the end reads zero,
     const uint32_t from = left > 0 ? (uint32_t)k0 * 2u : 0u;       // at offsets inside 32 bits
-    if (i < XA) {
+    if constexpr (WIDE) {
+      const bool a = i < XA;
+      const int I = a ? wave * XA + i : wave * XB + i - XA;
+      const bool across = a ? TA : TB;
+      const uint32_t own = a ? aoff[a ? i : 0] : boff[C8 || a ? 0 : i - XA];
+      uint32_t index;
+      if constexpr (G == kSums) {
+        index = own != kOOB ? (a ? arow[a ? i : 0] : brow[C8 || a ? 0 : i - XA]) + own : kOOB;
+      } else {
+        const bool ok = own != kOOB && (across ? trow(I, a ? LRA : LRB) : 8 * piece(I)) < left;
+        index = ok ? own + offset(across ? from * (a ? lda : ldb) : (int64_t)from) : kOOB;
+      }
+      load_lds16_wide(a ? abase : bbase, (a ? sa : sb) + I * 1024, index);
+    } else if (i < XA) {
       const int I = wave * XA + i;
       if constexpr (G == kSums) {
         load_lds16(ar, sa + I * 1024, aoff[i] != kOOB ? arow[i] + aoff[i] : kOOB, 0);
@@ -1061,18 +989,10 @@ Div divisor(int32_t d) { return {(uint32_t)d, 0xFFFFFFFFu / (uint32_t)d}; }
 
 int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
-// The tiles address an operand's rows with 32-bit offsets; what they do not cover
-// goes through the simple kernel.
+// Buffer loads address an operand's rows with 32-bit byte offsets.
 bool fits(int64_t elems) { return elems * 2 < (int64_t)kOOB; }
 
-template <Group G, bool TA, bool TB, bool C8>
-hipError_t run_simple(const Job& j, hipStream_t st) {
-  const int64_t tiles = tiles_of(j.M, j.N, 64, 64) * (G == kSums ? j.g.E : 1);
-  hipLaunchKernelGGL((k_bf16_simple<G, TA, TB, C8>), dim3((unsigned)tiles), dim3(256), 0, st, j);
-  return hipGetLastError();
-}
-
-template <int MI, int NI, Group G, bool TA, bool TB, bool C8>
+template <int MI, int NI, Group G, bool TA, bool TB, bool C8, bool WIDE = false>
 hipError_t run_tile(Job j, hipStream_t st) {
   j.mt = (int)((j.M + 32 * MI - 1) / (32 * MI));
   j.nt = (int)((j.N + 32 * NI - 1) / (32 * NI));
@@ -1087,7 +1007,7 @@ hipError_t run_tile(Job j, hipStream_t st) {
   } else {
     mine = (int64_t)j.per * (G == kSums ? j.g.E : 1) * j.splits;
   }
-  hipLaunchKernelGGL((k_bf16_tile<MI, NI, G, TA, TB, C8>), dim3((unsigned)(8 * mine)), dim3(256), 0, st, j);
+  hipLaunchKernelGGL((k_bf16_tile<MI, NI, G, TA, TB, C8, WIDE>), dim3((unsigned)(8 * mine)), dim3(256), 0, st, j);
   return hipGetLastError();
 }
 
@@ -1200,8 +1120,15 @@ Choice choose_sums(int64_t groups, int64_t sum, int64_t M, int64_t N, bool works
   return choose(groups, M, N, sum, 0, 0, workspace);
 }
 
+// wide: operands of 2 GiB and more, whose tiles have 64-bit addresses (131142 x 8192
+// by 1024 columns: rows 2680 us, weight gradient of 2 experts 2070, dense sums 2530; with
+// 131000 rows, below 2 GiB: 1840 to 1970, 1760 and 2210).
 template <Group G, bool TA, bool TB, bool C8 = false>
-hipError_t run_kind(int kind, const Job& j, hipStream_t st) {
+hipError_t run_kind(int kind, const Job& j, bool wide, hipStream_t st) {
+  if (wide) {
+    if (kind <= 1) return run_tile<2, 2, G, TA, TB, C8, true>(j, st);   // 64 x 128: few rows, not such operands
+    return kind == 2 ? run_tile<4, 4, G, TA, TB, C8, true>(j, st) : run_tile<8, 8, G, TA, TB, C8, true>(j, st);
+  }
   switch (kind) {
     case 0: return run_tile<2, 2, G, TA, TB, C8>(j, st);
     case 1: return run_tile<2, 4, G, TA, TB, C8>(j, st);
@@ -1220,10 +1147,6 @@ Job job(const uint16_t* A, const Bf16Rows& B, uint16_t* C, int64_t M, int64_t N,
   return j;
 }
 
-bool sums_fit(const Job& j, int64_t rows_a, int64_t rows_b) {
-  return fits(rows_a * j.M) && fits(rows_b * j.N);
-}
-
 template <Group G>
 hipError_t join(const Job& j, int64_t groups, int64_t rows, int64_t lines, hipStream_t st) {
   const int64_t pieces = groups * lines * ((j.N + 7) / 8);
@@ -1233,14 +1156,16 @@ hipError_t join(const Job& j, int64_t groups, int64_t rows, int64_t lines, hipSt
 }
 
 template <Group G>
-hipError_t run_sums(Job j, const Choice& c, hipStream_t st) {
-  if (c.run > 0) {
+hipError_t run_sums(Job j, const Choice& c, int64_t rows_a, int64_t rows_b, hipStream_t st) {
+  const bool wide = !fits(rows_a * j.M) || !fits(rows_b * j.N);
+  const int kind = c.run > 0 ? 3 : c.kind;
+  if (c.run > 0 && !wide) {
     j.run = c.run;
     return j.B.scales ? run_short<G, true>(j, st) : run_short<G, false>(j, st);
   }
   j.splits = c.splits;
-  const hipError_t e = j.B.scales ? run_kind<G, true, true, true>(c.kind, j, st)
-                                  : run_kind<G, true, true>(c.kind, j, st);
+  const hipError_t e = j.B.scales ? run_kind<G, true, true, true>(kind, j, wide, st)
+                                  : run_kind<G, true, true>(kind, j, wide, st);
   return e != hipSuccess || j.splits == 1 ? e : join<G>(j, G == kSums ? j.g.E : 1, j.M, j.M, st);
 }
 
@@ -1267,13 +1192,11 @@ hipError_t launch_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, uint16_t* 
                                 const Bf16Plan& plan, int64_t N, int64_t K, int32_t div,
                                 bool transposed, float* workspace, hipStream_t st) {
   Job j = job(X, {W, nullptr}, Y, moe_cap(plan.P, plan.E, plan.B), N, K, plan, div, 1, workspace);
-  if (!fits(plan.P / div * K) || !fits(transposed ? N * K : std::min(N, (int64_t)256) * K))
-    return transposed ? run_simple<kRows, false, true, false>(j, st)
-                      : run_simple<kRows, false, false, false>(j, st);
+  const bool wide = !fits(plan.P / div * K) || !fits(transposed ? N * K : std::min(N, (int64_t)256) * K);
   const Choice c = choose_rows(plan, N, K, workspace != nullptr);
   j.splits = c.splits;
-  const hipError_t e = transposed ? run_kind<kRows, false, true>(c.kind, j, st)
-                                  : run_kind<kRows, false, false>(c.kind, j, st);
+  const hipError_t e = transposed ? run_kind<kRows, false, true>(c.kind, j, wide, st)
+                                  : run_kind<kRows, false, false>(c.kind, j, wide, st);
   return e != hipSuccess || j.splits == 1 ? e : join<kRows>(j, 1, plan.P, j.M, st);
 }
 
@@ -1281,19 +1204,14 @@ hipError_t launch_bf16_moe_wgrad(const uint16_t* dY, const Bf16Rows& X, uint16_t
                                  const Bf16Plan& plan, int64_t N, int64_t K, int32_t dy_div,
                                  int32_t x_div, float* workspace, hipStream_t st) {
   const Job j = job(dY, X, dW, N, K, 0, plan, dy_div, x_div, workspace);
-  if (!sums_fit(j, plan.P / dy_div, plan.P / x_div))
-    return X.scales ? run_simple<kSums, true, true, true>(j, st)
-                    : run_simple<kSums, true, true, false>(j, st);
-  return run_sums<kSums>(j, choose_sums(plan.E, plan.P / plan.E, N, K, workspace != nullptr), st);
+  return run_sums<kSums>(j, choose_sums(plan.E, plan.P / plan.E, N, K, workspace != nullptr),
+                         plan.P / dy_div, plan.P / x_div, st);
 }
 
 hipError_t launch_bf16_gemm_tn(const uint16_t* A, const Bf16Rows& B, uint16_t* C, int64_t M,
                                int64_t N, int64_t K, float* workspace, hipStream_t st) {
   const Job j = job(A, B, C, N, K, M, {}, 1, 1, workspace);
-  if (!sums_fit(j, M, M))
-    return B.scales ? run_simple<kDense, true, true, true>(j, st)
-                    : run_simple<kDense, true, true, false>(j, st);
-  return run_sums<kDense>(j, choose_sums(1, M, N, K, workspace != nullptr), st);
+  return run_sums<kDense>(j, choose_sums(1, M, N, K, workspace != nullptr), M, M, st);
 }
 
 }  // namespace w4

@@ -72,6 +72,22 @@ def test_wgrad_refusals(lib):
     assert moe_gemm(lib, T=1 << 24, k=16, div=16, N=8, K=8, X=None) == NULL
 
 
+def test_rows_out_of_reach(lib):
+    """2^34 elements of rows, 2^31 of a checkpoint's scales."""
+    big, below = 1 << 14, (1 << 14) - 1
+    assert moe_gemm(lib, T=big, k=1, div=1, N=8, K=1 << 20, X=None) == UNSUPPORTED
+    assert moe_gemm(lib, T=below, k=1, div=1, N=8, K=1 << 20, X=None) == NULL
+    assert moe_gemm(lib, T=1, k=1, div=1, N=1 << 14, K=1 << 20, tr=1, E=1, X=None) == UNSUPPORTED
+    assert moe_gemm(lib, T=1, k=1, div=1, N=1 << 14, K=1 << 20, E=1, X=None) == NULL
+    for sizes in (dict(N=1 << 20, K=8), dict(N=8, K=1 << 20)):
+        assert wgrad(lib, T=big, k=1, dd=1, dx=1, E=1, dY=None, **sizes) == UNSUPPORTED
+        assert wgrad(lib, T=below, k=1, dd=1, dx=1, E=1, dY=None, **sizes) == NULL
+    tn = lambda M, N, K, SB=None: lib.w4_bf16_gemm_tn(None, A16, SB, A16, M, N, K, None, None)
+    assert tn(big, 1 << 20, 8) == tn(big, 8, 1 << 20) == tn((1 << 30) + 1, 8, 8) == UNSUPPORTED
+    assert tn(1 << 29, 8, 16, A4) == UNSUPPORTED
+    assert tn(below, 1 << 20, 8) == tn(1 << 30, 8, 8) == tn((1 << 29) - 1, 8, 16, A4) == NULL
+
+
 def test_gemm_tn_refusals(lib):
     f = lambda *a, ws=None: lib.w4_bf16_gemm_tn(*a[:-1], ws, a[-1])
     for M, N, K, SB in ((-1, 8, 8, None), (4, -8, 8, None), (4, 8, -8, None), (4, 12, 8, None), (4, 8, 12, None),

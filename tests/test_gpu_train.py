@@ -772,3 +772,39 @@ def test_short_sums_of_rows_that_hold_nan():
             continue
         ye, xe = dY[f].double().to(dev()), X[f].double().to(dev())
         check_large(got[e], ye.t() @ xe, ye.abs().t() @ xe.abs(), T, f"dW[{e}]")
+
+
+@pytest.mark.parametrize("N,B", [(64, 64), (64, 128), (520, 256)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_tiles_with_wide_addresses(N, B, transposed):
+    """The last rows of X, past 2^31 bytes, in each tile of the products by rows, and the
+    weight gradients of few and of many columns."""
+    T, K, E = (1 << 17) + 40, 8208, 2
+    say(f"wide addresses N={N} B={B} transposed={transposed}")
+    g = torch.Generator(device=dev()).manual_seed(7)
+    X = torch.randn((T, K), generator=g, device=dev(), dtype=torch.bfloat16)
+    W = normal((E, K, N) if transposed else (E, N, K), 2, 0.05).to(dev())
+    ids = torch.randint(0, E, (T, 1), generator=g, device=dev(), dtype=torch.int32)
+    p = w4.moe_align_block_size(ids, E, B)
+    Y = w4.w4_bf16_moe_gemm(X, W, *p, T, 1, B, 1, transposed=transposed)
+    rows = torch.cat([torch.arange(0, 30), torch.arange(T - 150, T)]).to(dev())
+    x, w, one = X[rows].double(), W.double(), ids[rows, 0] == 1
+    for e in range(E):
+        at = one if e else ~one
+        we = w[e] if transposed else w[e].t().contiguous()
+        check_large(Y[rows[at]], x[at] @ we, x[at].abs() @ we.abs(), K, f"Y of {e}")
+    del Y
+    dY = normal((T, N), 3).to(dev())
+    dW = w4.w4_bf16_moe_wgrad(dY, X, *p, E, T, 1, B, 1, 1)
+    cols = slice(K - 24, K)
+    xc, d = X[:, cols].double(), dY.double()
+    for e in range(E):
+        f = (ids[:, 0] == e)[:, None]
+        check_large(dW[e][:, cols], (d * f).t() @ xc, (d * f).abs().t() @ xc.abs(), T, f"dW[{e}]")
+    X8, SX = w4.w8_quantize_rows(X)
+    dW = w4.w4_bf16_moe_wgrad(dY, X8, *p, E, T, 1, B, 1, 1, SX=SX)
+    last = K // 128 * 128                             # the last scale's columns
+    xc = stored(X8[:, last:].contiguous(), SX[:, K // 128: K // 128 + 1].contiguous())
+    for e in range(E):
+        f = (ids[:, 0] == e)[:, None]
+        check_large(dW[e][:, last:], (d * f).t() @ xc, (d * f).abs().t() @ xc.abs(), T, f"dW[{e}] from codes")
