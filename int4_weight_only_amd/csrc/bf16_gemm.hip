@@ -148,9 +148,10 @@ __device__ __forceinline__ uint32_t cvt2h(uint32_t codes, float s) {
 // about 9 us per round to begin and to store, which nothing hides on a CU that holds
 // one workgroup.  4096 x 8 pairs over 64 of [4096, 2048]: 587 us (937 TFLOP/s), the input
 // gradient 597, with the experts' last blocks half empty; weight gradient over 32 of
-// [4096, 4096]: 1165 (944); dense sums 4096^3: 100 us (1370 TFLOP/s).  The matrix unit is busy 61% of the CUs' cycles by rows, 44% in sums.
+// [4096, 4096]: 1165 (944); dense sums 4096^3: 100 us (1370 TFLOP/s).  The matrix unit
+// is busy 61% of the CUs' cycles by rows, 44% in sums.
 // Few pairs: the experts' weights from memory (8 pairs of 8 [1024, 1024]: 6.5 us;
-// 512 x 1 pairs over 64 of [4096, 2048]: 209 us, 5.1 TB/s).
+// 256 x 2 pairs over 64 of [4096, 2048]: 209 us, 5.1 TB/s).
 namespace {
 
 constexpr uint32_t kOOB = 0x80000000u;   // byte offset past any buffer: reads 0
