@@ -842,6 +842,13 @@ def _out(t, name, shape, dtype, like):
     raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _gradient(grad, shape):
+    """What autograd hands to a backward, as the entry points take it: bf16 [shape],
+    contiguous, at a multiple of 16 bytes (it may be a piece of another tensor)."""
+    g = grad.to(_BF16).reshape(shape).contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 def _ints(t, name, size, device):
     if (isinstance(t, _Tensor) and t.dtype is _I32 and t.is_contiguous() and t.get_device() == device
             and t.numel() >= size):

@@ -48,7 +48,7 @@ from dataclasses import dataclass
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (_call, _in, _ptr, _shape, moe_align_block_size, w4_bf16_moe_gemm_workspace,
+from . import (_call, _gradient, _in, _ptr, _shape, moe_align_block_size, w4_bf16_moe_gemm_workspace,
                w4_bf16_moe_wgrad_workspace, w4_bf16_pick_block_size, w4_moe_align_capacity, w4_moe_combine_workspace_words,
                w4_moe_route, w4_moe_sum, w4a16_moe_gemm_combine,
                w4_pick_block_size, w4_quantize_pack, w4_quantize_pack_asym, w4_repack,
@@ -470,7 +470,7 @@ class RoutedExperts(torch.autograd.Function):
         T, k, E, H, I, B = ctx.sizes
         need_x, need_w, need_up, need_dn = ctx.needs_input_grad[:4]
         P, at = T * k, _plan_at(plan)
-        dO = grad_out.to(torch.bfloat16).contiguous()
+        dO = _gradient(grad_out, (T, H))
         device = dO.get_device()
 
         def back(dy, W, S, N, K, div):

@@ -36,7 +36,7 @@ gradient do not change.
 
 import torch
 
-from . import (w4_bf16_gemm_nt, w4_bf16_gemm_tn, w4_bf16_transpose, w4_dequant_t, w4_fake_quant,
+from . import (_gradient, w4_bf16_gemm_nt, w4_bf16_gemm_tn, w4_bf16_transpose, w4_dequant_t, w4_fake_quant,
                w4_quantize_pack, w4a16_gemm, w8_quantize_rows)
 
 __all__ = ["FakeInt4STE", "fake_quant_ste", "Int4QATLinear", "qat_linear"]
@@ -86,7 +86,7 @@ class Int4QATLinear(torch.autograd.Function):
     def backward(ctx, grad_out):
         X2, SX, Wq, S = ctx.saved_tensors
         N = Wq.shape[0]
-        dY = grad_out.reshape(-1, N).to(torch.bfloat16).contiguous()
+        dY = _gradient(grad_out, (X2.shape[0], N))
         dX = dW = None
         if ctx.needs_input_grad[0]:
             if N % 8:

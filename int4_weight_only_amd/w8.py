@@ -24,7 +24,8 @@ capture a backward into a graph, take gradients with
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (w4_bf16_gemm_nt, w4_bf16_gemm_tn, w4_bf16_transpose, w8_quantize_blocks, w8_quantize_rows, w8a8_gemm)
+from . import (_gradient, w4_bf16_gemm_nt, w4_bf16_gemm_tn, w4_bf16_transpose, w8_quantize_blocks,
+               w8_quantize_rows, w8a8_gemm)
 
 __all__ = ["W8Linear", "w8_linear"]
 
@@ -59,14 +60,14 @@ class W8Linear(torch.autograd.Function):
         Y = w8a8_gemm(X8, SX, W8, SW)
         kept = (X8, SX) if checkpoint else (X2, None)
         ctx.save_for_backward(*(kept if need_dw else (None, None)), WT8, ST)
-        ctx.x_shape, ctx.n = X.shape, N
+        ctx.x_shape, ctx.m, ctx.n = X.shape, X2.shape[0], N
         return Y.reshape(*X.shape[:-1], N)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_out):
         X2, SX, WT8, ST = ctx.saved_tensors
-        dY = grad_out.reshape(-1, ctx.n).to(torch.bfloat16).contiguous()
+        dY = _gradient(grad_out, (ctx.m, ctx.n))
         dX = dW = None
         if ctx.needs_input_grad[0]:
             dX = w8a8_gemm(*w8_quantize_rows(dY), WT8, ST).reshape(ctx.x_shape)
