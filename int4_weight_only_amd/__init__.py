@@ -849,6 +849,14 @@ def _gradient(grad, shape):
     return g if g.data_ptr() % 16 == 0 else g.clone()
 
 
+def _check_sizes(what, name, *args):
+    """ValueError where the entry point ``name`` refuses these sizes.  The pointers of
+    ``args`` are null: it looks at sizes first, so that nothing is enqueued."""
+    status = getattr(_lib.load(), name)(*args, None)
+    if status > 1:                                 # but for ok and null
+        raise ValueError(f"{what} ({name}) does not take these sizes: {_lib.W4Error(name, status)}")
+
+
 def _ints(t, name, size, device):
     if (isinstance(t, _Tensor) and t.dtype is _I32 and t.is_contiguous() and t.get_device() == device
             and t.numel() >= size):

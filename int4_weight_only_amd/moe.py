@@ -43,12 +43,13 @@ activations between kept in bf16 or as 8-bit checkpoints:
 """
 
 import contextlib
+import functools
 from dataclasses import dataclass
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (_call, _gradient, _in, _ptr, _shape, moe_align_block_size, w4_bf16_moe_gemm_workspace,
+from . import (_call, _check_sizes, _gradient, _in, _ptr, _shape, moe_align_block_size, w4_bf16_moe_gemm_workspace,
                w4_bf16_moe_wgrad_workspace, w4_bf16_pick_block_size, w4_moe_align_capacity, w4_moe_combine_workspace_words,
                w4_moe_route, w4_moe_sum, w4a16_moe_gemm_combine,
                w4_pick_block_size, w4_quantize_pack, w4_quantize_pack_asym, w4_repack,
@@ -427,6 +428,10 @@ class RoutedExperts(torch.autograd.Function):
         k = topk_ids.shape[1]
         E, I = gate_up.shape[0], down.shape[2]
         P = T * k
+        # needs_input_grad goes by the inputs alone, also under torch.no_grad()
+        need_x, need_w, need_up, need_dn = (n and grad for n in ctx.needs_input_grad[:4])
+        if need_x or need_w or need_up or need_dn:
+            check_moe_backward(T, k, E, H, I, B, checkpoint, need_x, need_up, need_dn)
         plan = moe_align_block_size(topk_ids, E, B)
         at = _plan_at(plan)
 
@@ -448,8 +453,6 @@ class RoutedExperts(torch.autograd.Function):
         H2, dn = product(A, down, H, I, 1)
         out = torch.empty_like(X)
         _call("w4_moe_sum", device, H2.data_ptr(), weights.data_ptr(), out.data_ptr(), T, k, H)
-        # needs_input_grad goes by the inputs alone, also under torch.no_grad()
-        need_x, need_w, need_up, need_dn = (n and grad for n in ctx.needs_input_grad[:4])
         inner = need_x or need_up
         XS = HS = None
         if checkpoint:
@@ -511,6 +514,28 @@ class RoutedExperts(torch.autograd.Function):
         return dX, dw, d_up, d_dn, None, None, None, None, None
 
 
+@functools.lru_cache(1024)
+def check_moe_backward(T, k, E, H, I, B, checkpoint, need_x, need_up, need_dn):
+    """Refuses in the forward what ``moe_train``'s backward could not compute: ValueError."""
+    none, some = (None,) * 3, 16 if checkpoint else None      # some: not null, not read
+
+    def product(N, K, div):
+        _check_sizes("the backward's product", "w4_bf16_moe_gemm", None, None, *none, None, T, k, E, N, K, B, div,
+                     1, None)
+
+    def sums(N, K, scales, dy_div, x_div):
+        _check_sizes("the weight gradient", "w4_bf16_moe_wgrad", None, None, scales, *none, None, T, k, E, N, K, B,
+                     dy_div, x_div, None)
+    product(I, H, k)
+    _check_sizes("the SwiGLU's gradient", "w4_silu_mul_bwd", None, some, None, None, T * k, I, *none)
+    if need_dn:
+        sums(H, I, None, k, 1)
+    if need_up:
+        sums(2 * I, H, some, 1, k)
+    if need_x:
+        product(H, 2 * I, 1)
+
+
 def _plan_at(plan):
     return tuple(t.data_ptr() for t in plan)
 
@@ -535,7 +560,8 @@ def moe_train(X, topk_ids, topk_weights, gate_up, down, int4=False, checkpoint=F
     backward as e4m3 codes (``w8_quantize_rows``), half the bytes; the output does
     not change, the gradients of the weights, of X and of the top-k weights are
     those at the kept values (H, 2I multiples of 16).  Otherwise H, I multiples of
-    8.  B defaults to ``w4_bf16_pick_block_size``.  Returns out bf16 [T, H].  The
+    8.  B defaults to ``w4_bf16_pick_block_size``; sizes that the backward does not take
+    are refused here where a gradient is wanted (B a multiple of 64 up to 1024).  Returns out bf16 [T, H].  The
     backward is not differentiable again.  To capture it into a graph, take
     gradients with ``torch.autograd.grad``, or let no eager graph of the same leaves
     be alive.

@@ -52,3 +52,21 @@ def test_gradient_at_any_address(layer):
     joined = torch.cat([torch.zeros(3, device=dev(), dtype=torch.bfloat16), f(*leaves).reshape(-1)])
     for a, b in zip(want, torch.autograd.grad(joined, leaves, dO)):
         assert torch.equal(a, b)
+
+
+# --------------------------------------------------------------------- refusals --
+
+def test_moe_train_refuses_in_the_forward_what_the_backward_does_not_take():
+    """Blocks of 16 are the INT4 product's, not the backward's: refused where a gradient is wanted,
+    taken (and the same bits) where none is."""
+    T, k, E, H, I = 20, 2, 4, 64, 32
+    ids, w, X = up(spread(T, k, E)), torch.full((T, k), 0.5, device=dev()), normal((T, H), 1).to(dev())
+    gu, dn = normal((E, 2 * I, H), 2, 0.2).to(dev()), normal((E, H, I), 3, 0.2).to(dev())
+    out = moe.moe_train(X, ids, w, gu, dn, int4=True, B=16)
+    assert torch.equal(out, moe.moe_train(X, ids, w, gu, dn, int4=True))
+    for i in range(4):
+        leaves = [t.clone().requires_grad_(n == i) for n, t in enumerate((X, w, gu, dn))]
+        with pytest.raises(ValueError):
+            moe.moe_train(leaves[0], ids, *leaves[1:], int4=True, B=16)
+        with torch.no_grad():
+            assert torch.equal(out, moe.moe_train(leaves[0], ids, *leaves[1:], int4=True, B=16))

@@ -1,0 +1,34 @@
+"""What the training layers refuse in the forward since their backward could not compute
+it.  Sizes only: no GPU."""
+
+import pytest
+
+from int4_weight_only_amd import moe
+
+
+def moe_sizes(T=32, k=4, E=8, H=128, I=64, B=64, checkpoint=False, x=True, up=True, dn=True):
+    return moe.check_moe_backward(T, k, E, H, I, B, checkpoint, x, up, dn)
+
+
+@pytest.mark.parametrize("checkpoint", [False, True])
+def test_moe_train_sizes(checkpoint):
+    for good in (dict(), dict(B=1024), dict(B=192), dict(T=0), dict(T=1, k=1, E=1, H=16, I=8),
+                 dict(T=4096, k=8, E=384, H=7168, I=2048, B=128)):
+        moe_sizes(checkpoint=checkpoint, **good)
+    for bad in (dict(B=16), dict(B=32), dict(B=96), dict(B=1088), dict(B=16, T=0), dict(E=1025)):
+        with pytest.raises(ValueError):
+            moe_sizes(checkpoint=checkpoint, **bad)
+
+
+def test_moe_train_limits_of_each_gradient():
+    """The weight gradients take 2^28 slots, the products more; rows of 2^34 elements nothing."""
+    slots = dict(T=1 << 25, k=8, E=1, H=32, I=16)
+    for want in (dict(up=False), dict(dn=False)):
+        with pytest.raises(ValueError, match="weight gradient"):
+            moe_sizes(**slots, **want)
+    moe_sizes(**slots, up=False, dn=False)
+    moe_sizes(**{**slots, "T": (1 << 25) - 8})
+    rows = dict(T=1 << 20, k=16, E=1, H=64, I=512)            # dH1: 2^24 rows of 1024
+    with pytest.raises(ValueError, match="product"):
+        moe_sizes(**rows, up=False, dn=False)
+    moe_sizes(**rows, x=False, up=False)
