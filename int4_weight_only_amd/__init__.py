@@ -1187,6 +1187,13 @@ def w4_bf16_gemm_tn(A, B, SB=None, out=None, workspace=None):
     return out
 
 
+@functools.lru_cache(1024)
+def check_checkpoint_wgrad(M, N, K):
+    """Refuses in the forward a linear layer's weight gradient that ``w4_bf16_gemm_tn``
+    could not compute from codes [M, K]: ValueError."""
+    _check_sizes("the weight gradient from a checkpoint", "w4_bf16_gemm_tn", None, None, 16, None, M, N, K, None)
+
+
 def w4_silu_mul_bwd(H1, dA, weights=None, SH=None, dH1=None, A=None, dw=None):
     """Gradient of the SwiGLU and of the top-k weight behind it: (dH1 bf16 [R,
     2I], A bf16 [R, I], dw fp32 [R]).

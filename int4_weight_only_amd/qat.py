@@ -36,8 +36,8 @@ gradient do not change.
 
 import torch
 
-from . import (_gradient, w4_bf16_gemm_nt, w4_bf16_gemm_tn, w4_bf16_transpose, w4_dequant_t, w4_fake_quant,
-               w4_quantize_pack, w4a16_gemm, w8_quantize_rows)
+from . import (_gradient, check_checkpoint_wgrad, w4_bf16_gemm_nt, w4_bf16_gemm_tn, w4_bf16_transpose,
+               w4_dequant_t, w4_fake_quant, w4_quantize_pack, w4a16_gemm, w8_quantize_rows)
 
 __all__ = ["FakeInt4STE", "fake_quant_ste", "Int4QATLinear", "qat_linear"]
 
@@ -71,12 +71,15 @@ class Int4QATLinear(torch.autograd.Function):
             raise ValueError(f"X has {X.shape[-1]} features, W expects {K}")
         W = W.contiguous()
         X2 = X.reshape(-1, K).contiguous()
+        keep = checkpoint and grad and ctx.needs_input_grad[1]
+        if keep:
+            if N % 8:
+                raise ValueError(f"the weight gradient from a checkpoint needs N % 8 == 0 (N = {N})")
+            check_checkpoint_wgrad(X2.shape[0], N, K)
         Wq, S = w4_quantize_pack(W)
         Y = w4a16_gemm(X2, Wq, S)
         SX = None
-        if checkpoint and grad and ctx.needs_input_grad[1]:
-            if N % 8:
-                raise ValueError(f"the weight gradient from a checkpoint needs N % 8 == 0 (N = {N})")
+        if keep:
             X2, SX = w8_quantize_rows(X2)
         ctx.save_for_backward(X2, SX, Wq, S)
         ctx.x_shape = X.shape

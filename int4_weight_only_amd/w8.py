@@ -24,8 +24,8 @@ capture a backward into a graph, take gradients with
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (_gradient, w4_bf16_gemm_nt, w4_bf16_gemm_tn, w4_bf16_transpose, w8_quantize_blocks,
-               w8_quantize_rows, w8a8_gemm)
+from . import (_gradient, check_checkpoint_wgrad, w4_bf16_gemm_nt, w4_bf16_gemm_tn, w4_bf16_transpose,
+               w8_quantize_blocks, w8_quantize_rows, w8a8_gemm)
 
 __all__ = ["W8Linear", "w8_linear"]
 
@@ -53,6 +53,8 @@ class W8Linear(torch.autograd.Function):
             raise ValueError(f"the W8A8 input gradient needs N % 16 == 0 (N = {N})")
         if need_dw and checkpoint and N % 8:
             raise ValueError(f"the weight gradient from a checkpoint needs N % 8 == 0 (N = {N})")
+        if need_dw and checkpoint:
+            check_checkpoint_wgrad(X2.shape[0], N, K)
         if need_dw and not checkpoint and min(256, max(N, K)) * _padded(X2.shape[0]) * 2 >= 1 << 31:
             raise ValueError(f"the W8A8 weight gradient covers fewer than 2^22 tokens, got {X2.shape[0]}")
         W8, SW, WT8, ST = w8_quantize_blocks(W, transposed=need_dx)

@@ -3,6 +3,7 @@ it.  Sizes only: no GPU."""
 
 import pytest
 
+import int4_weight_only_amd as w4
 from int4_weight_only_amd import moe
 
 
@@ -32,3 +33,45 @@ def test_moe_train_limits_of_each_gradient():
     with pytest.raises(ValueError, match="product"):
         moe_sizes(**rows, up=False, dn=False)
     moe_sizes(**rows, x=False, up=False)
+
+
+class Huge:
+    """A bf16 matrix of M rows, as far as the linear layers' checks look at it."""
+
+    def __init__(self, M, K):
+        self.shape = (M, K)
+
+    def reshape(self, *shape):
+        return self
+
+    def contiguous(self):
+        return self
+
+
+class Context:
+    needs_input_grad = (True, True, False, False)
+
+
+@pytest.mark.parametrize("M,K", [((1 << 30) + 16, 64), (1 << 29, 32), (1 << 24, 1024)])
+def test_linear_checkpoint_limits(M, K, monkeypatch):
+    """Rows, scales and elements past what the product from codes takes, before anything runs."""
+    from int4_weight_only_amd import qat, w8
+
+    def ran(*a, **k):
+        raise AssertionError("a kernel before the refusal")
+    for module, names in ((w8, ("w8_quantize_blocks", "w8_quantize_rows", "w8a8_gemm")),
+                          (qat, ("w4_quantize_pack", "w8_quantize_rows", "w4a16_gemm"))):
+        for n in names:
+            monkeypatch.setattr(module, n, ran)
+    with pytest.raises(ValueError, match="from a checkpoint"):
+        w8.W8Linear.forward(Context(), Huge(M, K), Huge(64, K), True, True)
+    with pytest.raises(ValueError, match="from a checkpoint"):
+        qat.Int4QATLinear.forward(Context(), Huge(M, K), Huge(64, K), True, True)
+
+
+def test_linear_checkpoint_sizes_that_are_taken():
+    """dY and the codes: fewer than 2^34 elements each."""
+    for M, N, K in ((0, 16, 32), (1, 8, 16), ((1 << 22) - 1, 4096, 4080), ((1 << 29) - 1, 8, 16)):
+        w4.check_checkpoint_wgrad(M, N, K)
+    with pytest.raises(ValueError):
+        w4.check_checkpoint_wgrad(1 << 22, 4096, 4080)
