@@ -709,8 +709,9 @@ int32_t w4_bf16_pick_block_size(int64_t T, int32_t k, int32_t E);
  * not overlap in time); or NULL.  With it few results of long sums are computed in
  * parts, faster, whose order of addition differs from the call's without.
  *
- * w4_bf16_moe_gemm_workspace -- its size in fp32 values; 0: no use for one; -1 on sizes
- * that the call refuses.
+ * w4_bf16_moe_gemm_workspace -- its size in fp32 values, by these sizes alone (the same
+ * whatever the current device); 0: no use for one; -1 on sizes that are negative, zero or
+ * past the limits (the multiples that a call asks for are its own check).
  */
 int64_t w4_bf16_moe_gemm_workspace(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B);
 int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted_token_ids,

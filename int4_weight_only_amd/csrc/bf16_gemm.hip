@@ -1045,8 +1045,13 @@ constexpr Kind kKinds[] = {
 };
 constexpr int kKindCount = 4;
 
+// The estimates count the MI355X's compute units, whatever the current device has: a
+// workspace is sized before the launch, perhaps with another device current, and both have
+// to come to the same parts.
+constexpr int64_t kCUs = 256;
+
 float estimate(const Kind& t, int64_t tiles, float steps, bool sums) {
-  const int64_t cus = cu_count(), mine = (tiles + cus - 1) / cus;
+  const int64_t mine = (tiles + kCUs - 1) / kCUs;
   const int64_t waves = (mine + t.occupancy - 1) / t.occupancy;
   const float busy = (float)mine * (t.fixed[sums] + steps * t.step[sums]);
   const float alone = (float)waves * (t.latency[sums] + steps * t.latency_step[sums]);
@@ -1058,7 +1063,7 @@ float estimate(const Kind& t, int64_t tiles, float steps, bool sums) {
 // large results (64 x [2816, 2048] over 256 pairs each: 396 us, 432 in 128 x 128 tiles;
 // over 2050 x 6 pairs on 48 of [2808, 2064], the two are even and it loses 8%).
 float estimate_short(int run, int64_t workgroups, float steps) {
-  const int64_t cus = cu_count(), mine = (workgroups + cus - 1) / cus, waves = (mine + 1) / 2;
+  const int64_t mine = (workgroups + kCUs - 1) / kCUs, waves = (mine + 1) / 2;
   const float busy = ((float)mine + 0.25f) * (0.7f + (float)run * (1.1f + 0.65f * steps));
   const float alone = (float)waves * (3.2f + (float)run * (0.35f + 0.9f * steps));
   return 3.0f + std::max(busy, alone);
