@@ -13,15 +13,17 @@ namespace w4 {
 namespace {
 
 struct Point {
-  float dg, du, a;
+  float dg, du, a, wa;     // a without the weight, and with it
 };
 
-// One element, G without the weight.  The sigmoid is formed as in
-// silu_mul_fast: from t = -g log2 e = 120 on it carries 2^136, which each result
-// gives back as 2^-34 with u and G and the rest at the end, so that products in
-// the normal range keep their value where the sigmoid alone is below it, and no
-// partial product passes the range where the result does not.
-__device__ __forceinline__ Point swiglu_point(float g, float u, float G) {
+// One element; G without the weight w.  The sigmoid is formed as in silu_mul_fast: from
+// t = -g log2 e = 120 on it carries 2^136, which the other factors give back piece by
+// piece.  dg = s (1 + g (1 - s)) times the larger of u and w G, then the smaller: the first
+// product is at most 1.1 times the larger factor (nearer gates halve it) and does not pass
+// below the range before the result does.  So where w G, w u, g s u and the result lie in
+// fp32's normal range, no partial product leaves it; gates below -181 give zeros (u and w G
+// would have to be above 2^64 both for more).
+__device__ __forceinline__ Point swiglu_point(float g, float u, float G, float w) {
   constexpr float kLog2e = 1.44269502f, kRest = 1.92596299e-8f, kLn2 = 0.693147182f;
   const float c = __builtin_amdgcn_fmed3f(g, -1024.0f, 1024.0f);
   const float t = -c * kLog2e;
@@ -29,12 +31,14 @@ __device__ __forceinline__ Point swiglu_point(float g, float u, float G) {
   const bool far = t > 120.0f;
   const float e = __builtin_amdgcn_exp2f(far ? t - 136.0f : t) * __builtin_fmaf(r, kLn2, 1.0f);
   const float q = __builtin_amdgcn_rcpf(e + (far ? 0x1p-136f : 1.0f));   // the sigmoid, or 2^136 times it
-  const float part = far ? 0x1p-34f : 1.0f, tail = far ? 0x1p-102f : 1.0f;
   // 1 - s = e^-g / (1 + e^-g): no cancellation for large g
   const float rest = far ? 1.0f : e * q;
-  const float gs = g * q, us = u * part, Gs = G * part;
-  return {us * (q * __builtin_fmaf(g, rest, 1.0f)) * Gs * (far ? 0x1p-68f : 1.0f), Gs * gs * tail,
-          us * gs * tail};
+  const float gs = g * q, us = u * (far ? 0x1p-34f : 1.0f), tail = far ? 0x1p-102f : 1.0f;
+  const float Gw = w * G, part = far ? 0x1p-51f : 1.0f;
+  const bool more = __builtin_fabsf(u) > __builtin_fabsf(Gw);
+  const float big = more ? u : Gw, small = more ? Gw : u;
+  return {q * __builtin_fmaf(g, rest, 1.0f) * (big * (far ? 0x1p-34f : 0.5f)) * part * (small * part) * (far ? 1.0f : 2.0f),
+          Gw * part * gs * (far ? 0x1p-85f : 1.0f), us * gs * tail, w * us * gs * tail};
 }
 
 template <bool C8>
@@ -95,11 +99,11 @@ __global__ __launch_bounds__(256) void k_silu_mul_bwd(Bf16Rows H1, const uint16_
       load8<false>({dA, nullptr}, row, I, i, d);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const Point p = swiglu_point(g[q], u[q], d[q]);
+        const Point p = swiglu_point(g[q], u[q], d[q], w);
         sum = __builtin_fmaf(d[q], p.a, sum);
-        dg[q] = w * p.dg;
-        du[q] = w * p.du;
-        a[q] = w * p.a;
+        dg[q] = p.dg;
+        du[q] = p.du;
+        a[q] = p.wa;
       }
       *(u32x4*)(dH1 + row * 2 * I + i) = pack8(dg);
       *(u32x4*)(dH1 + row * 2 * I + I + i) = pack8(du);

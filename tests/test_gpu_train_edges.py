@@ -12,8 +12,11 @@ from gpu_util import dev, say, up
 from int4_weight_only_amd import moe
 from int4_weight_only_amd.qat import qat_linear
 from int4_weight_only_amd.w8 import w8_linear
+from oracle import train
 
 pytestmark = pytest.mark.gpu
+
+HALF, TINY = 2.0 ** -8, 2.0 ** -133
 
 
 def normal(shape, seed, sigma=1.0):
@@ -70,3 +73,41 @@ def test_moe_train_refuses_in_the_forward_what_the_backward_does_not_take():
             moe.moe_train(leaves[0], ids, *leaves[1:], int4=True, B=16)
         with torch.no_grad():
             assert torch.equal(out, moe.moe_train(leaves[0], ids, *leaves[1:], int4=True, B=16))
+
+# ----------------------------------------------------------------------- SwiGLU's range --
+
+def test_silu_mul_bwd_large_factors():
+    """Products whose factors pass fp32's range together while the result does not: the weight
+    brings it back, the factor of u is above one, or the sigmoid lies below fp32's range."""
+    top = 255 * 2.0 ** 120                            # the largest bf16
+    rows = [(2.0 ** 30, 1.0, 2.0 ** 100, 2.0 ** -10),      # (g, u, dA, w)
+            (2.0 ** 30, 1.0, 2.0 ** 110, 2.0 ** -20), (2.40625, top, 2.0 ** -10, 2.0 ** -4),
+            (2.40625, -top, 2.0 ** -10, 2.0 ** -4), (1.5, 2.0 ** -20, top, 2.0 ** -3),
+            (-84.0, 2.0 ** 127, 2.0 ** 60, 1.0), (-84.0, top, 2.0 ** 90, 2.0 ** -4),
+            (-100.0, 2.0 ** 120, 2.0 ** 120, 2.0 ** -5), (-84.0, 2.0 ** -20, 2.0 ** 100, 0.5),
+            (-84.0, 2.0 ** 100, 2.0 ** -20, 0.5), (-150.0, 2.0 ** 127, 2.0 ** 20, 0.5),
+            (2.0 ** 70, 2.0 ** 70, 2.0 ** -60, 2.0 ** -20), (0.5, 2.0 ** -60, 2.0 ** 126, 0.25),
+            (-80.0, 2.0 ** 10, 2.0 ** -20, 0.5)]
+    I = 8
+    v = np.array(rows)
+    H1 = torch.from_numpy(np.concatenate([np.repeat(v[:, :1], I, 1), np.repeat(v[:, 1:2], I, 1)], 1)).to(torch.bfloat16)
+    G = torch.from_numpy(np.repeat(v[:, 2:3], I, 1)).to(torch.bfloat16)
+    w = torch.from_numpy(v[:, 3].astype(np.float32))
+    assert np.array_equal(H1.double().numpy()[:, [0, I]], v[:, :2]) and np.array_equal(G.double().numpy()[:, 0], v[:, 2])
+    got = w4.w4_silu_mul_bwd(H1.to(dev()), G.to(dev()), weights=w.to(dev()))
+    dh, a, _, _ = train.silu_mul_bwd(H1.double().numpy(), G.double().numpy(), v[:, 3])
+    # the sigmoid and each product are good to a few units in the last place of fp32; 1 + g (1 - s)
+    # does not cancel at these gates; results below 2^-126 are rounded to steps of 2^-133
+    units = 16 * 2.0 ** -24
+    for name, y, want in (("dH1", got[0], dh), ("A", got[1], a)):
+        y = y.double().cpu().numpy()
+        for r, row in enumerate(rows):
+            if name == "A":
+                parts = [("A", slice(0, I))]
+            else:
+                parts = [("dg", slice(0, I)), ("du", slice(I, 2 * I))]
+            for what, at in parts:
+                x, t = y[r, at], want[r, at]
+                assert np.isfinite(t).all() and (np.abs(t) < 2.0 ** 127).all()
+                tol = (HALF + units) * np.abs(t) + 2.0 ** -126 * (np.abs(t) < 2.0 ** -126) + TINY
+                assert (np.abs(x - t) <= tol).all(), f"{what} of {row}: {x[0]} for {t[0]}"
