@@ -714,6 +714,16 @@ int32_t w4_bf16_pick_block_size(int64_t T, int32_t k, int32_t E);
  * past the limits (the multiples that a call asks for are its own check).
  */
 int64_t w4_bf16_moe_gemm_workspace(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B);
+/*
+ * w4_bf16_moe_gemm_tile, w4_bf16_moe_wgrad_tile -- the results that a workgroup computes
+ * in a call of these sizes that has its workspace, rows << 16 | columns (for profiles and
+ * for tests that mean to reach each kernel); w4_bf16_gemm_tn's are those of a weight
+ * gradient with T = M, k = E = 1.  128 rows by 256 columns and more are a run of 128 x 128
+ * tiles.  Operands of 2 GiB and more take 64 x 64 for 64 x 128, and 256 x 256 for runs.
+ * 0: nothing to compute; -1 as the workspaces' sizes.
+ */
+int32_t w4_bf16_moe_gemm_tile(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B);
+int32_t w4_bf16_moe_wgrad_tile(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K);
 int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted_token_ids,
                      const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
                      uint16_t* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K,

@@ -47,6 +47,7 @@ __all__ = [
     "w8_pick_block_size", "w8a8_moe_gemm", "w8a8_moe_gemm_swiglu", "w4_moe_route_scored",
     "w4_moe_route_scored_bwd",
     "w4_bf16_pick_block_size", "w4_bf16_moe_gemm", "w4_bf16_moe_wgrad", "w4_bf16_gemm_tn",
+    "w4_bf16_moe_gemm_tile", "w4_bf16_moe_wgrad_tile",
     "w4_bf16_moe_gemm_workspace", "w4_bf16_moe_wgrad_workspace", "w4_bf16_gemm_tn_workspace", "w4_silu_mul_bwd",
 ]
 
@@ -1110,6 +1111,23 @@ def w4_bf16_gemm_tn_workspace(M, N, K):
     if n < 0:
         raise ValueError("invalid M, N or K")
     return n
+
+
+def _tile(v):
+    if v < 0:
+        raise ValueError("invalid sizes")
+    return v >> 16, v & 0xFFFF
+
+
+def w4_bf16_moe_gemm_tile(T, k, E, N, K, B):
+    """(rows, columns) that a workgroup of ``w4_bf16_moe_gemm`` computes."""
+    return _tile(_lib.load().w4_bf16_moe_gemm_tile(T, k, E, N, K, B))
+
+
+def w4_bf16_moe_wgrad_tile(T, k, E, N, K):
+    """(rows, columns) that a workgroup of ``w4_bf16_moe_wgrad`` computes, and with T = M, k = E =
+    1 one of ``w4_bf16_gemm_tn``; more than 128 columns in 128 rows: a run of tiles."""
+    return _tile(_lib.load().w4_bf16_moe_wgrad_tile(T, k, E, N, K))
 
 
 def _workspace(t, size, like):

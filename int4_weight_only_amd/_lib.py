@@ -76,6 +76,8 @@ SIGNATURES = {
     "w4_bf16_pick_block_size": (_i32, [_i64, _i32, _i32]),
     "w4_bf16_moe_gemm": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i64, _i64, _i32,
                                         _i32, _i32, _p, _p]),
+    "w4_bf16_moe_gemm_tile": (_i32, [_i64, _i32, _i32, _i64, _i64, _i32]),
+    "w4_bf16_moe_wgrad_tile": (_i32, [_i64, _i32, _i32, _i64, _i64]),
     "w4_bf16_moe_gemm_workspace": (_i64, [_i64, _i32, _i32, _i64, _i64, _i32]),
     "w4_bf16_moe_wgrad": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i64, _i64,
                                          _i32, _i32, _i32, _p, _p]),

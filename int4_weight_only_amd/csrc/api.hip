@@ -833,6 +833,11 @@ int64_t w4_bf16_moe_gemm_workspace(int64_t T, int32_t k, int32_t E, int64_t N, i
   return T == 0 ? 0 : w4::bf16_moe_workspace(T * k, E, N, K, B);
 }
 
+int32_t w4_bf16_moe_gemm_tile(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K, int32_t B) {
+  if (w4_bf16_moe_gemm_workspace(T, k, E, N, K, B) < 0) return -1;
+  return T == 0 ? 0 : w4::bf16_moe_tile(T * k, E, N, K, B);
+}
+
 int w4_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, const int32_t* sorted_token_ids,
                      const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
                      uint16_t* Y, int64_t T, int32_t k, int32_t E, int64_t N, int64_t K,
@@ -886,6 +891,11 @@ int64_t w4_bf16_moe_wgrad_workspace(int64_t T, int32_t k, int32_t E, int64_t N, 
       K > kBf16MaxCols || E > 1024 || T * k > kBf16MaxSumSlots || E * (N * K) > kMaxElems)
     return -1;
   return w4::bf16_sums_workspace(E, T * k / E, N, K);
+}
+
+int32_t w4_bf16_moe_wgrad_tile(int64_t T, int32_t k, int32_t E, int64_t N, int64_t K) {
+  if (w4_bf16_moe_wgrad_workspace(T, k, E, N, K) < 0) return -1;
+  return w4::bf16_sums_tile(E, T * k / E, N, K);
 }
 
 int64_t w4_bf16_gemm_tn_workspace(int64_t M, int64_t N, int64_t K) {

@@ -28,6 +28,9 @@ int64_t bf16_wgrad_threads(int32_t E, int64_t N, int64_t K);
 // fp32 values of the partial sums that a call with a workspace is split into (0: not)
 int64_t bf16_moe_workspace(int64_t P, int32_t E, int64_t N, int64_t K, int32_t B);
 int64_t bf16_sums_workspace(int64_t groups, int64_t sum, int64_t N, int64_t K);
+// results of a workgroup, rows << 16 | columns, of a call with its workspace
+int32_t bf16_moe_tile(int64_t P, int32_t E, int64_t N, int64_t K, int32_t B);
+int32_t bf16_sums_tile(int64_t groups, int64_t sum, int64_t N, int64_t K);
 // Y[f] = X[f / div] W_e^T (W [E, N, K]) or, transposed, X[f / div] W_e (W [E, K, N])
 hipError_t launch_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, uint16_t* Y,
                                 const Bf16Plan& plan, int64_t N, int64_t K, int32_t div,

@@ -1194,6 +1194,18 @@ int64_t bf16_sums_workspace(int64_t groups, int64_t sum, int64_t N, int64_t K) {
   return splits == 1 ? 0 : groups * splits * N * K;
 }
 
+namespace {
+int32_t tile_of(const Choice& c) {
+  return c.run > 0 ? 128 << 16 | 128 * c.run : kKinds[c.kind].bm << 16 | kKinds[c.kind].bn;
+}
+}  // namespace
+int32_t bf16_moe_tile(int64_t P, int32_t E, int64_t N, int64_t K, int32_t B) {
+  return tile_of(choose(1, P, N, K, B, E, true));
+}
+int32_t bf16_sums_tile(int64_t groups, int64_t sum, int64_t N, int64_t K) {
+  return tile_of(choose_sums(groups, sum, N, K, true));
+}
+
 hipError_t launch_bf16_moe_gemm(const uint16_t* X, const uint16_t* W, uint16_t* Y,
                                 const Bf16Plan& plan, int64_t N, int64_t K, int32_t div,
                                 bool transposed, float* workspace, hipStream_t st) {
