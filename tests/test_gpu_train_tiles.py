@@ -108,3 +108,60 @@ def test_dense(M, N, K, tile, parts, codes):
     if codes:
         B, SB = w4.w8_quantize_rows(B)
     assert torch.equal(w4.w4_bf16_gemm_tn(A, B, SB=SB), want)
+
+
+# ------------------------------------------------------------------- 2 GiB and more --
+
+def marked(T, cols):
+    """Rows at both ends, around 2^30, 2^31 and 2^32 of one and two bytes, and between."""
+    rows = {*range(70), *range(T - 100, T), *range(0, T, 1009)}
+    for where in (1 << 29, 1 << 30, 1 << 31):
+        rows |= {r for r in range(where // cols - 20, where // cols + 20) if 0 <= r < T}
+    return torch.tensor(sorted(rows), device=dev())
+
+
+@pytest.mark.parametrize("T,N,K,B,tile", tt.WIDE_ROWS)
+@pytest.mark.parametrize("transposed", [False, True])
+def test_wide_rows(T, N, K, B, tile, transposed):
+    say(f"wide rows T={T} N={N} K={K} B={B} tile={tile} transposed={transposed}")
+    E = 2
+    X, W = whole((T, K), 1), whole((E, K, N) if transposed else (E, N, K), 2)
+    ids = torch.randint(0, E, (T, 1), generator=torch.Generator().manual_seed(3), dtype=torch.int32).to(dev())
+    Y = w4.w4_bf16_moe_gemm(X, W, *w4.moe_align_block_size(ids, E, B), T, 1, B, 1, transposed=transposed)
+    w = [(W[e] if transposed else W[e].t()).float().contiguous() for e in range(E)]
+    for first in range(0, T, 1 << 14):
+        x, one = X[first:first + (1 << 14)].float(), ids[first:first + (1 << 14)] == 1
+        want = torch.where(one, x @ w[1], x @ w[0])
+        assert torch.equal(Y[first:first + (1 << 14)], rounded(want)), first
+
+
+@pytest.mark.parametrize("T,N,K,transposed,tile", tt.WIDE_WEIGHTS)
+def test_wide_weights(T, N, K, transposed, tile):
+    say(f"wide weights T={T} N={N} K={K} transposed={transposed}")
+    cols = marked(K, N if transposed else 1)[::2]     # of X: rows of W where it lies across
+    X = torch.zeros((T, K), dtype=torch.bfloat16, device=dev())
+    X[:, cols] = whole((T, cols.numel()), 1)
+    W = whole((1, K, N) if transposed else (1, N, K), 2)
+    ids = torch.zeros((T, 1), dtype=torch.int32, device=dev())
+    Y = w4.w4_bf16_moe_gemm(X, W, *w4.moe_align_block_size(ids, 1, 64), T, 1, 64, 1, transposed=transposed)
+    w = W[0][cols].double() if transposed else W[0][:, cols].double().t().contiguous()
+    assert torch.equal(Y, rounded(X[:, cols].double() @ w))
+
+
+@pytest.mark.parametrize("T,E,N,K,codes,tile", tt.WIDE_SUMS)
+def test_wide_sums(T, E, N, K, codes, tile):
+    say(f"wide sums T={T} E={E} N={N} K={K} codes={codes} tile={tile}")
+    rows = marked(T, max(N, K))
+    A, B, SB = whole((T, N), 1), whole((T, K), 2), None
+    if N < K:                                         # the narrow operand holds the zeros
+        A = at(rows, A)
+    else:
+        B = at(rows, B)
+    ids = torch.randint(0, E, (T, 1), generator=torch.Generator().manual_seed(3), dtype=torch.int32).to(dev())
+    want = grouped_sums(ids, E, A, B, 1, 1, rows)
+    if codes:
+        B, SB = w4.w8_quantize_rows(B)
+    plan = w4.moe_align_block_size(ids, E, 256)
+    assert torch.equal(w4.w4_bf16_moe_wgrad(A, B, *plan, E, T, 1, 256, 1, 1, SX=SB), want)
+    if E == 1:
+        assert torch.equal(w4.w4_bf16_gemm_tn(A, B, SB=SB), want[0])

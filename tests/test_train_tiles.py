@@ -23,6 +23,13 @@ def test_sizes_reach_their_kernels():
     for M, N, K, tile, parts in tt.DENSE:
         assert sums(M, 1, 1, N, K) == (tile, parts), (M, N, K)
         assert (w4.w4_bf16_gemm_tn_workspace(M, N, K) > 0) == parts
+    for T, N, K, B, tile in tt.WIDE_ROWS:
+        assert T * K >= 1 << 30 and rows(T, 1, 2, N, K, B)[0] == tile, (T, N, K)
+    for T, N, K, transposed, tile in tt.WIDE_WEIGHTS:
+        assert (N if transposed else min(N, 256)) * K >= 1 << 30 and rows(T, 1, 1, N, K, 64) == (tile, True)
+    for T, E, N, K, codes, tile in tt.WIDE_SUMS:
+        assert T * max(N, K) >= 1 << 30 and sums(T, 1, E, N, K)[0] == tile, (T, E, N, K)
+    assert any(codes and T * K >= 1 << 31 for T, _, _, K, codes, _ in tt.WIDE_SUMS)
 
 
 def test_every_kernel_is_reached():
@@ -31,6 +38,11 @@ def test_every_kernel_is_reached():
     assert {min(c[-2], (128, 256)) if c[-2][0] == 128 and c[-2][1] > 128 else c[-2] for c in tt.SUMS} == tiles | {(128, 256)}
     assert {c[-2] for c in tt.DENSE} == tiles | {(128, 256)}
     assert any(c[-1] for c in tt.ROWS) and any(c[-1] for c in tt.SUMS) and any(c[-1] for c in tt.DENSE)
+    wide = {(64, 64): (64, 64), (64, 128): (64, 64), (128, 128): (128, 128), (256, 256): (256, 256)}
+    assert {wide[c[-1]] for c in tt.WIDE_ROWS} == set(wide.values())
+    # run bf16 and from codes where the codes are wide too
+    for one in (True, False):
+        assert {wide[c[-1]] for c in tt.WIDE_SUMS if (c[1] == 1) == one} == set(wide.values())
 
 
 def test_tiles_of_invalid_sizes():

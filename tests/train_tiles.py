@@ -41,3 +41,32 @@ DENSE = [
     (8200, 4104, 2064, (256, 256), False),
     (64, 4104, 4112, (128, 256), False),
 ]
+
+# operands of 2 GiB and more.  (T, N, K, B, tile): rows of X, either way round
+WIDE = (1 << 17) + 40                                 # rows of 8208 columns: 2^31 bytes and more
+WIDE_ROWS = [
+    (WIDE, 136, 8208, 64, (64, 64)),
+    (WIDE, 264, 8208, 128, (128, 128)),
+    (WIDE, 520, 8208, 256, (256, 256)),
+]
+# (T, N, K, transposed, tile): one expert's weights, in parts
+WIDE_WEIGHTS = [
+    (40, 8208, 131080, True, (64, 128)),
+    (4, 264, 1 << 22, False, (64, 64)),
+]
+# (rows, E, N, K, codes, tile): sums; of one expert, the dense ones too.  A has N columns, B K
+WIDE_SUMS = [
+    (WIDE, 1, 64, 8208, False, (64, 128)),            # taken as 64 x 64
+    (WIDE, 1, 200, 8208, False, (128, 128)),
+    (WIDE, 1, 1280, 8208, False, (256, 256)),
+    (WIDE, 1, 8208, 16, False, (64, 64)),
+    (WIDE, 1, 8208, 208, True, (128, 128)),
+    (WIDE, 1, 8208, 1264, False, (256, 256)),
+    (WIDE, 2, 200, 8208, False, (128, 128)),
+    (WIDE, 2, 520, 8208, False, (256, 256)),
+    (WIDE, 2, 8208, 16, True, (64, 64)),
+    (2 * WIDE, 1, 8, 8208, True, (64, 128)),          # 2^31 codes and more
+    (2 * WIDE, 1, 200, 8208, True, (128, 128)),
+    (2 * WIDE, 2, 200, 8208, True, (128, 128)),
+    (2 * WIDE, 2, 1296, 8208, True, (256, 256)),
+]
