@@ -1074,6 +1074,8 @@ def _bf16_plan(sorted_token_ids, expert_ids, num_tokens_post_padded, T, k, E, B,
 
 def _pair_rows(t, name, dtype, T, k, div, device=None):
     """(device, columns) of an operand with a row per ``div`` pairs."""
+    if T < 0 or k < 1:
+        raise ValueError("invalid T or k")
     if div != 1 and div != k:
         raise ValueError(f"{name}'s row divisor must be 1 or k")
     device = _in(t, name, dtype, 2, device)

@@ -2,6 +2,7 @@
 it.  Sizes only: no GPU."""
 
 import pytest
+import torch
 
 import int4_weight_only_amd as w4
 from int4_weight_only_amd import moe
@@ -75,3 +76,14 @@ def test_linear_checkpoint_sizes_that_are_taken():
         w4.check_checkpoint_wgrad(M, N, K)
     with pytest.raises(ValueError):
         w4.check_checkpoint_wgrad(1 << 22, 4096, 4080)
+
+
+def test_no_pairs_per_token_is_refused_as_an_argument():
+    """k = 0 with its divisor: not a division by zero."""
+    x = torch.zeros((0, 64), dtype=torch.bfloat16, device="meta")
+    i = torch.zeros(64, dtype=torch.int32, device="meta")
+    for T, k in ((4, 0), (-1, 1)):
+        with pytest.raises(ValueError, match="T or k"):
+            w4.w4_bf16_moe_gemm(x, x.view(1, 0, 64), i, i, i, T, k, 64, k)
+        with pytest.raises(ValueError, match="T or k"):
+            w4.w4_bf16_moe_wgrad(x, x, i, i, i, 1, T, k, 64, k, 1)
