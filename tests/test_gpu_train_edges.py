@@ -111,3 +111,57 @@ def test_silu_mul_bwd_large_factors():
                 assert np.isfinite(t).all() and (np.abs(t) < 2.0 ** 127).all()
                 tol = (HALF + units) * np.abs(t) + 2.0 ** -126 * (np.abs(t) < 2.0 ** -126) + TINY
                 assert (np.abs(x - t) <= tol).all(), f"{what} of {row}: {x[0]} for {t[0]}"
+
+
+# ------------------------------------------------------------ rows that are not finite --
+
+# the tile kernels (few columns, and sums in parts) and the runs of tiles
+@pytest.mark.parametrize("T,k,E,N,K", [(300, 2, 8, 72, 144), (1500, 2, 6, 520, 1040), (96, 2, 32, 1032, 1040),
+                                       (4000, 1, 4, 64, 144)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("side", ["gate_up", "down"])
+def test_checkpoint_row_that_is_not_finite(T, k, E, N, K, value, side):
+    """The first row of X holds a value that is not finite, so that its 128 codes and their scale
+    are NaN: only the gradients of the experts that the row goes to may see it."""
+    say(f"checkpoint row not finite T={T} k={k} E={E} N={N} K={K} {value} {side}")
+    ids = spread(T, k, E)
+    dd, dx = (1, k) if side == "gate_up" else (k, 1)
+    used = set(ids[0]) if side == "gate_up" else {ids[0, 0]}
+    dY, X = normal((T * k // dd, N), 1).to(dev()), normal((T * k // dx, K), 2).to(dev())
+    B = w4.w4_bf16_pick_block_size(T, k, E)
+    plan = w4.moe_align_block_size(up(ids), E, B)
+
+    def grad():
+        X8, SX = w4.w8_quantize_rows(X)
+        return w4.w4_bf16_moe_wgrad(dY, X8, *plan, E, T, k, B, dd, dx, SX=SX)
+    clean = grad()
+    X[0, 5] = value
+    got = grad()
+    for e in range(E):
+        if e in used:
+            assert torch.equal(got[e][:, 128:], clean[e][:, 128:]), e
+            assert bool(got[e][:, :128].isnan().all()), e
+        else:
+            assert torch.equal(got[e], clean[e]), e
+
+
+def test_layer_of_checkpoints_with_a_token_that_is_not_finite():
+    """A token that is not finite reaches the gradients of its own experts only."""
+    T, k, E, H, I = 70, 2, 8, 128, 64
+    ids = spread(T, k, E)
+    w = torch.full((T, k), 0.5, device=dev())
+    X, gu, dn = normal((T, H), 1).to(dev()), normal((E, 2 * I, H), 2, 0.2).to(dev()), normal((E, H, I), 3, 0.2).to(dev())
+    dO = normal((T, H), 4).to(dev())
+    dO[0] = 0
+
+    def grads():
+        leaves = [t.clone().requires_grad_() for t in (X, gu, dn)]
+        out = moe.moe_train(leaves[0], up(ids), w, *leaves[1:], checkpoint=True)
+        return torch.autograd.grad(out, leaves, dO)
+    clean = grads()
+    X[0, 3] = float("nan")
+    got = grads()
+    others = [e for e in range(E) if e not in ids[0]]
+    assert torch.equal(got[0][1:], clean[0][1:])
+    for a, b in zip(got[1:], clean[1:]):
+        assert torch.equal(a[others], b[others])
