@@ -165,3 +165,100 @@ def test_layer_of_checkpoints_with_a_token_that_is_not_finite():
     assert torch.equal(got[0][1:], clean[0][1:])
     for a, b in zip(got[1:], clean[1:]):
         assert torch.equal(a[others], b[others])
+
+
+# ---------------------------------------------------- how gradients come and go --
+
+def linear_case(kind, shape, N, seed=0):
+    X, W = normal((*shape, 64), seed + 1).to(dev()).requires_grad_(), normal((N, 64), seed + 2).to(dev()).requires_grad_()
+    call = w8_linear if kind == "w8" else qat_linear
+    return X, W, lambda x, w: call(x, w, checkpoint=True)
+
+
+def moe_case(T=40, k=2, E=4, H=64, I=32, seed=0, **kw):
+    ids = up(spread(T, k, E))
+    w = torch.rand((T, k), generator=torch.Generator().manual_seed(seed)).to(dev()).requires_grad_()
+    X, gu, dn = (normal(s, seed + i, sigma).to(dev()).requires_grad_()
+                 for i, (s, sigma) in enumerate((((T, H), 1.0), ((E, 2 * I, H), 0.2), ((E, H, I), 0.2))))
+    return (X, w, gu, dn), lambda X, w, gu, dn: moe.moe_train(X, ids, w, gu, dn, checkpoint=True, **kw)
+
+
+@pytest.mark.parametrize("layer", ["moe", "moe_int4", "w8", "int4"])
+def test_gradients_of_every_form(layer):
+    """Broadcast, transposed and fp32 gradients are those of the same values laid out plainly; a
+    graph can be walked twice."""
+    if layer.startswith("moe"):
+        leaves, f = moe_case(int4="int4" in layer)
+    else:
+        *leaves, f = linear_case(layer, (2, 20), 64)
+    y = f(*leaves)
+    plain = lambda g: torch.autograd.grad(y, leaves, g.contiguous(), retain_graph=True)
+    for z, g in ((y.sum(), torch.ones_like(y)), (y.transpose(0, -1).reshape(-1)[::2].sum(), None),
+                 (y.float().square().sum(), (2 * y.float()).to(torch.bfloat16))):
+        got = torch.autograd.grad(z, leaves, retain_graph=True)
+        if g is None:
+            g = torch.zeros_like(y.transpose(0, -1)).reshape(-1)
+            g[::2] = 1
+            g = g.view(y.transpose(0, -1).shape).transpose(0, -1)
+        for a, b in zip(got, plain(g)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["w8", "int4"])
+def test_linear_checkpoint_graph_replay(kind):
+    """Forward and backward from codes in a graph, replayed on new values."""
+    X, W, f = linear_case(kind, (300,), 272)
+    dY = normal((300, 272), 9).to(dev())
+
+    def step(x, w):
+        y = f(x, w)
+        return (y, *torch.autograd.grad(y, (x, w), dY))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(X, W)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(X, W)
+    for seed in (3, 4, 5):
+        with torch.no_grad():
+            X.copy_(normal((300, 64), seed))
+            W.copy_(normal((272, 64), seed + 10))
+            dY.copy_(normal((300, 272), seed + 20))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step(X.detach().clone().requires_grad_(), W.detach().clone().requires_grad_())):
+            assert torch.equal(a, b)
+
+
+def test_linear_checkpoint_of_no_rows_and_of_three_dimensions():
+    for kind in ("w8", "int4"):
+        X, W, f = linear_case(kind, (0,), 32)
+        dX, dW = torch.autograd.grad(f(X, W), (X, W), torch.empty((0, 32), dtype=torch.bfloat16, device=dev()))
+        assert dX.shape == X.shape and dW.shape == W.shape and not bool(dW.any())
+        X, W, f = linear_case(kind, (3, 7), 32)
+        dY = normal((3, 7, 32), 5).to(dev())
+        flat = X.detach().reshape(21, 64).requires_grad_()
+        for a, b in zip(torch.autograd.grad(f(X, W), (X, W), dY), torch.autograd.grad(f(flat, W), (flat, W), dY.view(21, 32))):
+            assert torch.equal(a.reshape(-1), b.reshape(-1))
+
+
+@pytest.mark.parametrize("R,I", [((1 << 23) + 37, 8), (70000, 16384)])
+@pytest.mark.parametrize("codes", [False, True])
+def test_silu_mul_bwd_of_many_rows(R, I, codes):
+    """More rows than workgroups, and more than 2^31 elements: the last rows are those of a call
+    of their own."""
+    say(f"silu_mul_bwd of many rows R={R} I={I} codes={codes}")
+    g = torch.Generator(device=dev()).manual_seed(1)
+    H1 = torch.randn((R, 2 * I), generator=g, device=dev(), dtype=torch.bfloat16)
+    G = torch.randn((R, I), generator=g, device=dev(), dtype=torch.bfloat16)
+    w, SH = torch.rand(R, generator=g, device=dev()), None
+    if codes:
+        H1, SH = w4.w8_quantize_rows(H1)
+    got = w4.w4_silu_mul_bwd(H1, G, weights=w, SH=SH)
+    for rows in (slice(0, 50), slice(R // 2, R // 2 + 50), slice(R - 50, R)):
+        few = w4.w4_silu_mul_bwd(H1[rows].clone(), G[rows].clone(), weights=w[rows].clone(), SH=None if SH is None else SH[rows].clone())
+        for a, b in zip(got, few):
+            assert torch.equal(a[rows], b)
