@@ -16,29 +16,36 @@ struct Point {
   float dg, du, a, wa;     // a without the weight, and with it
 };
 
-// One element; G without the weight w.  The sigmoid is formed as in silu_mul_fast: from
-// t = -g log2 e = 120 on it carries 2^136, which the other factors give back piece by
-// piece.  dg = s (1 + g (1 - s)) times the larger of u and w G, then the smaller: the first
-// product is at most 1.1 times the larger factor (nearer gates halve it) and does not pass
-// below the range before the result does.  So where w G, w u, g s u and the result lie in
-// fp32's normal range, no partial product leaves it; gates below -181 give zeros (u and w G
-// would have to be above 2^64 both for more).
+// One element; G without the weight w.  The exponential is that of silu_mul_fast.  u is
+// halved on the way to dg, since s (1 + g (1 - s)) reaches 1.1: with w G and w u below fp32's
+// largest value no partial product passes it where the result (for dw: a) does not.
+//
+// FAR: gates below kFar, whose sigmoid is near fp32's smallest values or below them.  It
+// carries 2^136, which the other factors give back piece by piece; dg takes the larger of
+// u and w G first, so that neither product passes the range before the result does.  Gates
+// below -181 give zeros (u and w G would have to be above 2^64 both for more).
+constexpr float kFar = -83.0f;
+
+template <bool FAR>
 __device__ __forceinline__ Point swiglu_point(float g, float u, float G, float w) {
   constexpr float kLog2e = 1.44269502f, kRest = 1.92596299e-8f, kLn2 = 0.693147182f;
   const float c = __builtin_amdgcn_fmed3f(g, -1024.0f, 1024.0f);
   const float t = -c * kLog2e;
   const float r = __builtin_fmaf(-c, kLog2e, -t) - c * kRest;
-  const bool far = t > 120.0f;
-  const float e = __builtin_amdgcn_exp2f(far ? t - 136.0f : t) * __builtin_fmaf(r, kLn2, 1.0f);
-  const float q = __builtin_amdgcn_rcpf(e + (far ? 0x1p-136f : 1.0f));   // the sigmoid, or 2^136 times it
-  // 1 - s = e^-g / (1 + e^-g): no cancellation for large g
-  const float rest = far ? 1.0f : e * q;
-  const float gs = g * q, us = u * (far ? 0x1p-34f : 1.0f), tail = far ? 0x1p-102f : 1.0f;
-  const float Gw = w * G, part = far ? 0x1p-51f : 1.0f;
-  const bool more = __builtin_fabsf(u) > __builtin_fabsf(Gw);
-  const float big = more ? u : Gw, small = more ? Gw : u;
-  return {q * __builtin_fmaf(g, rest, 1.0f) * (big * (far ? 0x1p-34f : 0.5f)) * part * (small * part) * (far ? 1.0f : 2.0f),
-          Gw * part * gs * (far ? 0x1p-85f : 1.0f), us * gs * tail, w * us * gs * tail};
+  const float e = __builtin_amdgcn_exp2f(FAR ? t - 136.0f : t) * __builtin_fmaf(r, kLn2, 1.0f);
+  const float q = __builtin_amdgcn_rcpf(e + (FAR ? 0x1p-136f : 1.0f));   // the sigmoid, or 2^136 times it
+  const float gs = g * q, Gw = w * G;
+  if constexpr (FAR) {                             // 1 - s is 1
+    const bool more = __builtin_fabsf(u) > __builtin_fabsf(Gw);
+    const float big = more ? u : Gw, small = more ? Gw : u;
+    const float us = u * 0x1p-34f;
+    return {q * (g + 1.0f) * (big * 0x1p-34f) * 0x1p-51f * (small * 0x1p-51f), Gw * 0x1p-51f * gs * 0x1p-85f,
+            us * gs * 0x1p-102f, w * us * gs * 0x1p-102f};
+  } else {
+    // 1 - s = e^-g / (1 + e^-g): no cancellation for large g
+    const float part = q * __builtin_fmaf(g, e * q, 1.0f);
+    return {0.5f * u * part * Gw * 2.0f, Gw * gs, u * gs, w * u * gs};
+  }
 }
 
 template <bool C8>
@@ -97,13 +104,24 @@ __global__ __launch_bounds__(256) void k_silu_mul_bwd(Bf16Rows H1, const uint16_
       load8<C8>(H1, row, 2 * I, i, g);
       load8<C8>(H1, row, 2 * I, I + i, u);
       load8<false>({dA, nullptr}, row, I, i, d);
+      Point p[8];
+      bool far = false;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const Point p = swiglu_point(g[q], u[q], d[q], w);
-        sum = __builtin_fmaf(d[q], p.a, sum);
-        dg[q] = p.dg;
-        du[q] = p.du;
-        a[q] = p.wa;
+        p[q] = swiglu_point<false>(g[q], u[q], d[q], w);
+        far |= g[q] < kFar;
+      }
+      if (far) {                                   // hardly ever
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (g[q] < kFar) p[q] = swiglu_point<true>(g[q], u[q], d[q], w);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        sum = __builtin_fmaf(d[q], p[q].a, sum);
+        dg[q] = p[q].dg;
+        du[q] = p[q].du;
+        a[q] = p[q].wa;
       }
       *(u32x4*)(dH1 + row * 2 * I + i) = pack8(dg);
       *(u32x4*)(dH1 + row * 2 * I + I + i) = pack8(du);
