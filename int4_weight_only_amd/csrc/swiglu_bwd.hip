@@ -76,6 +76,29 @@ __device__ __forceinline__ void load8(const Bf16Rows& o, int64_t row, int64_t co
   }
 }
 
+template <bool C8>
+__device__ __forceinline__ void load4(const Bf16Rows& o, int64_t row, int64_t cols, int64_t c, float* v) {
+  uint32_t lo, hi;
+  if constexpr (!C8) {
+    const u32x2 x = *(const u32x2*)((const uint16_t*)o.p + row * cols + c);
+    lo = x.x;
+    hi = x.y;
+  } else {
+    const uint32_t x = *(const uint32_t*)((const uint8_t*)o.p + row * cols + c);
+    const float s = __uint_as_float((uint32_t)o.scales[row * w8_cols(cols) + (c >> 7)] << 23);
+    lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, false));
+    hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, true));
+  }
+  v[0] = bf16_lo(lo);
+  v[1] = bf16_hi(lo);
+  v[2] = bf16_lo(hi);
+  v[3] = bf16_hi(hi);
+}
+
+__device__ __forceinline__ u32x2 pack4(const float* v) {
+  return u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+}
+
 __device__ __forceinline__ u32x4 pack8(const float* v) {
   return u32x4{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7])};
 }
@@ -84,10 +107,15 @@ __device__ __forceinline__ u32x4 pack8(const float* v) {
 
 // One workgroup per row, eight elements a thread and pass (16-byte loads and stores of
 // bf16, 8 of codes); dw's terms meet in a fixed order (a thread's own, its wave's by
-// exchange, the waves' in order), in fp32.  Memory bounds it: an element of I moves 10
-// bytes from codes, 12 from bf16 (with A), and 32775 rows of 2000 from codes take 115 us
-// (5.7 TB/s, above the copy rate since a stream that is mostly stores runs faster).
-// 64 rows of 2048: 4 us, a launch and a row's chain of loads.
+// exchange, the waves' in order), in fp32.  An element of I moves 10 bytes from codes, 12
+// from bf16 (with A).  Memory bounds rows of a thousand and more: 32775 rows of 2000 take
+// 115 us from codes (5.7 TB/s, above the copy rate since a stream that is mostly stores runs
+// faster) and 142 from bf16 (5.5).  Shorter rows leave threads without work, and their
+// beginnings bound it: 32768 rows of 768 49 us from codes, 60 from bf16 (5.0 TB/s), of 64
+// 32 and 30.  64 rows of 2048: 4 us, a launch and a row's chain of loads.
+// Far gates are computed apart, in fewer registers (scales selected for every element: 125
+// us, and 94 registers with both forms side by side); a hundredth of them among the 32775 x
+// 2000 gates makes it 162 us, nothing else 174.
 template <bool C8>
 __global__ __launch_bounds__(256) void k_silu_mul_bwd(Bf16Rows H1, const uint16_t* __restrict__ dA,
                                                       const float* __restrict__ weights, int64_t R,
@@ -104,24 +132,38 @@ __global__ __launch_bounds__(256) void k_silu_mul_bwd(Bf16Rows H1, const uint16_
       load8<C8>(H1, row, 2 * I, i, g);
       load8<C8>(H1, row, 2 * I, I + i, u);
       load8<false>({dA, nullptr}, row, I, i, d);
-      Point p[8];
       bool far = false;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        p[q] = swiglu_point<false>(g[q], u[q], d[q], w);
-        far |= g[q] < kFar;
-      }
-      if (far) {                                   // hardly ever
+      for (int q = 0; q < 8; ++q) far |= g[q] < kFar;
+      if (far) {                                   // hardly ever: four at a time, for the registers' sake
+        int c = (int)i;
+        asm volatile("" : "+v"(c));                // addresses formed here, not kept by every pass
+#pragma unroll 1
+        for (int last = c + 8; c < last; c += 4) {
+          load4<C8>(H1, row, 2 * I, c, g);
+          load4<C8>(H1, row, 2 * I, I + c, u);
+          load4<false>({dA, nullptr}, row, I, c, d);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (g[q] < kFar) p[q] = swiglu_point<true>(g[q], u[q], d[q], w);
+          for (int q = 0; q < 4; ++q) {
+            const Point p = g[q] < kFar ? swiglu_point<true>(g[q], u[q], d[q], w) : swiglu_point<false>(g[q], u[q], d[q], w);
+            sum = __builtin_fmaf(d[q], p.a, sum);
+            dg[q] = p.dg;
+            du[q] = p.du;
+            a[q] = p.wa;
+          }
+          *(u32x2*)(dH1 + row * 2 * I + c) = pack4(dg);
+          *(u32x2*)(dH1 + row * 2 * I + I + c) = pack4(du);
+          if (A) *(u32x2*)(A + row * I + c) = pack4(a);
+        }
+        continue;
       }
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        sum = __builtin_fmaf(d[q], p[q].a, sum);
-        dg[q] = p[q].dg;
-        du[q] = p[q].du;
-        a[q] = p[q].wa;
+        const Point p = swiglu_point<false>(g[q], u[q], d[q], w);
+        sum = __builtin_fmaf(d[q], p.a, sum);
+        dg[q] = p.dg;
+        du[q] = p.du;
+        a[q] = p.wa;
       }
       *(u32x4*)(dH1 + row * 2 * I + i) = pack8(dg);
       *(u32x4*)(dH1 + row * 2 * I + I + i) = pack8(du);
