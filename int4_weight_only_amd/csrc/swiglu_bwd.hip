@@ -108,11 +108,11 @@ __device__ __forceinline__ u32x4 pack8(const float* v) {
 // One workgroup per row, eight elements a thread and pass (16-byte loads and stores of
 // bf16, 8 of codes); dw's terms meet in a fixed order (a thread's own, its wave's by
 // exchange, the waves' in order), in fp32.  An element of I moves 10 bytes from codes, 12
-// from bf16 (with A).  Memory bounds rows of a thousand and more: 32775 rows of 2000 take
+// from bf16 (with A).  Memory bounds rows of about 500 and more: 32775 rows of 2000 take
 // 115 us from codes (5.7 TB/s, above the copy rate since a stream that is mostly stores runs
-// faster) and 142 from bf16 (5.5).  Shorter rows leave threads without work, and their
-// beginnings bound it: 32768 rows of 768 49 us from codes, 60 from bf16 (5.0 TB/s), of 64
-// 32 and 30.  64 rows of 2048: 4 us, a launch and a row's chain of loads.
+// faster) and 142 from bf16 (5.5), 32768 rows of 768 49 and 60.  Shorter rows leave threads
+// without work, and the beginning of a workgroup bounds them: 32768 rows of 256 39 and 36 us,
+// of 64 32 and 30.  64 rows of 2048: 4 us, a launch and a row's chain of loads.
 // Far gates are computed apart, in fewer registers (scales selected for every element: 125
 // us, and 94 registers with both forms side by side); a hundredth of them among the 32775 x
 // 2000 gates makes it 162 us, nothing else 174.

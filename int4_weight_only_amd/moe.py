@@ -556,15 +556,16 @@ def moe_train(X, topk_ids, topk_weights, gate_up, down, int4=False, checkpoint=F
     2I, H] and down bf16 [E, H, I], master weights.  ``int4``: the products run on
     the weights' INT4 codes, so that the output is ``moe_forward``'s bit for bit, and
     the straight-through estimator passes the gradient to the weights (H, I
-    multiples of 32).  ``checkpoint``: X and the gate_up product are kept for the
-    backward as e4m3 codes (``w8_quantize_rows``), half the bytes; the output does
-    not change, the gradients of the weights, of X and of the top-k weights are
-    those at the kept values (H, 2I multiples of 16).  Otherwise H, I multiples of
+    multiples of 32; X and the activations [T * k, I] below 2 GiB each, which the
+    layer without ``int4`` may exceed).  ``checkpoint``: X and the gate_up product are
+    kept for the backward as e4m3 codes (``w8_quantize_rows``), half the bytes; the
+    output does not change, the gradients of the weights, of X and of the top-k weights
+    are those at the kept values (H, 2I multiples of 16).  Otherwise H, I multiples of
     8.  B defaults to ``w4_bf16_pick_block_size``; sizes that the backward does not take
-    are refused here where a gradient is wanted (B a multiple of 64 up to 1024).  Returns out bf16 [T, H].  The
-    backward is not differentiable again.  To capture it into a graph, take
-    gradients with ``torch.autograd.grad``, or let no eager graph of the same leaves
-    be alive.
+    are refused here where a gradient is wanted (B a multiple of 64 up to 1024).
+    Returns out bf16 [T, H].  The backward is not differentiable again.  To capture it
+    into a graph, take gradients with ``torch.autograd.grad``, or let no eager graph of
+    the same leaves be alive.
     """
     device = _in(X, "X", torch.bfloat16, 2)
     T, H = X.shape
