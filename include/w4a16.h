@@ -777,8 +777,9 @@ int w4_bf16_gemm_tn(const uint16_t* A, const void* B, const uint8_t* SB, uint16_
  * the down product's output need be kept.  fp32 arithmetic, good to a few units
  * in the last place (dw: of the largest terms) where w * dA, w * u, g * s * u, u * s *
  * (1 + g * (1 - s)) and the result lie in fp32's normal range (s alone may lie below it);
- * gates below -181 give zeros.  H1 bf16 [R, 2I], or with SH a checkpoint of such rows (I
- * % 8 == 0 is enough for it here); dA, A bf16 [R, I], dH1 bf16 [R, 2I], all 16-byte aligned; weights, dw fp32 [R].  I % 8 == 0.
+ * gates below -181 give zeros.  H1 bf16 [R, 2I], or with SH a checkpoint of such rows
+ * (I % 8 == 0 is enough for it here); dA, A bf16 [R, I], dH1 bf16 [R, 2I], all 16-byte
+ * aligned; weights, dw fp32 [R].  I % 8 == 0.
  * R or I == 0 is a no-op, but for dw, which is written as zeros where I == 0.
  */
 int w4_silu_mul_bwd(const void* H1, const uint8_t* SH, const uint16_t* dA, const float* weights,

@@ -431,7 +431,7 @@ class RoutedExperts(torch.autograd.Function):
         # needs_input_grad goes by the inputs alone, also under torch.no_grad()
         need_x, need_w, need_up, need_dn = (n and grad for n in ctx.needs_input_grad[:4])
         if need_x or need_w or need_up or need_dn:
-            check_moe_backward(T, k, E, H, I, B, checkpoint, need_x, need_up, need_dn)
+            check_moe_backward(T, k, E, H, I, B, checkpoint, need_x, need_w, need_up, need_dn)
         plan = moe_align_block_size(topk_ids, E, B)
         at = _plan_at(plan)
 
@@ -515,7 +515,7 @@ class RoutedExperts(torch.autograd.Function):
 
 
 @functools.lru_cache(1024)
-def check_moe_backward(T, k, E, H, I, B, checkpoint, need_x, need_up, need_dn):
+def check_moe_backward(T, k, E, H, I, B, checkpoint, need_x, need_w, need_up, need_dn):
     """Refuses in the forward what ``moe_train``'s backward could not compute: ValueError."""
     none, some = (None,) * 3, 16 if checkpoint else None      # some: not null, not read
 
@@ -526,7 +526,8 @@ def check_moe_backward(T, k, E, H, I, B, checkpoint, need_x, need_up, need_dn):
     def sums(N, K, scales, dy_div, x_div):
         _check_sizes("the weight gradient", "w4_bf16_moe_wgrad", None, None, scales, *none, None, T, k, E, N, K, B,
                      dy_div, x_div, None)
-    product(I, H, k)
+    if need_x or need_w or need_up:
+        product(I, H, k)
     _check_sizes("the SwiGLU's gradient", "w4_silu_mul_bwd", None, some, None, None, T * k, I, *none)
     if need_dn:
         sums(H, I, None, k, 1)

@@ -8,8 +8,8 @@ import int4_weight_only_amd as w4
 from int4_weight_only_amd import moe
 
 
-def moe_sizes(T=32, k=4, E=8, H=128, I=64, B=64, checkpoint=False, x=True, up=True, dn=True):
-    return moe.check_moe_backward(T, k, E, H, I, B, checkpoint, x, up, dn)
+def moe_sizes(T=32, k=4, E=8, H=128, I=64, B=64, checkpoint=False, x=True, w=True, up=True, dn=True):
+    return moe.check_moe_backward(T, k, E, H, I, B, checkpoint, x, w, up, dn)
 
 
 @pytest.mark.parametrize("checkpoint", [False, True])
@@ -87,3 +87,13 @@ def test_no_pairs_per_token_is_refused_as_an_argument():
             w4.w4_bf16_moe_gemm(x, x.view(1, 0, 64), i, i, i, T, k, 64, k)
         with pytest.raises(ValueError, match="T or k"):
             w4.w4_bf16_moe_wgrad(x, x, i, i, i, 1, T, k, 64, k, 1)
+
+
+def test_moe_train_checks_what_a_gradient_runs():
+    """Weights of 2^34 elements an expert, which the input gradient's product refuses: the down
+    weights' own gradient does not run it."""
+    big = dict(T=8, k=1, E=1, H=1 << 17, I=1 << 17)
+    moe_sizes(**big, x=False, w=False, up=False)
+    for only in ("x", "w", "up"):
+        with pytest.raises(ValueError, match="product"):
+            moe_sizes(**big, **{n: n == only for n in ("x", "w", "up", "dn")})
